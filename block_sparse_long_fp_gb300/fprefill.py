@@ -22,6 +22,8 @@ FP_MAX_BATCH = 128
 FP_SELECT_THRESHOLD, FP_SELECT_TOPK, FP_SELECT_TOPP = 0, 1, 2
 FP_SCORE_PACKED, FP_SCORE_HEAD_UNION = 0, 1
 FP_V_TOKEN_MAJOR, FP_V_DIM_MAJOR = 0, 1
+FP_WS_HEADER_BYTES = 256
+FP_TABLES_MAX_BATCH = 4096
 
 
 class FpParams(Structure):
@@ -38,6 +40,32 @@ class FpProblem(Structure):
                 ("k_cache", c_void_p), ("v_cache", c_void_p), ("page_size", c_int),
                 ("num_pages", c_int), ("block_table", c_void_p), ("max_pages_per_seq", c_int),
                 ("q_scale", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("v_layout", c_int)]
+
+
+class FpTables(Structure):
+    _fields_ = [("batch", c_int), ("page_size", c_int), ("num_pages", c_int), ("max_pages_per_seq", c_int),
+                ("num_free", c_int), ("capacity", c_int), ("seqlens", c_void_p), ("new_lens", c_void_p),
+                ("free_pages", c_void_p), ("free_head", c_void_p), ("block_table", c_void_p),
+                ("cu_seqlens_q", c_void_p), ("seqlens_k", c_void_p), ("positions", c_void_p), ("slots", c_void_p),
+                ("free_next", c_void_p)]
+
+
+class FpQCache(Structure):
+    _fields_ = [("data", c_void_p), ("num_pages", c_int), ("page_size", c_int), ("h_kv", c_int), ("d", c_int),
+                ("group", c_int)]
+
+
+class FpQCacheRows(Structure):
+    _fields_ = [("rows", c_int), ("dtype", c_int), ("k", c_void_p), ("v", c_void_p), ("stride_tok", c_longlong),
+                ("stride_head", c_longlong), ("slots", c_void_p), ("out_slots", c_void_p), ("out_rows", c_int),
+                ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class FpQCacheQuery(Structure):
+    _fields_ = [("batch", c_int), ("h_q", c_int), ("total_q", c_int), ("max_q", c_int), ("dtype", c_int),
+                ("q", c_void_p), ("q_stride_tok", c_longlong), ("q_stride_head", c_longlong), ("q_scale", c_void_p),
+                ("cu_seqlens_q", c_void_p), ("seqlens_k", c_void_p), ("block_table", c_void_p),
+                ("max_pages_per_seq", c_int), ("softmax_scale", c_float)]
 
 
 class FprefillError(RuntimeError):
@@ -58,6 +86,7 @@ def lib():
                                "run block_sparse_long_fp_gb300.build.build()")
         L = ctypes.CDLL(_LIB_PATH)
         P, PP = POINTER(FpProblem), POINTER(FpParams)
+        PT, PC, PR, PQ = POINTER(FpTables), POINTER(FpQCache), POINTER(FpQCacheRows), POINTER(FpQCacheQuery)
         sig = {
             "fp_default_params": ([], FpParams),
             "fp_num_rows": ([P, PP], c_longlong),
@@ -80,6 +109,13 @@ def lib():
             "fp_dense_attn": ([P, PP, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p], c_int),
             "fp_sparse_attn_noalloc": ([P, PP, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                         c_void_p, c_void_p], c_int),
+            "fp_page_tables": ([PT, c_void_p, c_size_t, c_void_p], c_int),
+            "fp_qcache_chunk_bytes": ([PC], c_size_t),
+            "fp_qcache_bytes": ([PC], c_size_t),
+            "fp_qcache_write": ([PC, PR, c_void_p, c_size_t, c_void_p], c_int),
+            "fp_qcache_read": ([PC, PR, c_void_p, c_size_t, c_void_p], c_int),
+            "fp_qcache_attn_scratch_bytes": ([PC, PQ], c_size_t),
+            "fp_qcache_attn": ([PC, PQ, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_size_t, c_void_p], c_int),
             "fp_reset_status": ([c_void_p, c_void_p], c_int),
             "fp_device_status": ([c_void_p, c_void_p, POINTER(c_int)], c_int),
             "fp_status_string": ([c_int], ctypes.c_char_p),
@@ -296,6 +332,261 @@ class Layer:
         row_ptr, col_idx, nnz = self.select(score)
         out, lse = self.sparse_attn(row_ptr, col_idx, k_mean, v_mean, out=out, lse=lse, want_lse=want_lse)
         return out, lse, (row_ptr, col_idx, nnz)
+
+
+def _need(t, name: str, dtypes, device, ndim: int, contiguous: bool = True):
+    """An argument check of the classes below: FprefillError (invalid argument) names the tensor."""
+    if t.dtype not in dtypes or t.dim() != ndim or t.device != device or (contiguous and not t.is_contiguous()):
+        raise FprefillError(FP_ERR_INVALID, f"{name}: {ndim}-d {'contiguous ' if contiguous else ''}tensor of "
+                            f"{' or '.join(str(d) for d in dtypes)} on {device} wanted, got {tuple(t.shape)} {t.dtype} on "
+                            f"{t.device}")
+
+
+class _OnDevice:
+    """What PageTables and QCache share: the status header, and calls on their
+    device's current stream whatever device is current."""
+
+    def __init__(self, device):
+        import torch
+        if device.type != "cuda":
+            raise FprefillError(FP_ERR_INVALID, f"a CUDA tensor is wanted, got {device}")
+        self.device = device
+        self._ws = torch.zeros(FP_WS_HEADER_BYTES // 4, dtype=torch.int32, device=device)
+        self._ws_ptr = self._ws.data_ptr()
+
+    def _call(self, what: str, *args):
+        import torch
+        f = getattr(lib(), what)
+        stream = torch.cuda.current_stream(self.device).cuda_stream
+        if torch.cuda.current_device() == self.device.index:
+            s = f(*args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                s = f(*args, stream)
+        if s != FP_OK:
+            raise FprefillError(s, what)
+
+    def device_status(self) -> int:
+        """Waits for the current stream; what its kernels found wrong in device data (FP_OK: nothing)."""
+        import torch
+        v = c_int(0)
+        with torch.cuda.device(self.device):
+            _check(lib().fp_device_status(self._ws_ptr, _stream_handle(), ctypes.byref(v)), "fp_device_status")
+        return v.value
+
+    def reset_status(self):
+        self._call("fp_reset_status", self._ws_ptr)
+
+
+class PageTables(_OnDevice):
+    """fp_page_tables: the block table, lengths and slot maps of a batch, step
+    by step, on the GPU.
+
+    block_table: int32 [batch, max_pages_per_seq], the caller's, updated in
+    place.  The results -- cu_seqlens_q, seqlens_k, positions, slots,
+    free_head, as fprefill.h describes them -- are buffers of this object that
+    each step overwrites: calls that overlap on the GPU need one object each.
+    """
+
+    def __init__(self, block_table, page_size: int, num_pages: int, capacity: int):
+        import torch
+        super().__init__(block_table.device)
+        _need(block_table, "block_table", (torch.int32,), self.device, 2)
+        if capacity < 1:
+            raise FprefillError(FP_ERR_INVALID, "capacity")
+        self.block_table, self.capacity = block_table, int(capacity)
+        batch = block_table.shape[0]
+
+        def new(n):
+            return torch.empty(n, dtype=torch.int32, device=self.device)
+        self.cu_seqlens_q, self.seqlens_k, self.free_head = new(batch + 1), new(batch), new(1)
+        self.positions, self.slots = new(self.capacity), new(self.capacity)
+        t = self._t = FpTables()
+        t.batch, t.max_pages_per_seq = batch, block_table.shape[1]
+        t.page_size, t.num_pages, t.capacity = int(page_size), int(num_pages), self.capacity
+        t.block_table, t.cu_seqlens_q = _ptr(block_table), _ptr(self.cu_seqlens_q)
+        t.seqlens_k, t.positions = _ptr(self.seqlens_k), _ptr(self.positions)
+        t.slots, t.free_next = _ptr(self.slots), _ptr(self.free_head)
+        self._int32 = (torch.int32,)
+
+    def step(self, seqlens, new_lens, free_pages, free_head=None):
+        """One step (returns this object).  seqlens, new_lens: int32 [batch];
+        free_pages: int32, used from entry free_head (int32 [1], 0 when None)
+        on.  Passing this object's own seqlens_k and free_head advances both in
+        place."""
+        t, dev, kinds = self._t, self.device, self._int32
+        _need(seqlens, "seqlens", kinds, dev, 1)
+        _need(new_lens, "new_lens", kinds, dev, 1)
+        _need(free_pages, "free_pages", kinds, dev, 1)
+        if seqlens.shape[0] != t.batch or new_lens.shape[0] != t.batch:
+            raise FprefillError(FP_ERR_INVALID, f"seqlens, new_lens: {t.batch} entries wanted")
+        if free_head is not None:
+            _need(free_head, "free_head", kinds, dev, 1)
+            if free_head.shape[0] != 1:
+                raise FprefillError(FP_ERR_INVALID, "free_head: one entry wanted")
+        t = FpTables(t.batch, t.page_size, t.num_pages, t.max_pages_per_seq, free_pages.shape[0], t.capacity,
+                     seqlens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), t.block_table,
+                     t.cu_seqlens_q, t.seqlens_k, t.positions, t.slots, t.free_next)
+        self._call("fp_page_tables", t, self._ws_ptr, FP_WS_HEADER_BYTES)
+        return self
+
+
+class QCache(_OnDevice):
+    """A paged K/V cache held in 4 bits: fp_qcache_write, fp_qcache_read and
+    fp_qcache_attn on it.
+
+    data: uint8 [num_pages, h_kv, page_size / 16, chunk_bytes] in the layout
+    that fprefill.h documents (QCache.empty makes one).  e4m3 tensors are uint8
+    codes or torch.float8_e4m3fn.
+    """
+
+    def __init__(self, data, page_size: int, group: int = 32):
+        import torch
+        super().__init__(data.device)
+        _need(data, "data", (torch.uint8,), self.device, 4)
+        c = self._c = FpQCache()
+        c.data, c.num_pages, c.h_kv, c.d = _ptr(data), data.shape[0], data.shape[1], 128
+        c.page_size, c.group = int(page_size), int(group)
+        if not int(lib().fp_qcache_bytes(c)):
+            raise FprefillError(FP_ERR_UNSUPPORTED, f"a 4-bit cache with pages of {page_size}, groups of {group}")
+        if data.numel() != int(lib().fp_qcache_bytes(c)) or data.shape[2] * 16 != c.page_size:
+            raise FprefillError(FP_ERR_INVALID, f"data: [pages, heads, {c.page_size // 16}, {self.chunk_bytes(group)}] "
+                                f"wanted, got {tuple(data.shape)}")
+        self.data, self.h_kv, self.page_size, self.group = data, c.h_kv, c.page_size, c.group
+        self._scratch = {}
+        self._bf16, self._fp8 = (torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn)
+        self._int32, self._fp32 = (torch.int32,), (torch.float32,)
+
+    @staticmethod
+    def chunk_bytes(group: int = 32) -> int:
+        return 2048 + 128 * (128 // group)
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, h_kv: int, group: int = 32, device="cuda"):
+        """An uninitialised cache."""
+        import torch
+        if group not in (32, 64, 128):
+            raise FprefillError(FP_ERR_UNSUPPORTED, f"groups of {group}")
+        return cls(torch.empty((num_pages, h_kv, page_size // 16, cls.chunk_bytes(group)), dtype=torch.uint8,
+                               device=device), page_size, group)
+
+    def _rows(self, k, v, slots, k_scale, v_scale, out_slots=None):
+        dev, h = self.device, self.h_kv
+        fp8 = k_scale is not None or v_scale is not None
+        kinds = self._fp8 if fp8 else self._bf16
+        _need(k, "k", kinds, dev, 3, False)
+        _need(v, "v", kinds, dev, 3, False)
+        _need(slots, "slots", self._int32, dev, 1)
+        if k.shape != v.shape or k.stride() != v.stride() or k.shape[1:] != (h, 128) or k.stride(2) != 1:
+            raise FprefillError(FP_ERR_INVALID, f"k, v: [rows, {h}, 128] with like strides and contiguous dims wanted, "
+                                f"got {tuple(k.shape)} {k.stride()} and {tuple(v.shape)} {v.stride()}")
+        if fp8:
+            for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if x is None:
+                    raise FprefillError(FP_ERR_INVALID, f"{name} is missing")
+                _need(x, name, self._fp32, dev, 1)
+                if x.shape[0] != h:
+                    raise FprefillError(FP_ERR_INVALID, f"{name}: {h} entries wanted")
+        rows, n = k.shape[0], slots.shape[0]
+        if out_slots is not None:
+            _need(out_slots, "out_slots", self._int32, dev, 1)
+        if (out_slots.shape[0] if out_slots is not None else rows) != n:
+            raise FprefillError(FP_ERR_INVALID, "slots: one for each row (and each of out_slots) wanted")
+        # a single row (or head) may carry any stride: the packed one stands for it
+        stride_head = k.stride(1) if h > 1 else 128
+        stride_tok = k.stride(0) if rows > 1 else h * stride_head
+        return FpQCacheRows(n, FP_E4M3 if fp8 else FP_BF16, k.data_ptr(), v.data_ptr(), stride_tok, stride_head,
+                            slots.data_ptr(), _ptr(out_slots), rows, _ptr(k_scale), _ptr(v_scale))
+
+    def write(self, k, v, slots, k_scale=None, v_scale=None):
+        """Quantise rows of k and v (bf16 [rows, h_kv, 128], or e4m3 with one
+        scale per head) into `slots` (int32 [rows]; -1: none)."""
+        self._call("fp_qcache_write", self._c, self._rows(k, v, slots, k_scale, v_scale), self._ws_ptr, FP_WS_HEADER_BYTES)
+
+    def read(self, slots, k_out=None, v_out=None, out_slots=None, k_scale=None, v_scale=None):
+        """Bring the tokens at `slots` back into k_out and v_out (bf16 [.., h_kv,
+        128], or e4m3 with one scale per head): row i, or row out_slots[i].
+        Without k_out and v_out, new bf16 rows, zero where a slot is -1.  A
+        paged cache is passed as its rows: k_cache.flatten(0, 1)."""
+        import torch
+        if (k_out is None) != (v_out is None):
+            raise FprefillError(FP_ERR_INVALID, "k_out and v_out come together")
+        if k_out is None:
+            if out_slots is not None or k_scale is not None:
+                raise FprefillError(FP_ERR_INVALID, "out_slots and e4m3 want k_out and v_out")
+            k_out, v_out = (torch.zeros((slots.shape[0], self.h_kv, 128), dtype=torch.bfloat16, device=self.device)
+                            for _ in range(2))
+        self._call("fp_qcache_read", self._c, self._rows(k_out, v_out, slots, k_scale, v_scale, out_slots), self._ws_ptr, FP_WS_HEADER_BYTES)
+        return k_out, v_out
+
+    def attn(self, q, block_table, seqlens_k, cu_seqlens_q=None, max_q=None, out=None, lse=None, want_lse=True,
+             q_scale=None, softmax_scale: float = 0.0):
+        """Attention of q (bf16 [total_q, h_q, 128], or e4m3 with q_scale [h_q])
+        over the cached tokens: (out bf16 [total_q, h_q, 128], lse fp32 [h_q,
+        total_q] or None).
+
+        block_table int32 [batch, max_pages], seqlens_k int32 [batch] (the
+        queries' own tokens included).  Request r owns rows cu_seqlens_q[r] ..
+        cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
+        cu_seqlens_q, max_q rows each (total_q / batch by default)."""
+        import torch
+        dev = self.device
+        _need(q, "q", self._bf16 if q_scale is None else self._fp8, dev, 3, False)
+        _need(block_table, "block_table", self._int32, dev, 2)
+        _need(seqlens_k, "seqlens_k", self._int32, dev, 1)
+        total_q, h_q, d = q.shape
+        batch = seqlens_k.shape[0]
+        if d != 128 or q.stride(2) != 1 or h_q % self.h_kv:
+            raise FprefillError(FP_ERR_INVALID, f"q: [rows, a multiple of {self.h_kv}, 128] with contiguous dims wanted, "
+                                f"got {tuple(q.shape)} {q.stride()}")
+        if block_table.shape[0] != batch:
+            raise FprefillError(FP_ERR_INVALID, "block_table, seqlens_k: as many rows as lengths wanted")
+        if cu_seqlens_q is not None:
+            _need(cu_seqlens_q, "cu_seqlens_q", self._int32, dev, 1)
+            if cu_seqlens_q.shape[0] != batch + 1:
+                raise FprefillError(FP_ERR_INVALID, f"cu_seqlens_q: {batch + 1} entries wanted")
+        if q_scale is not None:
+            _need(q_scale, "q_scale", self._fp32, dev, 1)
+            if q_scale.shape[0] != h_q:
+                raise FprefillError(FP_ERR_INVALID, f"q_scale: {h_q} entries wanted")
+        if max_q is None:
+            max_q = max(1, total_q // batch if batch and cu_seqlens_q is None else total_q)
+        stride_head = q.stride(1) if h_q > 1 else 128
+        Q = FpQCacheQuery(batch, h_q, total_q, max_q, FP_BF16 if q_scale is None else FP_E4M3, q.data_ptr(),
+                          q.stride(0) if total_q > 1 else h_q * stride_head, stride_head, _ptr(q_scale),
+                          _ptr(cu_seqlens_q), seqlens_k.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                          softmax_scale)
+        if out is None:
+            out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", self._bf16, dev, 3)
+            if out.shape != q.shape:
+                raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
+        if lse is None and want_lse:
+            lse = torch.empty((h_q, total_q), dtype=torch.float32, device=dev)
+        elif lse is not None:
+            _need(lse, "lse", self._fp32, dev, 2)
+            if lse.shape != (h_q, total_q):
+                raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
+        n = int(lib().fp_qcache_attn_scratch_bytes(self._c, Q))
+        scratch = self._scratch_of(n)
+        self._call("fp_qcache_attn", self._c, Q, out.data_ptr(), _ptr(lse), scratch.data_ptr(), n, self._ws_ptr,
+                   FP_WS_HEADER_BYTES)
+        return out, lse
+
+    def _scratch_of(self, nbytes: int):
+        """Scratch of the current stream: calls on two streams share none, and a
+        captured call has its own, out of the graph's memory."""
+        import torch
+        stream = torch.cuda.current_stream(self.device)
+        with torch.cuda.device(self.device):
+            capturing = torch.cuda.is_current_stream_capturing()
+        old = None if capturing else self._scratch.get(stream.cuda_stream)
+        if old is None or old.numel() < nbytes:
+            old = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
+            if not capturing:
+                self._scratch[stream.cuda_stream] = old
+        return old
 
 
 def layer_from_case(case, device="cuda", params: FpParams | None = None, v_layout: int = 0):

@@ -329,6 +329,176 @@ fp_status fp_sparse_attn_noalloc(const fp_problem *p, const fp_params *prm, cons
 fp_status fp_dense_attn(const fp_problem *p, const fp_params *prm, void *out, float *lse_opt,
                         void *ws, size_t ws_bytes, void *stream);
 
+/* ===========================================================================
+ * Serving operators: page tables built on the GPU, a K/V cache held in 4 bits,
+ * and attention over it at any position (no counterpart in the pages: what a
+ * server runs beside the prefill above).
+ *
+ * Lengths, tables and slot maps are DEVICE arrays here, read when the kernels
+ * run, so a call captured into a CUDA graph replays on the lengths of the
+ * moment.  Each call takes a `ws` of at least FP_WS_HEADER_BYTES whose first
+ * word is the status (fp_reset_status, fp_device_status); what a kernel finds
+ * wrong in device data is recorded there as FP_ERR_DEVICE_BOUNDS, the part
+ * concerned is left out as described at each call, and nothing outside the
+ * buffers is touched.
+ *
+ * Slots: the token at position t of request r is at slot
+ *   block_table[r * max_pages_per_seq + t / page_size] * page_size + t % page_size
+ * of a cache, whatever its type; a slot of -1 stands for a padding row.
+ * page_size as above (it divides 128 or is a multiple of 128, >= 16) and
+ * num_pages * page_size <= 2^31 - 1.
+ * ========================================================================= */
+#define FP_WS_HEADER_BYTES 256
+#define FP_TABLES_MAX_BATCH 4096
+
+/* ---------------------------------------------------------------------------
+ * fp_page_tables -- block tables, lengths and slot maps of one step
+ *
+ * Request r has seqlens[r] tokens cached and brings new_lens[r] more.  With
+ *   used_r = ceil(seqlens[r] / page_size)
+ *   need_r = ceil((seqlens[r] + new_lens[r]) / page_size) - used_r
+ *   off_r  = sum_{r' < r} need_r',   head = *free_head (0 when NULL):
+ *   block_table[r][used_r + k] = free_pages[head + off_r + k],  k < need_r
+ *   cu_seqlens_q[r] = sum_{r' < r} new_lens[r'],  seqlens_k[r] = seqlens[r] + new_lens[r]
+ *   positions[cu_seqlens_q[r] + i] = seqlens[r] + i, slots[...] = that token's slot
+ *   *free_next = head + sum_r need_r
+ * positions and slots behind the last token, up to capacity, are 0 and -1.
+ * The other entries of block_table stay as they are.
+ * A request that cannot be served -- a negative length, more than
+ * max_pages_per_seq pages, a free list or a capacity that does not reach --
+ * is refused as a whole: it takes no page, seqlens_k[r] = seqlens[r], its
+ * slots are -1 and its positions 0 (its rows stay counted in cu_seqlens_q
+ * unless new_lens[r] < 0, and saturate at 2^31 - 1), and the status says so.  When free list or
+ * capacity run out at some request, the later ones that need any are refused
+ * too.  A page id outside [0, num_pages) in either list gives slots of -1 and
+ * the status.
+ * seqlens_k may be seqlens, and free_next free_head: the step then advances
+ * them in place (and runs in one thread block).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int batch;                    /* 1 .. FP_TABLES_MAX_BATCH */
+    int page_size, num_pages, max_pages_per_seq;
+    int num_free;                 /* entries of free_pages */
+    int capacity;                 /* entries of positions and slots (>= 1) */
+    /* DEVICE int32 arrays, read */
+    const int *seqlens;           /* [batch] */
+    const int *new_lens;          /* [batch] */
+    const int *free_pages;        /* [num_free] (may be NULL when num_free is 0) */
+    const int *free_head;         /* [1], or NULL for 0 */
+    /* DEVICE int32 arrays, written */
+    int *block_table;             /* [batch, max_pages_per_seq], updated in place */
+    int *cu_seqlens_q;            /* [batch + 1] */
+    int *seqlens_k;               /* [batch] */
+    int *positions;               /* [capacity], 16-byte aligned */
+    int *slots;                   /* [capacity], 16-byte aligned */
+    int *free_next;               /* [1] */
+} fp_tables;
+fp_status fp_page_tables(const fp_tables *t, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 4-bit cache
+ *
+ * For each token and kv head, K and V are cut into d / group groups of
+ * consecutive dims; a group holds an f16 step s, an f16 minimum m and 4-bit
+ * codes c, and stands for s * c + m.  data is [num_pages, h_kv, page_size / 16]
+ * chunks; a chunk holds 16 tokens of one kv head, with n = 128 / group:
+ *   bytes    0 .. 1023   K codes: token t's dim 32 q + 8 j + i (i < 8) is nibble
+ *                        i of the 4 bytes at  64 t + 16 j + 4 q
+ *   bytes 1024 .. 2047   V codes: token t's dim 32 y + 4 r + i (i < 4) is nibble
+ *                        i of the 2 bytes at  512 (t / 8) + 64 r + 16 (t % 8 / 2) + 8 (t % 2) + 2 y
+ *   then f16 [16][n]          K steps, and K minima
+ *   then f16 [4][n][2][2]     V steps, and V minima: token t, group g at
+ *                             [t % 8 / 2][g][t / 8][t % 2]
+ * (nibble 0 is the low half of the first byte), which is the order in which
+ * the attention's matrix instructions take them.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *data;                   /* DEVICE, fp_qcache_bytes() bytes, 16-byte aligned */
+    int num_pages, page_size;
+    int h_kv;
+    int d;                        /* must be 128 */
+    int group;                    /* 32, 64 or 128 */
+} fp_qcache;
+/* Bytes of a chunk (2048 + 128 * n) and of the whole cache; 0 on an argument
+ * error.  Host-only. */
+size_t fp_qcache_chunk_bytes(const fp_qcache *c);
+size_t fp_qcache_bytes(const fp_qcache *c);
+
+/* fp_qcache_write -- quantise tokens into the cache
+ *
+ *   x' = x clamped to +-65504;  m = f16(min x');  s = f16(max(0, (max x' - m) / 15))
+ *   c = min(15, max(0, rint((x' - m) * (1 / s))))   (0 where s = 0), in fp32.
+ *   A NaN in a group makes its minimum NaN, so all of the group reads as NaN.
+ *   k, v (device): row i, head h at  i * stride_tok + h * stride_head  elements
+ *     (pointers and strides multiples of 16 bytes), dtype FP_BF16, or FP_E4M3
+ *     codes times k_scale / v_scale [h_kv].
+ *   slots (device int32 [rows]): where row i goes; -1 skips the row, another
+ *     value outside the cache skips it and sets the status.  No slot may appear
+ *     twice in one call (which row's parts it then holds is not defined).
+ *   Slots that no row names stay as they are. */
+typedef struct {
+    int rows;                     /* >= 0 */
+    fp_dtype dtype;
+    void *k, *v;                  /* DEVICE; read by the write, written by the read */
+    long long stride_tok, stride_head;      /* elements, of k and v alike */
+    const int *slots;             /* [rows] slots in the 4-bit cache */
+    const int *out_slots;         /* fp_qcache_read: [rows] target rows, or NULL (row i) */
+    int out_rows;                 /* fp_qcache_read: rows of k and v */
+    const float *k_scale, *v_scale;         /* [h_kv], FP_E4M3 only */
+} fp_qcache_rows;
+fp_status fp_qcache_write(const fp_qcache *c, const fp_qcache_rows *r, void *ws, size_t ws_bytes, void *stream);
+
+/* fp_qcache_read -- bring tokens back into rows of bf16 or e4m3
+ *
+ *   k, v row out_slots[i] (row i when out_slots is NULL) = s * c + m of slot
+ *   slots[i], rounded once to bf16, or to the e4m3 nearest to
+ *   (s * c + m) / scale[head], saturated at 448.  With out_slots a slot map of
+ *   a bf16 / e4m3 paged cache, its pages are what the prefill entry points read.
+ *   Rows with a slot of -1 in either map are left as they were; another value
+ *   out of range too, with the status set. */
+fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * fp_qcache_attn -- attention over the 4-bit cache
+ *
+ * Request r owns query rows cu_seqlens_q[r] .. cu_seqlens_q[r+1]-1 (or, with
+ * cu_seqlens_q NULL, max_q rows from r * max_q); its query i, of lq_r, sits at
+ * position  p = seqlens_k[r] - lq_r + i  and attends keys 0 .. p: a decode
+ * step (lq_r = 1), a run of drafted tokens, or a chunk, from any position.
+ *   O = sum_t e^{s_t - m} v_t / sum_t e^{s_t - m},  s_t = scale q.k_t,  k_t and
+ *   v_t the values the cache stands for;  LSE = m + ln(sum_t e^{s_t - m}).
+ * A row with no key (an empty cache, or p < 0) yields O = 0 and LSE = -inf.
+ *   out (device bf16 [total_q, h_q, d], contiguous), lse_opt (device fp32
+ *   [h_q, total_q], natural log; may be NULL).
+ *   Rows behind the last request, up to total_q, are left as they were.
+ *   A page id outside [0, num_pages) reads as zeros; a length below 0 or above
+ *   max_pages_per_seq * page_size reads as an empty cache; query rows outside
+ *   [0, total_q) are left out: each sets the status.
+ *   scratch: fp_qcache_attn_scratch_bytes() bytes (partial results of requests
+ *   that several thread blocks share); it holds nothing between calls.
+ *   max_q is the callers' bound of lq_r, which picks the kernel's tile: the
+ *   result does not depend on it beyond rounding.  Long chunks (lq_r in the
+ *   hundreds) are better served by fp_qcache_read and the prefill kernels.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int batch;                    /* 1 .. FP_TABLES_MAX_BATCH */
+    int h_q;                      /* a multiple of the cache's h_kv */
+    int total_q;                  /* rows of q and out (>= 0) */
+    int max_q;                    /* >= 1 */
+    fp_dtype dtype;               /* of q */
+    const void *q;                /* DEVICE [total_q, h_q, d] at the strides below */
+    long long q_stride_tok, q_stride_head;  /* elements; rows 16-byte aligned */
+    const float *q_scale;         /* [h_q], FP_E4M3 only */
+    const int *cu_seqlens_q;      /* DEVICE [batch + 1], or NULL */
+    const int *seqlens_k;         /* DEVICE [batch] */
+    const int *block_table;       /* DEVICE [batch, max_pages_per_seq] */
+    int max_pages_per_seq;
+    float softmax_scale;          /* <= 0 selects 1/sqrt(d) */
+} fp_qcache_query;
+size_t fp_qcache_attn_scratch_bytes(const fp_qcache *c, const fp_qcache_query *q);
+fp_status fp_qcache_attn(const fp_qcache *c, const fp_qcache_query *q, void *out, float *lse_opt, void *scratch,
+                         size_t scratch_bytes, void *ws, size_t ws_bytes, void *stream);
+
 /* Zero the status header of a workspace (enqueued on stream). */
 fp_status fp_reset_status(void *ws, void *stream);
 

@@ -1,0 +1,532 @@
+"""The serving operators on the GPU against their float64 oracle: page tables,
+the 4-bit cache's write and read, attention over it, and a run of them
+together with the prefill kernels."""
+import numpy as np
+import pytest
+
+from oracle import qcache as oq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from block_sparse_long_fp_gb300 import build, fprefill
+    build.build()
+    return fprefill
+
+
+def i32(x):
+    import torch
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+# -- page tables ----------------------------------------------------------------
+
+def tables_case(seed, batch, old_max, new_max, page, spare=3, pad=5, head=2):
+    rng = np.random.default_rng(seed)
+    old = rng.integers(0, old_max + 1, batch)
+    new = rng.integers(0, new_max + 1, batch)
+    used, total = -(-old // page), -(-(old + new) // page)
+    pool = int(total.sum()) + spare + head
+    order = rng.permutation(pool)
+    table = np.full((batch, max(1, int(total.max())) + 1), -7, np.int64)
+    at = 0
+    for r in range(batch):
+        table[r, :used[r]] = order[at:at + used[r]]
+        at += used[r]
+    free = np.concatenate([order[:head], order[at:]])
+    return table, old, new, free, pool, max(1, int(new.sum()) + pad)
+
+
+def check_tables(fp, table, old, new, free, head, page, pool, capacity, in_place=False):
+    import torch
+    want = oq.page_tables(table, old, new, free, head, page, pool, capacity)
+    bt = i32(table)
+    p = fp.PageTables(bt, page, pool, capacity)
+    lens, heads = i32(old), i32([head])
+    if in_place:
+        p.seqlens_k.copy_(lens)
+        p.free_head.copy_(heads)
+        lens, heads = p.seqlens_k, p.free_head
+    p.step(lens, i32(new), i32(free), heads)
+    for name, got, ref in zip(("table", "cu", "seqlens_k", "positions", "slots", "free_head"),
+                              (bt, p.cu_seqlens_q, p.seqlens_k, p.positions, p.slots, p.free_head), want):
+        assert np.array_equal(got.cpu().numpy().reshape(np.shape(ref)), ref), name
+    assert (p.device_status() != 0) == bool(want[6])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("batch,old_max,new_max,page", [
+    (1, 0, 1, 16), (1, 0, 5000, 16), (5, 300, 0, 64), (64, 3000, 1, 64), (7, 100, 900, 256), (300, 50, 40, 32),
+    (1500, 20, 9, 16), (4096, 6, 3, 128), (3, 70000, 40000, 128)])
+def test_page_tables(fp, batch, old_max, new_max, page, in_place):
+    table, old, new, free, pool, cap = tables_case(batch + page, batch, old_max, new_max, page)
+    check_tables(fp, table, old, new, free, 2, page, pool, cap, in_place)
+
+
+def test_page_tables_refuse_what_they_cannot_serve(fp):
+    table, old, new, free, pool, cap = tables_case(11, 9, 200, 100, 16)
+    check_tables(fp, table, old, new, free[:len(free) // 2], 2, 16, pool, cap)      # the free list runs out
+    check_tables(fp, table, old, new, free[:0], 0, 16, pool, cap)
+    check_tables(fp, table, old, new, free, len(free) + 4, 16, pool, cap)
+    check_tables(fp, table, old, new, free, -1, 16, pool, cap)
+    check_tables(fp, table, old, new, free, 2, 16, pool, max(1, cap // 2))          # the slot map runs out
+    check_tables(fp, table[:, :8], old, new, free, 2, 16, pool, cap)                # the table is too narrow
+    for at, value in ((0, -5), (4, -1)):
+        bad = old.copy()
+        bad[at] = value
+        check_tables(fp, table, bad, new, free, 2, 16, pool, cap)
+        bad = new.copy()
+        bad[at] = value
+        check_tables(fp, table, old, bad, free, 2, 16, pool, cap)
+    bad = free.copy()
+    bad[5] = pool
+    check_tables(fp, table, old, new, bad, 2, 16, pool, cap)                        # page ids out of range
+    big = new.copy()
+    big[2] = 2 ** 31 - 1
+    check_tables(fp, table, old, big, free, 2, 16, pool, cap)
+
+
+# -- write and read ---------------------------------------------------------------
+
+def source(seed, rows, h, dtype, scale=1.0):
+    """(tensor for the library, fp32 values it stands for, head scales or None)."""
+    import torch
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.normal(size=(rows, h, 128)).astype(np.float32) * scale + rng.normal(size=(h, 128)))
+    if dtype == "bf16":
+        x = x.to(torch.bfloat16)
+        return x.cuda(), x.float().numpy(), None
+    s = torch.from_numpy((0.01 + 0.01 * rng.random(h)).astype(np.float32))
+    c = (x / s.view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return c.view(torch.uint8).cuda(), (c.float() * s.view(-1, 1)).numpy(), s.cuda()
+
+
+def some_slots(seed, rows, slots, skip=0):
+    rng = np.random.default_rng(seed)
+    s = rng.permutation(slots)[:rows]
+    if skip:
+        s[rng.permutation(rows)[:skip]] = -1
+    return s
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,h,page", [(1, 1, 16), (3, 5, 32), (61, 2, 64), (40, 3, 256)])
+def test_write_is_the_definition_bit_for_bit(fp, rows, h, page, group, dtype):
+    import torch
+    pages = -(-(rows + 20) // page) + 1
+    data = np.random.default_rng(7).integers(0, 256, (pages, h, page // 16, oq.chunk_bytes(group)), dtype=np.uint8)
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    k, k32, ks = source(1, rows, h, dtype)
+    v, v32, vs = source(2, rows, h, dtype, 0.3)
+    slots = some_slots(3, rows, pages * page, skip=rows // 4)
+    c.write(k, v, i32(slots), ks, vs)
+    oq.write(data, page, group, slots, k32, v32)
+    assert np.array_equal(c.data.cpu().numpy(), data)
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_write_of_whole_chunks_from_strided_rows(fp, group):
+    """A prompt's consecutive slots (whole chunks, a ragged start and end), its
+    keys and values inside wider rows."""
+    import torch
+    h, page, rows = 3, 64, 203
+    data = np.zeros((6, h, 4, oq.chunk_bytes(group)), np.uint8)
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    x, x32, _ = source(5, rows, 5 * h, "bf16")
+    pages = np.array([4, 0, 5, 2])
+    pos = np.arange(13, 13 + rows)
+    slots = pages[pos // page] * page + pos % page
+    c.write(x[:, h:2 * h], x[:, 4 * h:], i32(slots))
+    oq.write(data, page, group, slots, x32[:, h:2 * h], x32[:, 4 * h:])
+    assert np.array_equal(c.data.cpu().numpy(), data)
+    # the same rows one by one give the same cache
+    d = fp.QCache(torch.zeros_like(c.data), page, group)
+    for i in range(0, rows, 7):
+        d.write(x[i:i + 7, h:2 * h], x[i:i + 7, 4 * h:], i32(slots[i:i + 7]))
+    assert torch.equal(c.data, d.data)
+
+
+def test_write_of_special_values(fp):
+    import torch
+    x = torch.randn((4, 1, 128))
+    x[0, 0, 3], x[0, 0, 40], x[0, 0, 41] = float("nan"), float("inf"), -float("inf")
+    x[1, 0, :64] = 2.5                                      # constant groups
+    x[1, 0, 64:] = 0.0
+    x[2, 0, :32] *= 1e-8                                    # below the f16 steps
+    x[2, 0, 32:64] *= 1e30
+    x[3, 0, 5] = 3e38
+    x = x.to(torch.bfloat16)
+    c = fp.QCache(torch.zeros((1, 1, 1, oq.chunk_bytes(32)), dtype=torch.uint8, device="cuda"), 16, 32)
+    c.write(x.cuda(), x.cuda(), i32([0, 7, 15, 8]))
+    data = np.zeros((1, 1, 1, oq.chunk_bytes(32)), np.uint8)
+    oq.write(data, 16, 32, [0, 7, 15, 8], x.float().numpy(), x.float().numpy())
+    for got, want in zip(oq.read(c.data.cpu().numpy(), 16, 32, [0, 7, 15, 8]), oq.read(data, 16, 32, [0, 7, 15, 8])):
+        assert np.array_equal(got, want, equal_nan=True)
+    k, v = c.read(i32([0, 7, 15, 8]))
+    assert torch.isnan(k[0, 0, :32]).all() and torch.isfinite(k[0, 0, 32:].float()).all()
+    assert c.device_status() == 0
+
+
+def test_bad_slots_are_skipped_and_reported(fp):
+    import torch
+    c = fp.QCache(torch.zeros((2, 1, 1, oq.chunk_bytes(64)), dtype=torch.uint8, device="cuda"), 16, 64)
+    x, x32, _ = source(1, 4, 1, "bf16")
+    c.write(x, x, i32([3, 32, -2, 9]))
+    data = np.zeros((2, 1, 1, oq.chunk_bytes(64)), np.uint8)
+    oq.write(data, 16, 64, [3, -1, -1, 9], x32, x32)
+    assert np.array_equal(c.data.cpu().numpy(), data)
+    assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    c.reset_status()
+    assert c.device_status() == 0
+    k, v = torch.full((3, 1, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.zeros((3, 1, 128), dtype=torch.bfloat16,
+                                                                                      device="cuda")
+    c.read(i32([3, 99, 9]), k, v, out_slots=i32([2, 1, 3]))
+    assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    assert (k[:2] == 5).all() and torch.equal(k[2].cpu().float(),
+                                              torch.from_numpy(oq.read(data, 16, 64, [3])[0][0]).float().bfloat16().float())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,h,page,mapped", [(1, 1, 16, False), (77, 3, 64, True), (50, 8, 128, False)])
+def test_read_rounds_once(fp, rows, h, page, mapped, group, dtype):
+    """s * c + m is exact in float64 and rounds once to fp32 in the kernel, then
+    to bf16 (or, over the head's scale, to e4m3): bit for bit."""
+    import torch
+    rng = np.random.default_rng(rows + group)
+    pages = 3
+    data = np.zeros((pages, h, page // 16, oq.chunk_bytes(group)), np.uint8)
+    n = min(rows, pages * page)
+    slots = some_slots(9, n, pages * page)
+    x, v = rng.normal(size=(2, n, h, 128)).astype(np.float32)
+    oq.write(data, page, group, slots, x + 1, v)
+    slots[rng.permutation(n)[:n // 5]] = -1
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    to = some_slots(4, n, n + 9) if mapped else np.arange(n)
+    shape = (n + 9 if mapped else n, h, 128)
+    ks = vs = None
+    if dtype == "bf16":
+        out = [torch.full(shape, 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    else:
+        ks, vs = (torch.from_numpy((0.005 + 0.02 * rng.random(h)).astype(np.float32)).cuda() for _ in range(2))
+        out = [torch.full(shape, 77, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want = [o.cpu().clone() for o in out]
+    c.read(i32(slots), *out, out_slots=i32(to) if mapped else None, k_scale=ks, v_scale=vs)
+    for w, val, s in zip(want, oq.read(data, page, group, slots), (ks, vs)):
+        y = torch.from_numpy(val).float()
+        y = y.bfloat16() if s is None else (y / s.cpu().view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        live = slots >= 0
+        w[torch.from_numpy(to[live])] = y[torch.from_numpy(live)]
+    for o, w in zip(out, want):
+        assert torch.equal(o.cpu(), w)
+    assert c.device_status() == 0
+
+
+# -- attention ------------------------------------------------------------------------
+
+def attn_case(seed, lens, lq, h_q, h, page, group, dtype="bf16", extra_pages=2, v_scale=1.0, q_scale=1.0, poison=True):
+    """A cache with random contents (NaN steps and minima behind the last tokens), queries and tables."""
+    import torch
+    rng = np.random.default_rng(seed)
+    count = [-(-max(0, n) // page) for n in lens]
+    pages = sum(count) + extra_pages
+    order = rng.permutation(pages)
+    table = np.full((len(lens), max(1, max(count))), 10 ** 6, np.int64)
+    data = np.zeros((pages, h, page // 16, oq.chunk_bytes(group)), np.uint8)
+    n = 128 // group
+    # random codes, steps and minima through the byte layout of a chunk
+    data[..., :2048] = rng.integers(0, 256, data[..., :2048].shape, dtype=np.uint8)
+    half = data[..., 2048:].view(np.float16)                     # [..., 4 * 16 * n]
+    step = (0.05 + 0.25 * rng.random(half.shape)).astype(np.float16)
+    step[..., 32 * n:48 * n] *= np.float16(v_scale)
+    half[...] = step
+    m = (rng.normal(size=half.shape) * 0.3 - 1.5).astype(np.float16)
+    half[..., 16 * n:32 * n] = m[..., 16 * n:32 * n]
+    half[..., 48 * n:] = (m[..., 48 * n:] * np.float16(v_scale)).astype(np.float16)
+    at = 0
+    for r, c in enumerate(count):
+        table[r, :c] = order[at:at + c]
+        at += c
+    if poison:
+        for r, length in enumerate(lens):
+            for t in range(max(0, length), count[r] * page):
+                _, _, *places = oq._places(t % 16, group)
+                chunk = data[table[r, t // page], :, t % page // 16]
+                for p in places:
+                    for b in p:
+                        chunk[:, b:b + 2] = [0, 0x7e]
+    total = int(sum(lq))
+    q = torch.from_numpy(rng.normal(size=(total, h_q, 128)).astype(np.float32) * q_scale)
+    if dtype == "bf16":
+        q = q.to(torch.bfloat16)
+        return data, table, q.cuda(), q.float().numpy(), None
+    s = torch.from_numpy((0.01 + 0.01 * rng.random(h_q)).astype(np.float32)) * q_scale
+    c = (q / s.view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    return data, table, c.view(torch.uint8).cuda(), (c.float() * s.view(-1, 1)).numpy(), s.cuda()
+
+
+UNIT_BOUNDS = (0.8, 6.0, 0.8, 6.0)       # steps and minima of groups drawn from N(0, 1)
+
+
+def tolerances(q32, data, group, ref_o, ref_lse, scale, bounds=None):
+    """Output: bf16 rounding of the result (2^-8 of it); two f16 roundings of each
+    weight times step (2^-10 of at most 15 steps) and one of each weight times
+    minimum (2^-11), both in sums that the weights' total divides; a logit error
+    d moves every weight by at most 2 d.  Logits: fp32 sums whose terms' magnitudes
+    add up to at most B = scale * sum |q| (15 s + |m|), with fewer than 32 roundings
+    of 2^-23 each (2^-18 B), and the exponential's 2^-21."""
+    n = 128 // group
+    if bounds is None:
+        half = np.ascontiguousarray(data[..., 2048:]).view(np.float16).astype(np.float64)
+        bounds = (np.nan_to_num(np.abs(half[..., i * 16 * n:(i + 1) * 16 * n])).max() for i in range(4))
+    ks, km, vs, vm = bounds
+    d = 2.0 ** -18 * scale * np.abs(q32).sum(-1).max() * (15 * ks + km) + 2.0 ** -20
+    tol_o = 2.0 ** -8 * np.abs(ref_o) + 2.0 ** -10 * 15 * vs + 2.0 ** -11 * vm + 2 * d * (15 * vs + vm)
+    return tol_o, d + 2.0 ** -22 * np.abs(np.nan_to_num(ref_lse, neginf=0.0))
+
+
+def check_attn(fp, case, lens, lq, page, group, ragged, scale=None, max_q=None):
+    import torch
+    data, table, q, q32, qs = case
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    cu = i32(np.concatenate([[0], np.cumsum(lq)])) if ragged else None
+    out, lse = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=max_q if max_q else max(1, max(lq)), q_scale=qs,
+                      softmax_scale=scale or 0.0)
+    ref_o, ref_lse = oq.attention(q32, data, page, group, table, lens, lq, scale)
+    tol_o, tol_lse = tolerances(q32, data, group, ref_o, ref_lse, scale or 128 ** -0.5)
+    got, got_lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    assert c.device_status() == 0
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - ref_o) <= tol_o), float((np.abs(got - ref_o) / tol_o).max())
+    empty = np.isneginf(ref_lse)
+    assert np.array_equal(empty, np.isneginf(got_lse))
+    assert np.all(np.abs(got_lse[~empty] - ref_lse[~empty]) <= tol_lse[~empty])
+    assert np.all(got.transpose(1, 0, 2)[empty] == 0)
+    return out, lse
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,h_q,h,page", [
+    ([1], 1, 1, 16), ([2, 0, 15, 16, 17], 4, 1, 16), ([700], 16, 2, 64), ([33, 129, 1, 0, 64, 300], 6, 2, 32),
+    ([257, 256, 255], 15, 3, 256), ([1000, 31], 40, 2, 128)])
+def test_decode(fp, lens, h_q, h, page, group, dtype):
+    lq = [1] * len(lens)
+    check_attn(fp, attn_case(len(lens) + h_q, lens, lq, h_q, h, page, group, dtype), lens, lq, page, group, False)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("lens,lq,h_q,h,page", [
+    ([5, 100, 64], [5, 3, 8], 8, 2, 16),              # a prompt from its first token, and drafts
+    ([300, 0, 17, 90], [4, 0, 1, 7], 12, 1, 64),      # a request without rows
+    ([40, 200], [33, 20], 5, 1, 32),                  # odd chunks
+    ([3, 2, 130], [5, 2, 4], 4, 2, 16),               # more queries than tokens: rows without keys
+    ([0, 50], [6, 1], 16, 1, 16)])                    # an empty cache with rows
+def test_ragged_queries(fp, lens, lq, h_q, h, page, group):
+    case = attn_case(sum(lq), lens, lq, h_q, h, page, group)
+    a = check_attn(fp, case, lens, lq, page, group, True)
+    b = check_attn(fp, case, lens, lq, page, group, True, max_q=1)       # a bound that is too small picks another tile
+    assert (a[0].float() - b[0].float()).abs().max() <= 2 ** -6
+
+
+@pytest.mark.parametrize("lq", [2, 3, 5, 8])
+def test_uniform_runs_of_queries(fp, lq):
+    lens = [70, 400, lq]
+    case = attn_case(lq, lens, [lq] * 3, 16, 2, 64, 64)
+    check_attn(fp, case, lens, [lq] * 3, 64, 64, False)
+
+
+@pytest.mark.parametrize("batch,length", [(1, 20000), (3, 5000), (150, 40)])
+def test_long_axis_and_many_requests(fp, batch, length):
+    rng = np.random.default_rng(batch)
+    lens = [length] + list(rng.integers(0, length, batch - 1))
+    check_attn(fp, attn_case(batch, lens, [1] * batch, 4, 2, 64, 32), lens, [1] * batch, 64, 32, False)
+
+
+@pytest.mark.parametrize("q_scale,v_scale", [(30.0, 1.0), (1e-20, 1.0), (1.0, 1e-3), (1.0, 900.0), (2e4, 0.01)])
+def test_far_from_unit_scale(fp, q_scale, v_scale):
+    """Sharp rows, flat rows, small and large values."""
+    lens, lq = [333, 64, 1], [1, 1, 1]
+    case = attn_case(5, lens, lq, 8, 2, 64, 32, q_scale=q_scale, v_scale=v_scale)
+    check_attn(fp, case, lens, lq, 64, 32, False, scale=0.05)
+
+
+def test_rising_logits(fp):
+    """The running maximum rises at every chunk of a long row."""
+    import torch
+    L, page = 600, 64
+    data, table, q, q32, _ = attn_case(8, [L], [1], 4, 1, page, 32, poison=False)
+    unit = q32[0, 0] / np.linalg.norm(q32[0, 0])
+    k = np.outer(np.arange(L) / 12.0, unit).astype(np.float32)[:, None]
+    t = np.arange(L)
+    slots = table[0, t // page] * page + t % page
+    oq.write(data, page, 32, slots, k, np.random.default_rng(1).normal(size=(L, 1, 128)).astype(np.float32))
+    check_attn(fp, (data, table, q, q32, None), [L], [1], page, 32, False)
+
+
+def test_q_strides_and_rows_behind_the_last_request(fp):
+    import torch
+    lens, lq = [90, 200, 7], [2, 1, 3]
+    data, table, q, q32, _ = attn_case(3, lens, lq, 8, 2, 16, 64)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 16, 64)
+    wide = torch.full((9, 14, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    wide[:6, 3:11] = q
+    out = torch.full((9, 8, 128), 4.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, 9), 4.0, device="cuda")
+    cu = i32([0, 2, 3, 6])
+    c.attn(wide[:, 3:11], i32(table), i32(lens), cu_seqlens_q=cu, max_q=3, out=out, lse=lse)
+    a, b = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=3)
+    assert torch.equal(out[:6], a) and torch.equal(lse[:, :6], b)
+    assert (out[6:] == 4).all() and (lse[:, 6:] == 4).all()
+    out2, none = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=3, want_lse=False)
+    assert none is None and torch.equal(out2, a)
+
+
+def test_bad_device_data_is_reported(fp):
+    """Page ids out of range read as zeros, lengths out of range as an empty
+    cache, rows outside q are left out."""
+    import torch
+    lens, lq = [90, 200, 40], [1, 1, 1]
+    data, table, q, q32, _ = attn_case(4, lens, lq, 8, 2, 16, 32)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 16, 32)
+    good, good_lse = c.attn(q, i32(table), i32(lens))
+    assert c.device_status() == 0
+    for value in (-1, data.shape[0], 2 ** 31 - 1):
+        bad = table.copy()
+        bad[1, 3] = value
+        out, lse = c.attn(q, i32(bad), i32(lens))
+        assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+        c.reset_status()
+        ref_o, ref_lse = oq.attention(q32, data, 16, 32, bad, lens, lq)
+        tol_o, tol_lse = tolerances(q32, data, 32, ref_o, ref_lse, 128 ** -0.5)
+        assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    for value in (-3, table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        out, lse = c.attn(q, i32(table), i32([90, value, 40]))
+        assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+        c.reset_status()
+        assert (out[1] == 0).all() and torch.isneginf(lse[:, 1]).all()
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    out = torch.full((2, 8, 128), 4.0, dtype=torch.bfloat16, device="cuda")
+    c.attn(q[:2], i32(table), i32(lens), cu_seqlens_q=i32([0, 1, 2, 3]), max_q=1, out=out)
+    assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    assert torch.equal(out, good[:2])
+
+
+def test_repeated_calls_are_bit_identical(fp):
+    lens = [3000, 1, 517, 2048]
+    data, table, q, q32, _ = attn_case(6, lens, [1] * 4, 32, 4, 64, 32)
+    import torch
+    c = fp.QCache(torch.from_numpy(data).cuda(), 64, 32)
+    first, l1 = c.attn(q, i32(table), i32(lens))
+    for _ in range(5):
+        again, l2 = c.attn(q, i32(table), i32(lens))
+        assert torch.equal(first, again) and torch.equal(l1, l2)
+
+
+# -- together -----------------------------------------------------------------------------
+
+def test_prefill_then_decode(fp):
+    """Two requests: tables, the prompt into the 4-bit cache, back into bf16 pages
+    for the prefill kernels, then decode steps that advance in place -- eagerly
+    and as one captured graph -- against the oracle over the same cache."""
+    import torch
+    h_q, h, page, group, batch, width, pool = 8, 2, 64, 32, 2, 8, 40
+    rng = np.random.default_rng(12)
+    free = i32(rng.permutation(pool))
+    table = i32(np.zeros((batch, width)))
+    c = fp.QCache.empty(pool, page, h, group)
+    c.data.random_(0, 256)
+    prompt = [256, 130]
+    total = sum(prompt)
+    step = fp.PageTables(table, page, pool, total)
+    step.step(i32([0, 0]), i32(prompt), free)
+    k, v, q = (torch.from_numpy(rng.normal(size=(total, n, 128)).astype(np.float32)).to(torch.bfloat16).cuda() for n in
+               (h, h, h_q))
+    c.write(k, v, step.slots)
+    # back into the bf16 pages (the same table), and the dense prefill over them
+    kc, vc = (torch.zeros((pool, page, h, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c.read(step.slots, kc.flatten(0, 1), vc.flatten(0, 1), out_slots=step.slots)
+    layer = fp.Layer(q, kc, vc, table, [0, prompt[0], total], prompt, [0, 0], h_q, h)
+    dense, dense_lse = layer.dense_attn()
+    att, att_lse = c.attn(q, table, step.seqlens_k, cu_seqlens_q=step.cu_seqlens_q, max_q=max(prompt))
+    assert c.device_status() == 0 and step.device_status() == 0 and layer.device_status() == 0
+    # the bf16 pages round the keys by 2^-9 of themselves, the bf16 weights of the prefill by 2^-9
+    assert (dense.float() - att.float()).abs().max() <= 4e-2
+    assert (dense_lse - att_lse).abs().max() <= 2e-2
+    data = c.data.cpu().numpy()
+    ref_o, ref_lse = oq.attention(q.float().cpu().numpy(), data, page, group, table.cpu().numpy(), prompt, prompt)
+    tol_o, tol_lse = tolerances(q.float().cpu().numpy(), data, group, ref_o, ref_lse, 128 ** -0.5, UNIT_BOUNDS)
+    assert np.all(np.abs(att.float().cpu().numpy() - ref_o) <= tol_o)
+    assert np.all(np.abs(att_lse.cpu().numpy() - ref_lse) <= tol_lse)
+
+    dec = fp.PageTables(table, page, pool, batch)
+    dec.seqlens_k.copy_(step.seqlens_k)
+    dec.free_head.copy_(step.free_head)
+    ones = i32([1, 1])
+    k1, v1 = (torch.zeros((batch, h, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q1 = torch.zeros((batch, h_q, 128), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.zeros_like(q1), torch.zeros((h_q, batch), device="cuda")
+
+    def decode():
+        dec.step(dec.seqlens_k, ones, free, dec.free_head)
+        c.write(k1, v1, dec.slots)
+        c.attn(q1, table, dec.seqlens_k, out=out, lse=lse)
+
+    graph = None
+    for i in range(70):                                  # past the ends of pages
+        for x in (k1, v1, q1):
+            x.copy_(torch.from_numpy(rng.normal(size=tuple(x.shape)).astype(np.float32)))
+        if i == 3:
+            lens, head = dec.seqlens_k.clone(), dec.free_head.clone()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                decode()
+            assert torch.equal(lens, dec.seqlens_k) and torch.equal(head, dec.free_head)
+        if graph is None:
+            decode()
+        else:
+            graph.replay()
+        if i in (0, 2, 3, 40, 69):
+            lens = [n + i + 1 for n in prompt]
+            assert dec.seqlens_k.tolist() == lens
+            data = c.data.cpu().numpy()
+            q32 = q1.float().cpu().numpy()
+            ref_o, ref_lse = oq.attention(q32, data, page, group, table.cpu().numpy(), lens, [1, 1])
+            tol_o, tol_lse = tolerances(q32, data, group, ref_o, ref_lse, 128 ** -0.5, UNIT_BOUNDS)
+            assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
+            assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
+    used = sum(-(-(n + 70) // page) for n in prompt)
+    assert dec.free_head.item() == used
+    assert sorted(table[r, j].item() for r, n in enumerate(prompt) for j in range(-(-(n + 70) // page))) == \
+        sorted(free[:used].tolist())
+    assert c.device_status() == 0 and dec.device_status() == 0
+
+
+def test_two_streams_and_another_current_stream(fp):
+    """Calls of one cache on two streams at once share no scratch."""
+    import torch
+    lens = [9000, 4000]
+    data, table, q, q32, _ = attn_case(9, lens, [1, 1], 16, 2, 64, 32)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 64, 32)
+    bt, ln = i32(table), i32(lens)
+    qs = [q, q * 2]
+    want = [c.attn(x, bt, ln)[0].clone() for x in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for s, x in zip(streams, qs):
+            with torch.cuda.stream(s):
+                got.append(c.attn(x, bt, ln)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
