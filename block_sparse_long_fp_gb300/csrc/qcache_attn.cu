@@ -1,99 +1,698 @@
 // fp_qcache_attn: attention over the 4-bit cache.
 //
-// One warp per (query row, head) walks the keys with the running maximum and
-// sum of a softmax in fp32, four dims per lane.
+// Arithmetic.  A nibble c in the low ten bits of an fp16 is the subnormal
+// c 2^-24 (or c 2^-20 four bits up), exactly, and the tensor cores multiply
+// subnormals at full rate.  So the codes go into m16n8k16 products as they lie
+// in memory, one AND a pair, and steps and minima fold in around them:
+//   K: S^T[token, col] = sum_g s_g(t) (C_g Q^T)[t, col] + (M Qsum^T)[t, col]
+//      -- a product per group of dims, its fp32 result times the token's step,
+//      plus one m16n8k8 product of the minima with the queries' group sums (two
+//      fp16 terms each); dims whose nibble lies four bits up meet queries / 16.
+//   V: O^T[dim, col] = sum_t c_g(t) (p_t s_g(t)), the weights times the steps
+//      rounded to fp16 as the B operand, plus one product of the minima with
+//      the weights; rows whose nibble lies four bits up end 16 times too large.
+// A column is one (query, head) of the kv head's group, so the keys fill the
+// long side of the instruction and 8 columns suffice for a decode step: with
+// tokens on the short side half of every instruction would be padding.
+// Queries enter as fp16 under a power of two per row (exact for bf16 and e4m3
+// within 2^-29 of the row's largest), logits, weights' sums and outputs are fp32,
+// weights are fp16 (2^-11 each, as is their product with a step).
+//
+// Weights are exp2(logit - m + koff), m a maximum that only follows when the
+// logits pass it by 4 (a warp vote), koff = 11 - max(0, e), 2^e above every V
+// step so far: weight times step stays below 2^15, and what fp16 flushes is
+// below 2^-35 of the largest weight.
+//
+// Work.  The (request, kv head, column tile) items laid end to end, in chunks
+// of 16 tokens, are cut into equal ranges, one per thread block, whatever the
+// lengths (which only the GPU knows).  The warps of a block take every kWarps-th
+// chunk of an item, each through a ring of its own in shared memory (cp.async:
+// nothing to wait on but its own copies), and join their results at the item's
+// end.  An item cut by a range's end leaves partial results, which the second
+// kernel joins.
 #include "qcache.cuh"
 
 namespace fp {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kSm = 152;
+constexpr int kMinChunks = 2 * kWarps;       // fewest chunks worth a thread block
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's result in shared memory
 
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(QAttn a) {
-    const long long unit = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
-    if (unit >= (long long)a.total_q * a.h_q) return;
-    if (unit == 0 && a.cu && a.cu[a.batch] > a.total_q) set_status(a.status, FP_ERR_DEVICE_BOUNDS);
-    const int row = (int)(unit / a.h_q), head = (int)(unit % a.h_q), l = threadIdx.x & 31;
-    int r, i, lq;
+// An item that its first thread block leaves open: where, and in how many parts.
+struct Open {
+    int parts, r, kv, tile;
+};
+
+struct Scratch {
+    Open *open;                              // [blocks]
+    float2 *ml;                              // [blocks][2][cols]: exponent base and weight sum
+    float *o;                                // [blocks][2][cols][kHeadDim]
+};
+
+template <int NT>
+constexpr int blocks_per_sm() { return NT == 1 ? 4 : 3; }
+template <int NT>
+constexpr int stages() { return 4; }
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mma16(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float c[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(b0));
+}
+// Transpose of the 8 x 8 fp16 matrix whose row lane / 4 holds the lane's pair.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+struct Request {
+    int row0, lq, rows, len;      // rows: those of its lq that q has
+};
+
+__device__ __forceinline__ Request request_of(const QAttn &a, int r) {
+    Request q;
     if (a.cu) {
-        int lo = 0, hi = a.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.cu[mid] <= row) lo = mid; else hi = mid - 1;
-        }
-        r = lo;
-        i = row - a.cu[r];
-        lq = a.cu[r + 1] - a.cu[r];
+        const int x = a.cu[r], y = a.cu[r + 1];
+        q.row0 = x;
+        q.lq = x >= 0 && y > x ? y - x : 0;
+        q.rows = min(q.lq, max(0, a.total_q - x));
+        if (x < 0 || q.rows < q.lq) set_status(a.status, FP_ERR_DEVICE_BOUNDS);
     } else {
-        r = row / a.max_q;
-        i = row % a.max_q;
-        lq = a.max_q;
+        q.row0 = r * a.max_q;
+        q.lq = q.rows = a.max_q;
     }
-    if (r >= a.batch || i < 0 || i >= lq) return;
-    int len = a.seqlens_k[r];
-    if (len < 0 || len > (long long)a.max_pages * a.c.page_size) {
+    q.len = a.seqlens_k[r];
+    if (q.len < 0 || q.len > (long long)a.max_pages * a.c.page_size) {
         set_status(a.status, FP_ERR_DEVICE_BOUNDS);
-        len = 0;
+        q.len = 0;
     }
-    const int keys = min(len, len - lq + i + 1);
-    const long long at = row * a.q_stride_tok + head * a.q_stride_head + 4 * l;
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, sum = 0.f;
+    return q;
+}
+__device__ __forceinline__ int tiles_of(const QAttn &a, const Request &q, int cols) {
+    return (int)(((long long)q.rows * a.g + cols - 1) / cols);
+}
+// Chunks of an item; an empty cache counts as one, which writes its zeros.
+__device__ __forceinline__ int chunks_of(const Request &q) { return q.len > 0 ? (q.len + kChunk - 1) / kChunk : 1; }
+
+// Sum over the block, for every thread.
+__device__ __forceinline__ long long block_sum(long long v, long long *warp_sums) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (a.q_scale) {
-            __nv_fp8_e4m3 x;
-            x.__x = static_cast<const unsigned char *>(a.q)[at + e];
-            q[e] = (float)x * a.q_scale[head];
-        } else {
-            q[e] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[at + e]);
-        }
+    for (int d = 16; d; d /= 2) v += __shfl_xor_sync(~0u, v, d);
+    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x / 32] = v;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < kWarps; ++w) all += warp_sums[w];
+    __syncthreads();
+    return all;
+}
+
+// One warp's state for the columns of an item.
+template <int NT>
+struct State {
+    float o[NT][8][4];      // O^T: 8 tiles of 16 dims
+    float z[NT][4];         // the minima's part, a row per group
+    float base[NT][2];      // log2 of what weight 1 stands for (-inf: no key yet)
+    float sum[NT][2];       // this lane's share of the weights
+};
+
+template <int NG, int NT>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAttn a, Scratch sc) {
+    constexpr int kCols = 8 * NT, kBytes = 2 * kCodeBytes + 128 * NG, kStages = stages<NT>();
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ long long warp_sums[kWarps];
+    __shared__ long long s_at;
+    __shared__ int s_r;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r8 = lane >> 2, j4 = lane & 3;
+
+    // this block's range of chunks, and the request it starts in
+    long long mine = 0;
+    for (int r = tid; r < a.batch; r += kThreads) {
+        const Request q = request_of(a, r);
+        mine += (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q);
     }
-    const int groups = a.c.groups, lane_group = l * groups / 32, kv = head / a.g;
-    for (int t = 0; t < keys; ++t) {
-        const int page = a.block_table[(long long)r * a.max_pages + t / a.c.page_size];
-        float s = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (page >= 0 && page < a.c.num_pages) {
-            const unsigned char *chunk = qcache_chunk(a.c, page * a.c.page_size + t % a.c.page_size, kv);
-            const int tt = t % kChunk;
-            const uint32_t kw = *reinterpret_cast<const uint16_t *>(chunk + k_code_off(tt, l));
-            const uint32_t vw = *reinterpret_cast<const uint16_t *>(chunk + v_code_off(tt, l));
-            const __half *ks = reinterpret_cast<const __half *>(chunk + k_step_off(tt, lane_group, groups));
-            const __half *vs = reinterpret_cast<const __half *>(chunk + v_step_off(tt, lane_group, groups));
-            const float s_k = __half2float(ks[0]), m_k = __half2float(ks[16 * groups]);
-            const float s_v = __half2float(vs[0]), m_v = __half2float(vs[16 * groups]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s = fmaf(q[e], fmaf(s_k, (float)((kw >> (4 * e)) & 15u), m_k), s);
-                v[e] = fmaf(s_v, (float)((vw >> (4 * e)) & 15u), m_v);
+    const long long total = block_sum(mine, warp_sums);
+    const long long want = (total + kMinChunks - 1) / kMinChunks;
+    const int blocks = (int)(want < gridDim.x ? want : gridDim.x);
+    if (tid == 0) sc.open[blockIdx.x].parts = 0;
+    if ((int)blockIdx.x >= blocks) return;
+    const long long first = (long long)blockIdx.x * total / blocks, end = (long long)(blockIdx.x + 1) * total / blocks;
+    {
+        long long before = 0;
+        for (int base = 0; base < a.batch; base += kThreads) {
+            const int r = base + tid;
+            long long n = 0;
+            if (r < a.batch) {
+                const Request q = request_of(a, r);
+                n = (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q);
             }
-        } else if (l == 0) {
-            set_status(a.status, FP_ERR_DEVICE_BOUNDS);
+            long long x = n;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const long long y = __shfl_up_sync(~0u, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) warp_sums[warp] = x;
+            __syncthreads();
+            long long all = 0, low = before;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) low += warp_sums[w];
+                all += warp_sums[w];
+            }
+            low += x - n;
+            if (low <= first && first < low + n) {
+                s_r = r;
+                s_at = low;
+            }
+            __syncthreads();
+            before += all;
+            if (before > first) break;
         }
-#pragma unroll
-        for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-        s *= a.scale * kLog2e;
-        const float top = fmaxf(m, s), keep = exp2f(m - top), p = exp2f(s - top);
-        m = top;
-        sum = fmaf(sum, keep, p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(o[e], keep, p * v[e]);
     }
-    const float inv = keys > 0 ? 1.f / sum : 0.f;
-    __nv_bfloat16 *out = a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * l;
+    int r = s_r;
+    long long item0 = s_at;                       // first chunk of the current item
+    Request q = request_of(a, r);
+    int tiles = tiles_of(a, q, kCols), chunks = chunks_of(q);
+    int item = (int)((first - item0) / chunks);   // kv head and tile
+    item0 += (long long)item * chunks;
+
+    unsigned char *ring = smem + warp * kStages * kBytes;
+    const uint32_t ring_at = smem_addr(ring);
+    const int per_page = a.c.page_size / kChunk;
+
+    for (long long at = first; at < end;) {
+        while (item >= a.c.h_kv * tiles) {        // the next request that has rows
+            if (++r >= a.batch) return;           // lengths that changed under the kernel
+            q = request_of(a, r);
+            tiles = tiles_of(a, q, kCols);
+            chunks = chunks_of(q);
+            item = 0;
+        }
+        const int kv = item / tiles, tile = item - kv * tiles;
+        const int c0 = (int)(at - item0), c1 = (int)(end - item0 < chunks ? end - item0 : chunks);
+        const int n = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+
+        // -- copies ahead: chunk c0 + warp + i * kWarps into stage i % kStages ------
+        int issued = 0, pg = (c0 + warp) / per_page, in_page = (c0 + warp) % per_page;
+        const int *table = a.block_table + (long long)r * a.max_pages;
+        int page = n > 0 && q.len > 0 ? table[pg] : 0;
+        auto issue = [&]() {
+            if (issued < n) {
+                const bool live = q.len > 0 && page >= 0 && page < a.c.num_pages;
+                if (!live && q.len > 0 && lane == 0) set_status(a.status, FP_ERR_DEVICE_BOUNDS);
+                const unsigned char *src =
+                    a.c.data + (((long long)(live ? page : 0) * a.c.h_kv + kv) * per_page + in_page) * kBytes;
+                const uint32_t dst = ring_at + (issued % kStages) * kBytes;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
-    if (a.lse && l == 0) a.lse[(long long)head * a.total_q + row] = keys > 0 ? (m + log2f(sum)) / kLog2e : -INFINITY;
+                for (int i = 0; i < (kBytes + 511) / 512; ++i) {
+                    const int b = i * 512 + lane * 16;
+                    if (kBytes % 512 == 0 || b < kBytes) copy16(dst + b, src + b, live);
+                }
+                ++issued;
+                in_page += kWarps;
+                while (in_page >= per_page) in_page -= per_page, ++pg;
+                if (issued < n) page = table[pg];
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue();
+
+        // -- queries of this item -----------------------------------------------------
+        uint32_t qf[NT][4][2][2];                 // [quarter][half of its 16 B][b0, b1]
+        uint32_t qsum[NT];
+        float factor[NT][2];
+        int keys[NT][2], min_keys = 0x7fffffff;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int col = tile * kCols + t * 8 + r8, i = col / a.g, head = kv * a.g + col % a.g, row = q.row0 + i;
+            const bool live = i < q.rows;
+            float x[32], top = 0.f, f = a.scale * kLog2e;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = 0.f;
+            if (live) {
+                const long long at_q = row * a.q_stride_tok + head * a.q_stride_head + 8 * j4;
+                if (a.q_scale) {
+                    f *= a.q_scale[head];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint2 w =
+                            *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at_q + 32 * y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            __nv_fp8_e4m3 c;
+                            c.__x = (__nv_fp8_storage_t)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xff);
+                            x[8 * y + e] = (float)c;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint4 w =
+                            *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at_q + 32 * y);
+                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[8 * y + 2 * e] = __uint_as_float(v[e] << 16);
+                            x[8 * y + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const int ex = fp16_scale_exp(__float_as_uint(top));
+            const float up = pow2f(ex);
+            float part[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                part[y] = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float *p = x + 8 * y + 2 * u;
+                    const __half2 b0 = __floats2half2_rn(p[0] * up, p[4] * up);
+                    const __half2 b1 = __floats2half2_rn(p[1] * up * 0.0625f, p[5] * up * 0.0625f);
+                    qf[t][y][u][0] = *reinterpret_cast<const uint32_t *>(&b0);
+                    qf[t][y][u][1] = *reinterpret_cast<const uint32_t *>(&b1);
+                    const float2 f0 = __half22float2(b0), f1 = __half22float2(b1);
+                    part[y] += f0.x + f0.y + 16.f * (f1.x + f1.y);
+                }
+                part[y] += __shfl_xor_sync(~0u, part[y], 1);
+                part[y] += __shfl_xor_sync(~0u, part[y], 2);
+            }
+            // the queries' sum over group j4, times 2^-18, in two fp16 terms
+            float gs = 0.f;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) gs += y * NG / 4 == j4 ? part[y] : 0.f;
+            gs *= 0x1p-18f;
+            const float hi = __half2float(__float2half_rn(gs));
+            qsum[t] = pack_half2(hi, gs - hi);
+            f *= pow2f(24) * pow2f(-ex);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                factor[t][e] = __shfl_sync(~0u, f, (2 * j4 + e) * 4);
+                const int c = tile * kCols + t * 8 + 2 * j4 + e;
+                keys[t][e] = min(q.len, q.len - q.lq + c / a.g + 1);
+                if (c / a.g < q.rows) min_keys = min(min_keys, keys[t][e]);
+            }
+        }
+        min_keys = min(min_keys, __shfl_xor_sync(~0u, min_keys, 1));
+        min_keys = min(min_keys, __shfl_xor_sync(~0u, min_keys, 2));
+
+        State<NT> s;
+        float koff = 11.f;
+        uint32_t v_limit = 0x3c003c00u;           // 2^e of koff = 11 - max(0, e), as a pair of fp16
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s.o[t][m][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s.z[t][e] = 0.f;
+            s.base[t][0] = s.base[t][1] = -INFINITY;
+            s.sum[t][0] = s.sum[t][1] = 0.f;
+        }
+
+        for (int i = 0; i < n; ++i) {
+            copies_wait<kStages - 2>();
+            __syncwarp();
+            issue();
+            const unsigned char *chunk = ring + (i % kStages) * kBytes;
+            const int t0 = (c0 + warp + i * kWarps) * kChunk;
+
+            // logits
+            float x[NT][4];
+            {
+                const uint4 ka = *reinterpret_cast<const uint4 *>(chunk + lane * 16);
+                const uint4 kb = *reinterpret_cast<const uint4 *>(chunk + 512 + lane * 16);
+                const __half *steps = reinterpret_cast<const __half *>(chunk + 2 * kCodeBytes);
+                uint32_t m0 = 0, m1 = 0;
+                if (j4 < NG) {
+                    const uint16_t *low = reinterpret_cast<const uint16_t *>(chunk + 2 * kCodeBytes + 32 * NG);
+                    m0 = low[r8 * NG + j4] * 0x10001u;
+                    m1 = low[(r8 + 8) * NG + j4] * 0x10001u;
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma8(c, m0, m1, qsum[t]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[t][e] = c[e] * 0x1p-6f;
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    float acc[NT][4];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+#pragma unroll
+                    for (int y = g * 4 / NG; y < (g + 1) * 4 / NG; ++y) {
+                        uint32_t wa = y == 0 ? ka.x : y == 1 ? ka.y : y == 2 ? ka.z : ka.w;
+                        uint32_t wb = y == 0 ? kb.x : y == 1 ? kb.y : y == 2 ? kb.z : kb.w;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+                                mma16(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
+                                      qf[t][y][u][0], qf[t][y][u][1]);
+                            wa >>= 8;
+                            wb >>= 8;
+                        }
+                    }
+                    const float s0 = __half2float(steps[r8 * NG + g]), s1 = __half2float(steps[(r8 + 8) * NG + g]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        x[t][0] = fmaf(s0, acc[t][0], x[t][0]);
+                        x[t][1] = fmaf(s0, acc[t][1], x[t][1]);
+                        x[t][2] = fmaf(s1, acc[t][2], x[t][2]);
+                        x[t][3] = fmaf(s1, acc[t][3], x[t][3]);
+                    }
+                }
+            }
+
+            // V steps and minima: tokens 2 j4, 2 j4 + 1 and the same 8 further, of each group
+            uint32_t vs[NG][2], vm[2] = {0, 0};
+            const unsigned char *v_meta = chunk + 2 * kCodeBytes + 64 * NG + j4 * 8 * NG;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(v_meta + 8 * g);
+                vs[g][0] = w.x;
+                vs[g][1] = w.y;
+            }
+            if (r8 < NG) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(v_meta + 32 * NG + 8 * r8);
+                vm[0] = w.x;
+                vm[1] = w.y;
+            }
+            const bool masked = t0 + kChunk > min_keys;
+            if (t0 + kChunk > q.len) {            // behind the last token anything may lie
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int tok = t0 + 8 * h + 2 * j4;
+                    const uint32_t keep = (tok < q.len ? 0xffffu : 0u) | (tok + 1 < q.len ? 0xffff0000u : 0u);
+                    vm[h] &= keep;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) vs[g][h] &= keep;
+                }
+            }
+            uint32_t v_top = 0;                   // steps are >= 0, so their bits order them
+#pragma unroll
+            for (int g = 0; g < NG; ++g) v_top = __vmaxu2(v_top, __vmaxu2(vs[g][0], vs[g][1]));
+
+            // weights
+            float y[NT][4];
+            bool rise = __vmaxu2(v_top, v_limit) != v_limit;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[t][e] *= factor[t][e & 1];
+                    if (masked && t0 + r8 + 4 * (e & 2) >= keys[t][e & 1]) x[t][e] = -INFINITY;
+                    y[t][e] = x[t][e] == -INFINITY ? -INFINITY : x[t][e] - s.base[t][e & 1];
+                    rise |= y[t][e] > koff + 4.f;
+                }
+            if (__any_sync(~0u, rise)) {
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) v_top = __vmaxu2(v_top, __shfl_xor_sync(~0u, v_top, d));
+                const uint32_t step = max(v_top & 0xffffu, v_top >> 16);
+                float koff2 = koff;
+                if (step > (v_limit & 0xffffu)) { // the power of two above the step
+                    const int e = min((int)(step >> 10) - 14, 16);
+                    koff2 = 11.f - e;
+                    v_limit = e >= 16 ? 0x7bff7bffu : (uint32_t)(e + 15) * 0x04000400u;
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float top = fmaxf(x[t][c], x[t][c + 2]);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                        const float old = s.base[t][c], b = fmaxf(old + koff, top) - koff2;
+                        const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
+                        s.base[t][c] = b;
+                        s.sum[t][c] *= keep;
+                        s.z[t][c] *= keep;
+                        s.z[t][c + 2] *= keep;
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) {
+                            s.o[t][m][c] *= keep;
+                            s.o[t][m][c + 2] *= keep;
+                        }
+                        y[t][c] = x[t][c] == -INFINITY ? -INFINITY : x[t][c] - b;
+                        y[t][c + 2] = x[t][c + 2] == -INFINITY ? -INFINITY : x[t][c + 2] - b;
+                    }
+                koff = koff2;
+            }
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[t][e] = fast_exp2(y[t][e]);
+                s.sum[t][0] += y[t][0] + y[t][2];
+                s.sum[t][1] += y[t][1] + y[t][3];
+                p[t][0] = transpose8(pack_half2(y[t][0], y[t][1]));
+                p[t][1] = transpose8(pack_half2(y[t][2], y[t][3]));
+                mma16(s.z[t], vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
+            }
+
+            // values
+            const uint4 va = *reinterpret_cast<const uint4 *>(chunk + kCodeBytes + lane * 16);
+            const uint4 vb = *reinterpret_cast<const uint4 *>(chunk + kCodeBytes + 512 + lane * 16);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t ps[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    ps[t][0] = mul_half2(p[t][0], vs[g][0]);
+                    ps[t][1] = mul_half2(p[t][1], vs[g][1]);
+                }
+#pragma unroll
+                for (int m = g * 4 / NG; m < (g + 1) * 4 / NG; ++m) {
+                    const uint32_t sel = m & 1 ? 0x7632 : 0x5410;
+                    uint32_t wa = __byte_perm(m < 2 ? va.x : va.y, m < 2 ? va.z : va.w, sel);
+                    uint32_t wb = __byte_perm(m < 2 ? vb.x : vb.y, m < 2 ? vb.z : vb.w, sel);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma16(s.o[t][2 * m + u], wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu,
+                                  wb & 0x00f000f0u, ps[t][0], ps[t][1]);
+                        wa >>= 8;
+                        wb >>= 8;
+                    }
+                }
+            }
+        }
+        copies_wait<0>();
+        __syncwarp();
+
+        // -- join the warps -----------------------------------------------------------
+        float *mine_o = reinterpret_cast<float *>(ring);                       // [kCols][kOutStride]
+        float2 *ml = reinterpret_cast<float2 *>(smem + kWarps * kStages * kBytes);   // [kWarps][kCols]
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = s.sum[t][c];
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(~0u, l, d);
+                const int col = t * 8 + 2 * j4 + c;
+                if (r8 == 0) ml[warp * kCols + col] = make_float2(s.base[t][c], l);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float z = __shfl_sync(~0u, s.z[t][c], (m * NG / 4) * 4 + j4);
+                    float4 v;
+                    v.x = fmaf(s.o[t][2 * m][c], 0x1p24f, z);
+                    v.y = fmaf(s.o[t][2 * m][c + 2], 0x1p20f, z);
+                    v.z = fmaf(s.o[t][2 * m + 1][c], 0x1p24f, z);
+                    v.w = fmaf(s.o[t][2 * m + 1][c + 2], 0x1p20f, z);
+                    *reinterpret_cast<float4 *>(mine_o + col * kOutStride + 32 * m + 4 * r8) = v;
+                }
+            }
+        }
+        __syncthreads();
+        const bool opens = c0 == 0, closes = c1 == chunks;
+        for (int col = warp; col < kCols; col += kWarps) {
+            const int cc = tile * kCols + col, i = cc / a.g, head = kv * a.g + cc % a.g, row = q.row0 + i;
+            if (i >= q.rows) continue;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kCols + col].x);
+            float l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 e = ml[w * kCols + col];
+                const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem + w * kStages * kBytes) + col * kOutStride + 4 * lane);
+                l += e.x == -INFINITY ? e.y : f * e.y;       // a NaN's sum stays one
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
+            }
+            if (opens && closes) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+                __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+                *reinterpret_cast<uint2 *>(a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * lane) =
+                    make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+                if (a.lse && lane == 0)
+                    a.lse[(long long)head * a.total_q + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+            } else {
+                const long long slot = ((long long)blockIdx.x * 2 + (opens ? 1 : 0)) * kCols + col;
+                *reinterpret_cast<float4 *>(sc.o + slot * kHeadDim + 4 * lane) = o;
+                if (lane == 0) sc.ml[slot] = make_float2(top, l);
+            }
+        }
+        if (opens && !closes && tid == 0) {
+            const long long last = item0 + chunks - 1;           // and the block that has it
+            const int b = (int)(((last + 1) * blocks - 1) / total);
+            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, r, kv, tile};
+        }
+        __syncthreads();
+        at = item0 + c1;
+        item0 += chunks;
+        ++item;
+    }
+}
+
+// Joins the parts of an item that several blocks share: part 0 in its first
+// block's second slot, the others in the first slots of the blocks behind it.
+// One warp per column.
+template <int NT>
+__global__ void __launch_bounds__(256) join_kernel(QAttn a, Scratch sc) {
+    constexpr int kCols = 8 * NT;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Open it = sc.open[blockIdx.x];
+    if (it.parts == 0) return;
+    const int lane = threadIdx.x & 31;
+    const Request q = request_of(a, it.r);
+    for (int col = threadIdx.x / 32; col < kCols; col += 8) {
+        const int cc = it.tile * kCols + col, i = cc / a.g, head = it.kv * a.g + cc % a.g, row = q.row0 + i;
+        if (i >= q.rows) continue;
+        const auto slot = [&](int p) { return ((long long)(blockIdx.x + p) * 2 + (p == 0)) * kCols + col; };
+        float top = -INFINITY;
+        for (int p = lane; p < it.parts; p += 32) top = fmaxf(top, sc.ml[slot(p)].x);
+#pragma unroll
+        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int p = 0; p < it.parts; ++p) {
+            const float2 e = sc.ml[slot(p)];
+            const float4 v = *reinterpret_cast<const float4 *>(sc.o + slot(p) * kHeadDim + 4 * lane);
+            const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
+            l += e.x == -INFINITY ? e.y : f * e.y;
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * lane) =
+            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+        if (a.lse && lane == 0)
+            a.lse[(long long)head * a.total_q + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+    }
+}
+
+// 8 columns to a tile while they hold a kv head's (query, head) pairs, else 16.
+int tile_columns(const QAttn &a) { return (long long)a.max_q * a.g <= 8 ? 8 : 16; }
+
+int blocks_of(const QAttn &a) {
+    const int cols = tile_columns(a), most = kSm * (cols == 8 ? blocks_per_sm<1>() : blocks_per_sm<2>());
+    // no more than the longest lengths that the table can hold would use
+    const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
+    const long long tiles = rows * a.g / cols + a.batch;
+    const double chunks = (double)a.c.h_kv * tiles * a.max_pages * (a.c.page_size / kChunk);
+    return chunks < (double)most * kMinChunks ? (int)(chunks / kMinChunks) + 1 : most;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int NG, int NT>
+cudaError_t launch(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t st) {
+    constexpr int smem = kWarps * (stages<NT>() * (2 * kCodeBytes + 128 * NG) + 8 * NT * (int)sizeof(float2));
+    static_assert(stages<NT>() * (2 * kCodeBytes + 128 * NG) >= 8 * NT * kOutStride * 4, "a warp's result fits its ring");
+    static_assert(smem <= 47 * 1024, "no opt-in to more shared memory");
+    attn_kernel<NG, NT><<<blocks, kThreads, smem, st>>>(a, sc);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<NT>, a, sc);
+}
+
+template <int NT>
+cudaError_t launch_groups(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t st) {
+    switch (a.c.groups) {
+        case 4: return launch<4, NT>(a, sc, blocks, st);
+        case 2: return launch<2, NT>(a, sc, blocks, st);
+        default: return launch<1, NT>(a, sc, blocks, st);
+    }
 }
 
 }  // namespace
 
-size_t qcache_attn_scratch_bytes(const QAttn &) { return 16; }
+size_t qcache_attn_scratch_bytes(const QAttn &a) {
+    const size_t n = blocks_of(a), cols = tile_columns(a);
+    return align256(n * sizeof(Open)) + align256(n * 2 * cols * sizeof(float2)) + n * 2 * cols * kHeadDim * sizeof(float);
+}
 
-cudaError_t launch_qcache_attn(const QAttn &a, void *, cudaStream_t st) {
-    const long long units = (long long)a.total_q * a.h_q;
-    attn_kernel<<<(unsigned)((units + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_qcache_attn(const QAttn &a, void *scratch, cudaStream_t st) {
+    const size_t n = blocks_of(a), cols = tile_columns(a);
+    char *p = static_cast<char *>(scratch);
+    Scratch sc;
+    sc.open = reinterpret_cast<Open *>(p);
+    p += align256(n * sizeof(Open));
+    sc.ml = reinterpret_cast<float2 *>(p);
+    p += align256(n * 2 * cols * sizeof(float2));
+    sc.o = reinterpret_cast<float *>(p);
+    return cols == 8 ? launch_groups<1>(a, sc, (int)n, st) : launch_groups<2>(a, sc, (int)n, st);
 }
 
 }  // namespace fp
