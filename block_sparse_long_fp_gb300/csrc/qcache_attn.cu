@@ -19,7 +19,7 @@
 // weights are fp16 (2^-11 each, as is their product with a step).
 //
 // Weights are exp2(logit - m + koff), m a maximum that only follows when the
-// logits pass it by 4 (a warp vote), koff = 11 - max(0, e), 2^e above every V
+// logits pass it by 4 (a warp vote), koff = 11 - e, 2^e (e >= 1) above every V
 // step so far: weight times step stays below 2^15, and what fp16 flushes is
 // below 2^-35 of the largest weight.
 //
@@ -45,7 +45,7 @@ constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's re
 
 // An item that its first thread block leaves open: where, and in how many parts.
 struct Open {
-    int parts, r, kv, tile;
+    int parts, row0, rows, item, tiles;      // item: kv head * tiles + tile
 };
 
 struct Scratch {
@@ -54,10 +54,11 @@ struct Scratch {
     float *o;                                // [blocks][2][cols][kHeadDim]
 };
 
+// Blocks per SM (their registers: 128, 168 and 255 a thread) and copies ahead.
 template <int NT>
-constexpr int blocks_per_sm() { return NT == 1 ? 4 : 3; }
+constexpr int blocks_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
 template <int NT>
-constexpr int stages() { return 4; }
+constexpr int stages() { return NT == 4 ? 8 : 4; }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -87,8 +88,8 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -123,90 +124,189 @@ __device__ __forceinline__ int tiles_of(const QAttn &a, const Request &q, int co
 // Chunks of an item; an empty cache counts as one, which writes its zeros.
 __device__ __forceinline__ int chunks_of(const Request &q) { return q.len > 0 ? (q.len + kChunk - 1) / kChunk : 1; }
 
-// Sum over the block, for every thread.
-__device__ __forceinline__ long long block_sum(long long v, long long *warp_sums) {
-#pragma unroll
-    for (int d = 16; d; d /= 2) v += __shfl_xor_sync(~0u, v, d);
-    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x / 32] = v;
-    __syncthreads();
-    long long all = 0;
-    for (int w = 0; w < kWarps; ++w) all += warp_sums[w];
-    __syncthreads();
-    return all;
+// O = v / l and its log-sum-exp, top + log2(l) in base 2; zeros and -inf without a key.
+__device__ __forceinline__ void store_row(const QAttn &a, int row, int head, int lane, float4 v, float top, float l) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat162 x = __floats2bfloat162_rn(v.x * inv, v.y * inv), y = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2 *>(a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * lane) =
+        make_uint2(*reinterpret_cast<uint32_t *>(&x), *reinterpret_cast<uint32_t *>(&y));
+    if (a.lse && lane == 0) a.lse[(long long)head * a.total_q + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
-// One warp's state for the columns of an item.
-template <int NT>
-struct State {
-    float o[NT][8][4];      // O^T: 8 tiles of 16 dims
-    float z[NT][4];         // the minima's part, a row per group
-    float base[NT][2];      // log2 of what weight 1 stands for (-inf: no key yet)
-    float sum[NT][2];       // this lane's share of the weights
+// Exclusive scan over the block; *all is the sum.
+__device__ __forceinline__ long long block_scan(long long n, long long *all, long long *warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    long long x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long y = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    long long sum = 0;
+    x -= n;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const long long v = warp_sums[w];
+        if (w < warp) x += v;
+        sum += v;
+    }
+    __syncthreads();
+    *all = sum;
+    return x;
+}
+
+// The operands that one lane holds for 8 columns: queries as B fragments
+// ([quarter of the dims][half of its 16 bytes] of (b0, b1)), the query's sum over
+// group lane % 4 times 2^-18 in two fp16 terms, and what a column's fp32 products
+// times 2^24 have to be scaled by to be base-2 logits.
+struct Queries {
+    uint2 f[4][2];
+    uint32_t sum;
+    float factor;      // of column lane / 4
 };
+
+template <int NG>
+__device__ __forceinline__ void load_queries(const QAttn &a, const Request &q, int kv, int col, Queries &out) {
+    const int j4 = threadIdx.x & 3, i = col / a.g, head = kv * a.g + col % a.g;
+    float x[32], top = 0.f, f = a.scale * kLog2e;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) x[e] = 0.f;
+    if (i < q.rows) {
+        const long long at = (q.row0 + i) * a.q_stride_tok + head * a.q_stride_head + 8 * j4;
+        if (a.q_scale) {
+            f *= a.q_scale[head];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at + 32 * y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    __nv_fp8_e4m3 c;
+                    c.__x = (__nv_fp8_storage_t)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xff);
+                    x[8 * y + e] = (float)c;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at + 32 * y);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[8 * y + 2 * e] = __uint_as_float(v[e] << 16);
+                    x[8 * y + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+    const int ex = fp16_scale_exp(__float_as_uint(top));
+    const float up = pow2f(ex);
+    float gs = 0.f;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        float part = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float *p = x + 8 * y + 2 * u;
+            const __half2 b0 = __floats2half2_rn(p[0] * up, p[4] * up);
+            const __half2 b1 = __floats2half2_rn(p[1] * up * 0.0625f, p[5] * up * 0.0625f);
+            out.f[y][u] = make_uint2(*reinterpret_cast<const uint32_t *>(&b0), *reinterpret_cast<const uint32_t *>(&b1));
+            const float2 f0 = __half22float2(b0), f1 = __half22float2(b1);
+            part += f0.x + f0.y + 16.f * (f1.x + f1.y);
+        }
+        part += __shfl_xor_sync(~0u, part, 1);
+        part += __shfl_xor_sync(~0u, part, 2);
+        gs += y * NG / 4 == j4 ? part : 0.f;
+    }
+    gs *= 0x1p-18f;
+    const float hi = __half2float(__float2half_rn(gs));
+    out.sum = pack_half2(hi, gs - hi);
+    out.factor = f * pow2f(24) * pow2f(-ex);
+}
+
+// NG fp16 from shared memory, as floats.
+template <int NG>
+__device__ __forceinline__ void load_halves(const unsigned char *p, float out[NG]) {
+    if (NG == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
+        out[0] = a.x, out[1 % NG] = a.y, out[2 % NG] = b.x, out[3 % NG] = b.y;
+    } else if (NG == 2) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(p));
+        out[0] = a.x, out[1 % NG] = a.y;
+    } else {
+        out[0] = __half2float(*reinterpret_cast<const __half *>(p));
+    }
+}
 
 template <int NG, int NT>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAttn a, Scratch sc) {
     constexpr int kCols = 8 * NT, kBytes = 2 * kCodeBytes + 128 * NG, kStages = stages<NT>();
+    constexpr int kRing = kStages * kBytes;
+    constexpr bool kSharedQ = NT == 4;            // queries' fragments in shared memory instead of registers
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ long long warp_sums[kWarps];
     __shared__ long long s_at;
     __shared__ int s_r;
+    __shared__ Request s_q;
+    __shared__ float2 ml[kWarps][kCols];
+    __shared__ uint2 s_frag[kSharedQ ? NT : 1][4][2][32];
+    __shared__ uint32_t s_sum[kSharedQ ? NT : 1][32];
+    __shared__ float s_factor[kSharedQ ? kCols : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r8 = lane >> 2, j4 = lane & 3;
 
     // this block's range of chunks, and the request it starts in
-    long long mine = 0;
-    for (int r = tid; r < a.batch; r += kThreads) {
-        const Request q = request_of(a, r);
-        mine += (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q);
+    const auto units = [&](const Request &q) { return (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q); };
+    Request q = {0, 0, 0, 0};
+    if (tid < a.batch) q = request_of(a, tid);
+    long long n = units(q), total;
+    if (tid >= a.batch) n = 0;
+    long long low = block_scan(n, &total, warp_sums);
+    for (int base = kThreads; base < a.batch; base += kThreads) {
+        long long all;
+        block_scan(base + tid < a.batch ? units(request_of(a, base + tid)) : 0, &all, warp_sums);
+        total += all;
     }
-    const long long total = block_sum(mine, warp_sums);
     const long long want = (total + kMinChunks - 1) / kMinChunks;
     const int blocks = (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
     const long long first = (long long)blockIdx.x * total / blocks, end = (long long)(blockIdx.x + 1) * total / blocks;
-    {
-        long long before = 0;
-        for (int base = 0; base < a.batch; base += kThreads) {
-            const int r = base + tid;
-            long long n = 0;
-            if (r < a.batch) {
-                const Request q = request_of(a, r);
-                n = (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q);
-            }
-            long long x = n;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const long long y = __shfl_up_sync(~0u, x, d);
-                if (lane >= d) x += y;
-            }
-            if (lane == 31) warp_sums[warp] = x;
-            __syncthreads();
-            long long all = 0, low = before;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) low += warp_sums[w];
-                all += warp_sums[w];
-            }
-            low += x - n;
-            if (low <= first && first < low + n) {
-                s_r = r;
-                s_at = low;
-            }
-            __syncthreads();
+    long long before = 0;
+    for (int base = 0; base < a.batch; base += kThreads) {
+        if (base) {
+            n = 0;
+            if (base + tid < a.batch) n = units(q = request_of(a, base + tid));
+            long long all;
+            low = before + block_scan(n, &all, warp_sums);
             before += all;
-            if (before > first) break;
+        } else if (a.batch > kThreads) {
+            block_scan(n, &before, warp_sums);
         }
+        if (low <= first && first < low + n) {
+            s_r = base + tid;
+            s_at = low;
+            s_q = q;
+        }
+        if (before > first) break;
     }
+    __syncthreads();
     int r = s_r;
     long long item0 = s_at;                       // first chunk of the current item
-    Request q = request_of(a, r);
+    q = s_q;
     int tiles = tiles_of(a, q, kCols), chunks = chunks_of(q);
     int item = (int)((first - item0) / chunks);   // kv head and tile
     item0 += (long long)item * chunks;
 
-    unsigned char *ring = smem + warp * kStages * kBytes;
-    const uint32_t ring_at = smem_addr(ring);
+    unsigned char *ring = smem + warp * kRing;
+    const uint32_t ring_at = smem_addr(ring) + lane * 16;
     const int per_page = a.c.page_size / kChunk;
 
     for (long long at = first; at < end;) {
@@ -219,133 +319,99 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         }
         const int kv = item / tiles, tile = item - kv * tiles;
         const int c0 = (int)(at - item0), c1 = (int)(end - item0 < chunks ? end - item0 : chunks);
-        const int n = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
+        const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
 
-        // -- copies ahead: chunk c0 + warp + i * kWarps into stage i % kStages ------
-        int issued = 0, pg = (c0 + warp) / per_page, in_page = (c0 + warp) % per_page;
-        const int *table = a.block_table + (long long)r * a.max_pages;
-        int page = n > 0 && q.len > 0 ? table[pg] : 0;
-        auto issue = [&]() {
-            if (issued < n) {
-                const bool live = q.len > 0 && page >= 0 && page < a.c.num_pages;
-                if (!live && q.len > 0 && lane == 0) set_status(a.status, FP_ERR_DEVICE_BOUNDS);
-                const unsigned char *src =
-                    a.c.data + (((long long)(live ? page : 0) * a.c.h_kv + kv) * per_page + in_page) * kBytes;
+        // -- copies ahead: chunk c0 + warp + i * kWarps into stage i % kStages.  Lane l
+        //    looks up the addresses of chunks l, l + 32, ..., zero where there is none.
+        unsigned long long src = 0;
+        const auto look_up = [&](int i) {
+            const int c = c0 + warp + (i + lane) * kWarps;
+            src = 0;
+            if (i + lane < mine && q.len > 0) {
+                const int pg = c / per_page, page = a.block_table[(long long)r * a.max_pages + pg];
+                if (page >= 0 && page < a.c.num_pages)
+                    src = (unsigned long long)(a.c.data + (((long long)page * a.c.h_kv + kv) * per_page + c - pg * per_page) * kBytes);
+                else
+                    set_status(a.status, FP_ERR_DEVICE_BOUNDS);
+            }
+        };
+        int issued = 0;
+        const auto issue = [&]() {
+            if (issued < mine) {
+                if (issued && issued % 32 == 0) look_up(issued);
+                const unsigned long long from = __shfl_sync(~0u, src, issued & 31);
                 const uint32_t dst = ring_at + (issued % kStages) * kBytes;
+                if (from) {
+                    const char *p = reinterpret_cast<const char *>(from) + lane * 16;
 #pragma unroll
-                for (int i = 0; i < (kBytes + 511) / 512; ++i) {
-                    const int b = i * 512 + lane * 16;
-                    if (kBytes % 512 == 0 || b < kBytes) copy16(dst + b, src + b, live);
+                    for (int i = 0; i < (kBytes + 511) / 512; ++i)
+                        if ((i + 1) * 512 <= kBytes || lane * 16 < kBytes - i * 512) copy16(dst + i * 512, p + i * 512);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < (kBytes + 511) / 512; ++i)
+                        if ((i + 1) * 512 <= kBytes || lane * 16 < kBytes - i * 512)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512), "r"(0) : "memory");
                 }
                 ++issued;
-                in_page += kWarps;
-                while (in_page >= per_page) in_page -= per_page, ++pg;
-                if (issued < n) page = table[pg];
             }
             copies_commit();
         };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue();
+        look_up(0);
 
         // -- queries of this item -----------------------------------------------------
-        uint32_t qf[NT][4][2][2];                 // [quarter][half of its 16 B][b0, b1]
-        uint32_t qsum[NT];
-        float factor[NT][2];
-        int keys[NT][2], min_keys = 0x7fffffff;
+        Queries qs[kSharedQ ? 1 : NT];
+        if (kSharedQ) {
+            for (int t = warp; t < NT; t += kWarps) {
+                load_queries<NG>(a, q, kv, tile * kCols + t * 8 + r8, qs[0]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int col = tile * kCols + t * 8 + r8, i = col / a.g, head = kv * a.g + col % a.g, row = q.row0 + i;
-            const bool live = i < q.rows;
-            float x[32], top = 0.f, f = a.scale * kLog2e;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0.f;
-            if (live) {
-                const long long at_q = row * a.q_stride_tok + head * a.q_stride_head + 8 * j4;
-                if (a.q_scale) {
-                    f *= a.q_scale[head];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint2 w =
-                            *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at_q + 32 * y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            __nv_fp8_e4m3 c;
-                            c.__x = (__nv_fp8_storage_t)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xff);
-                            x[8 * y + e] = (float)c;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint4 w =
-                            *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at_q + 32 * y);
-                        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[8 * y + 2 * e] = __uint_as_float(v[e] << 16);
-                            x[8 * y + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
-                        }
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    s_frag[t][y][0][lane] = qs[0].f[y][0];
+                    s_frag[t][y][1][lane] = qs[0].f[y][1];
                 }
+                s_sum[t][lane] = qs[0].sum;
+                if (j4 == 0) s_factor[t * 8 + r8] = qs[0].factor;
             }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const int ex = fp16_scale_exp(__float_as_uint(top));
-            const float up = pow2f(ex);
-            float part[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                part[y] = 0.f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float *p = x + 8 * y + 2 * u;
-                    const __half2 b0 = __floats2half2_rn(p[0] * up, p[4] * up);
-                    const __half2 b1 = __floats2half2_rn(p[1] * up * 0.0625f, p[5] * up * 0.0625f);
-                    qf[t][y][u][0] = *reinterpret_cast<const uint32_t *>(&b0);
-                    qf[t][y][u][1] = *reinterpret_cast<const uint32_t *>(&b1);
-                    const float2 f0 = __half22float2(b0), f1 = __half22float2(b1);
-                    part[y] += f0.x + f0.y + 16.f * (f1.x + f1.y);
-                }
-                part[y] += __shfl_xor_sync(~0u, part[y], 1);
-                part[y] += __shfl_xor_sync(~0u, part[y], 2);
-            }
-            // the queries' sum over group j4, times 2^-18, in two fp16 terms
-            float gs = 0.f;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) gs += y * NG / 4 == j4 ? part[y] : 0.f;
-            gs *= 0x1p-18f;
-            const float hi = __half2float(__float2half_rn(gs));
-            qsum[t] = pack_half2(hi, gs - hi);
-            f *= pow2f(24) * pow2f(-ex);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                factor[t][e] = __shfl_sync(~0u, f, (2 * j4 + e) * 4);
-                const int c = tile * kCols + t * 8 + 2 * j4 + e;
-                keys[t][e] = min(q.len, q.len - q.lq + c / a.g + 1);
-                if (c / a.g < q.rows) min_keys = min(min_keys, keys[t][e]);
-            }
+            for (int t = 0; t < NT; ++t) load_queries<NG>(a, q, kv, tile * kCols + t * 8 + r8, qs[kSharedQ ? 0 : t]);
         }
-        min_keys = min(min_keys, __shfl_xor_sync(~0u, min_keys, 1));
-        min_keys = min(min_keys, __shfl_xor_sync(~0u, min_keys, 2));
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue();
+        if (kSharedQ) __syncthreads();
+        float factor[NT][2];
+        int min_keys = 0x7fffffff;
+        // keys that column c of this lane (of 8 t + 2 j4 + e) may see
+        const auto keys_of = [&](int t, int e) {
+            const int i = (tile * kCols + t * 8 + 2 * j4 + e) / a.g;
+            return min(q.len, q.len - q.lq + i + 1);
+        };
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                factor[t][e] = kSharedQ ? s_factor[t * 8 + 2 * j4 + e]
+                                        : __shfl_sync(~0u, qs[kSharedQ ? 0 : t].factor, (2 * j4 + e) * 4);
+        min_keys = min(q.len, q.len - q.lq + tile * kCols / a.g + 1);     // of the tile's first query
 
-        State<NT> s;
-        float koff = 11.f;
-        uint32_t v_limit = 0x3c003c00u;           // 2^e of koff = 11 - max(0, e), as a pair of fp16
+        float o[NT][8][4];                        // O^T: 8 tiles of 16 dims
+        float z[NT][4];                           // the minima's part, a row per group
+        float base[NT][2];                        // log2 of what weight 1 stands for (-inf: no key yet)
+        float sum[NT][2];                         // this lane's share of the weights
+        float koff = 10.f;
+        uint32_t v_limit = 0x40004000u;           // every V step so far is below it: 2^e, koff = 11 - e, e >= 1
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int m = 0; m < 8; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s.o[t][m][e] = 0.f;
+                for (int e = 0; e < 4; ++e) o[t][m][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s.z[t][e] = 0.f;
-            s.base[t][0] = s.base[t][1] = -INFINITY;
-            s.sum[t][0] = s.sum[t][1] = 0.f;
+            for (int e = 0; e < 4; ++e) z[t][e] = 0.f;
+            base[t][0] = base[t][1] = -INFINITY;
+            sum[t][0] = sum[t][1] = 0.f;
         }
 
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < mine; ++i) {
             copies_wait<kStages - 2>();
             __syncwarp();
             issue();
@@ -357,17 +423,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             {
                 const uint4 ka = *reinterpret_cast<const uint4 *>(chunk + lane * 16);
                 const uint4 kb = *reinterpret_cast<const uint4 *>(chunk + 512 + lane * 16);
-                const __half *steps = reinterpret_cast<const __half *>(chunk + 2 * kCodeBytes);
+                float s0[NG], s1[NG];
+                load_halves<NG>(chunk + 2 * kCodeBytes + r8 * 2 * NG, s0);
+                load_halves<NG>(chunk + 2 * kCodeBytes + (r8 + 8) * 2 * NG, s1);
                 uint32_t m0 = 0, m1 = 0;
                 if (j4 < NG) {
-                    const uint16_t *low = reinterpret_cast<const uint16_t *>(chunk + 2 * kCodeBytes + 32 * NG);
-                    m0 = low[r8 * NG + j4] * 0x10001u;
-                    m1 = low[(r8 + 8) * NG + j4] * 0x10001u;
+                    const uint16_t *m = reinterpret_cast<const uint16_t *>(chunk + 2 * kCodeBytes + 32 * NG);
+                    m0 = m[r8 * NG + j4] * 0x10001u;
+                    m1 = m[(r8 + 8) * NG + j4] * 0x10001u;
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma8(c, m0, m1, qsum[t]);
+                    mma8(c, m0, m1, kSharedQ ? s_sum[t][lane] : qs[kSharedQ ? 0 : t].sum);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[t][e] = c[e] * 0x1p-6f;
                 }
@@ -385,32 +453,37 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                            for (int t = 0; t < NT; ++t)
+                            for (int t = 0; t < NT; ++t) {
+                                const uint2 f = kSharedQ ? s_frag[t][y][u][lane] : qs[kSharedQ ? 0 : t].f[y][u];
                                 mma16(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                                      qf[t][y][u][0], qf[t][y][u][1]);
+                                      f.x, f.y);
+                            }
                             wa >>= 8;
                             wb >>= 8;
                         }
                     }
-                    const float s0 = __half2float(steps[r8 * NG + g]), s1 = __half2float(steps[(r8 + 8) * NG + g]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        x[t][0] = fmaf(s0, acc[t][0], x[t][0]);
-                        x[t][1] = fmaf(s0, acc[t][1], x[t][1]);
-                        x[t][2] = fmaf(s1, acc[t][2], x[t][2]);
-                        x[t][3] = fmaf(s1, acc[t][3], x[t][3]);
+                        x[t][0] = fmaf(s0[g], acc[t][0], x[t][0]);
+                        x[t][1] = fmaf(s0[g], acc[t][1], x[t][1]);
+                        x[t][2] = fmaf(s1[g], acc[t][2], x[t][2]);
+                        x[t][3] = fmaf(s1[g], acc[t][3], x[t][3]);
                     }
                 }
             }
 
             // V steps and minima: tokens 2 j4, 2 j4 + 1 and the same 8 further, of each group
-            uint32_t vs[NG][2], vm[2] = {0, 0};
+            uint32_t vs[NG][2], vm[2] = {0, 0}, any_step = 0;
             const unsigned char *v_meta = chunk + 2 * kCodeBytes + 64 * NG + j4 * 8 * NG;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(v_meta + 8 * g);
-                vs[g][0] = w.x;
-                vs[g][1] = w.y;
+                if (NG >= 2 && g % 2 == 0) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(v_meta + 8 * g);
+                    vs[g][0] = w.x, vs[g][1] = w.y, vs[(g + 1) % NG][0] = w.z, vs[(g + 1) % NG][1] = w.w;
+                } else if (NG == 1) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(v_meta);
+                    vs[g][0] = w.x, vs[g][1] = w.y;
+                }
             }
             if (r8 < NG) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(v_meta + 32 * NG + 8 * r8);
@@ -418,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 vm[1] = w.y;
             }
             const bool masked = t0 + kChunk > min_keys;
-            if (t0 + kChunk > q.len) {            // behind the last token anything may lie
+            if (masked && t0 + kChunk > q.len) {  // behind the last token anything may lie
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = t0 + 8 * h + 2 * j4;
@@ -428,65 +501,76 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     for (int g = 0; g < NG; ++g) vs[g][h] &= keep;
                 }
             }
-            uint32_t v_top = 0;                   // steps are >= 0, so their bits order them
 #pragma unroll
-            for (int g = 0; g < NG; ++g) v_top = __vmaxu2(v_top, __vmaxu2(vs[g][0], vs[g][1]));
+            for (int g = 0; g < NG; ++g) any_step |= vs[g][0] | vs[g][1];
 
             // weights
-            float y[NT][4];
-            bool rise = __vmaxu2(v_top, v_limit) != v_limit;
+            float y[NT][4], top = -INFINITY;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[t][e] *= factor[t][e & 1];
-                    if (masked && t0 + r8 + 4 * (e & 2) >= keys[t][e & 1]) x[t][e] = -INFINITY;
-                    y[t][e] = x[t][e] == -INFINITY ? -INFINITY : x[t][e] - s.base[t][e & 1];
-                    rise |= y[t][e] > koff + 4.f;
-                }
-            if (__any_sync(~0u, rise)) {
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) v_top = __vmaxu2(v_top, __shfl_xor_sync(~0u, v_top, d));
-                const uint32_t step = max(v_top & 0xffffu, v_top >> 16);
-                float koff2 = koff;
-                if (step > (v_limit & 0xffffu)) { // the power of two above the step
-                    const int e = min((int)(step >> 10) - 14, 16);
-                    koff2 = 11.f - e;
-                    v_limit = e >= 16 ? 0x7bff7bffu : (uint32_t)(e + 15) * 0x04000400u;
-                }
+                for (int e = 0; e < 4; ++e) y[t][e] = fmaf(x[t][e], factor[t][e & 1], -base[t][e & 1]);
+            if (masked) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float top = fmaxf(x[t][c], x[t][c + 2]);
+                    for (int e = 0; e < 4; ++e)
+                        if (t0 + r8 + 4 * (e & 2) >= keys_of(t, e & 1)) y[t][e] = -INFINITY;
+            }
 #pragma unroll
-                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                        const float old = s.base[t][c], b = fmaxf(old + koff, top) - koff2;
-                        const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
-                        s.base[t][c] = b;
-                        s.sum[t][c] *= keep;
-                        s.z[t][c] *= keep;
-                        s.z[t][c + 2] *= keep;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) {
-                            s.o[t][m][c] *= keep;
-                            s.o[t][m][c + 2] *= keep;
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, y[t][e]);
+            // a maximum to follow, or steps of 2 and more (bit 14 of an fp16 that is >= 0)
+            if (__any_sync(~0u, top > koff + 4.f || (any_step & 0x40004000u))) {
+                uint32_t v_top = 0;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) v_top = max(v_top, max(max(vs[g][0] & 0xffffu, vs[g][0] >> 16),
+                                                                    max(vs[g][1] & 0xffffu, vs[g][1] >> 16)));
+                v_top = __reduce_max_sync(~0u, v_top);
+                float koff2 = koff;
+                if (v_top >= (v_limit & 0xffffu)) {                   // the power of two above the step
+                    const int e = min((int)(v_top >> 10) - 14, 16);
+                    koff2 = 11.f - e;
+                    v_limit = e >= 16 ? 0x7fff7fffu : (uint32_t)(e + 15) * 0x04000400u;
+                }
+                if (koff2 != koff || __any_sync(~0u, top > koff + 4.f)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const bool out0 = y[t][c] == -INFINITY, out1 = y[t][c + 2] == -INFINITY;
+                            const float l0 = out0 ? -INFINITY : x[t][c] * factor[t][c];
+                            const float l1 = out1 ? -INFINITY : x[t][c + 2] * factor[t][c];
+                            float m = fmaxf(l0, l1);
+#pragma unroll
+                            for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+                            const float old = base[t][c], b = fmaxf(old + koff, m) - koff2;
+                            const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
+                            base[t][c] = b;
+                            sum[t][c] *= keep;
+                            z[t][c] *= keep;
+#pragma unroll
+                            for (int d = 0; d < 8; ++d) {
+                                o[t][d][c] *= keep;
+                                o[t][d][c + 2] *= keep;
+                            }
+                            y[t][c] = out0 ? -INFINITY : l0 - b;
+                            y[t][c + 2] = out1 ? -INFINITY : l1 - b;
                         }
-                        y[t][c] = x[t][c] == -INFINITY ? -INFINITY : x[t][c] - b;
-                        y[t][c + 2] = x[t][c + 2] == -INFINITY ? -INFINITY : x[t][c + 2] - b;
-                    }
-                koff = koff2;
+                    koff = koff2;
+                }
             }
             uint32_t p[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[t][e] = fast_exp2(y[t][e]);
-                s.sum[t][0] += y[t][0] + y[t][2];
-                s.sum[t][1] += y[t][1] + y[t][3];
+                sum[t][0] += y[t][0] + y[t][2];
+                sum[t][1] += y[t][1] + y[t][3];
                 p[t][0] = transpose8(pack_half2(y[t][0], y[t][1]));
                 p[t][1] = transpose8(pack_half2(y[t][2], y[t][3]));
-                mma16(s.z[t], vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
+                mma16(z[t], vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
             }
 
             // values
@@ -509,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
-                            mma16(s.o[t][2 * m + u], wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu,
+                            mma16(o[t][2 * m + u], wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu,
                                   wb & 0x00f000f0u, ps[t][0], ps[t][1]);
                         wa >>= 8;
                         wb >>= 8;
@@ -521,25 +605,24 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         __syncwarp();
 
         // -- join the warps -----------------------------------------------------------
-        float *mine_o = reinterpret_cast<float *>(ring);                       // [kCols][kOutStride]
-        float2 *ml = reinterpret_cast<float2 *>(smem + kWarps * kStages * kBytes);   // [kWarps][kCols]
+        float *mine_o = reinterpret_cast<float *>(ring);             // [kCols][kOutStride]
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float l = s.sum[t][c];
+                float l = sum[t][c];
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(~0u, l, d);
                 const int col = t * 8 + 2 * j4 + c;
-                if (r8 == 0) ml[warp * kCols + col] = make_float2(s.base[t][c], l);
+                if (r8 == 0) ml[warp][col] = make_float2(base[t][c], l);
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const float z = __shfl_sync(~0u, s.z[t][c], (m * NG / 4) * 4 + j4);
+                    const float low_part = __shfl_sync(~0u, z[t][c], (m * NG / 4) * 4 + j4);
                     float4 v;
-                    v.x = fmaf(s.o[t][2 * m][c], 0x1p24f, z);
-                    v.y = fmaf(s.o[t][2 * m][c + 2], 0x1p20f, z);
-                    v.z = fmaf(s.o[t][2 * m + 1][c], 0x1p24f, z);
-                    v.w = fmaf(s.o[t][2 * m + 1][c + 2], 0x1p20f, z);
+                    v.x = fmaf(o[t][2 * m][c], 0x1p24f, low_part);
+                    v.y = fmaf(o[t][2 * m][c + 2], 0x1p20f, low_part);
+                    v.z = fmaf(o[t][2 * m + 1][c], 0x1p24f, low_part);
+                    v.w = fmaf(o[t][2 * m + 1][c + 2], 0x1p20f, low_part);
                     *reinterpret_cast<float4 *>(mine_o + col * kOutStride + 32 * m + 4 * r8) = v;
                 }
             }
@@ -551,39 +634,33 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             if (i >= q.rows) continue;
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kCols + col].x);
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][col].x);
             float l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 e = ml[w * kCols + col];
+                const float2 e = ml[w][col];
                 const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
-                const float4 v = *reinterpret_cast<const float4 *>(
-                    reinterpret_cast<const float *>(smem + w * kStages * kBytes) + col * kOutStride + 4 * lane);
+                const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + w * kRing) +
+                                                                   col * kOutStride + 4 * lane);
                 l += e.x == -INFINITY ? e.y : f * e.y;       // a NaN's sum stays one
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
-                o.z = fmaf(f, v.z, o.z);
-                o.w = fmaf(f, v.w, o.w);
+                v.x = fmaf(f, x.x, v.x);
+                v.y = fmaf(f, x.y, v.y);
+                v.z = fmaf(f, x.z, v.z);
+                v.w = fmaf(f, x.w, v.w);
             }
             if (opens && closes) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-                __nv_bfloat162 hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-                *reinterpret_cast<uint2 *>(a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * lane) =
-                    make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-                if (a.lse && lane == 0)
-                    a.lse[(long long)head * a.total_q + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+                store_row(a, row, head, lane, v, top, l);
             } else {
                 const long long slot = ((long long)blockIdx.x * 2 + (opens ? 1 : 0)) * kCols + col;
-                *reinterpret_cast<float4 *>(sc.o + slot * kHeadDim + 4 * lane) = o;
+                *reinterpret_cast<float4 *>(sc.o + slot * kHeadDim + 4 * lane) = v;
                 if (lane == 0) sc.ml[slot] = make_float2(top, l);
             }
         }
         if (opens && !closes && tid == 0) {
-            const long long last = item0 + chunks - 1;           // and the block that has it
+            const long long last = item0 + chunks - 1;       // and the block that has it
             const int b = (int)(((last + 1) * blocks - 1) / total);
-            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, r, kv, tile};
+            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv * tiles + tile, tiles};
         }
         __syncthreads();
         at = item0 + c1;
@@ -602,10 +679,10 @@ __global__ void __launch_bounds__(256) join_kernel(QAttn a, Scratch sc) {
     const Open it = sc.open[blockIdx.x];
     if (it.parts == 0) return;
     const int lane = threadIdx.x & 31;
-    const Request q = request_of(a, it.r);
+    const int kv = it.item / it.tiles, tile = it.item - kv * it.tiles;
     for (int col = threadIdx.x / 32; col < kCols; col += 8) {
-        const int cc = it.tile * kCols + col, i = cc / a.g, head = it.kv * a.g + cc % a.g, row = q.row0 + i;
-        if (i >= q.rows) continue;
+        const int cc = tile * kCols + col, i = cc / a.g, head = kv * a.g + cc % a.g;
+        if (i >= it.rows) continue;
         const auto slot = [&](int p) { return ((long long)(blockIdx.x + p) * 2 + (p == 0)) * kCols + col; };
         float top = -INFINITY;
         for (int p = lane; p < it.parts; p += 32) top = fmaxf(top, sc.ml[slot(p)].x);
@@ -624,20 +701,19 @@ __global__ void __launch_bounds__(256) join_kernel(QAttn a, Scratch sc) {
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(a.out + ((long long)row * a.h_q + head) * kHeadDim + 4 * lane) =
-            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-        if (a.lse && lane == 0)
-            a.lse[(long long)head * a.total_q + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+        store_row(a, it.row0 + i, head, lane, o, top, l);
     }
 }
 
-// 8 columns to a tile while they hold a kv head's (query, head) pairs, else 16.
-int tile_columns(const QAttn &a) { return (long long)a.max_q * a.g <= 8 ? 8 : 16; }
+// The narrowest tile that holds a kv head's (query, head) pairs, or the widest.
+int tile_columns(const QAttn &a) {
+    const long long cols = (long long)a.max_q * a.g;
+    return cols <= 8 ? 8 : cols <= 16 ? 16 : 32;
+}
 
 int blocks_of(const QAttn &a) {
-    const int cols = tile_columns(a), most = kSm * (cols == 8 ? blocks_per_sm<1>() : blocks_per_sm<2>());
+    const int cols = tile_columns(a);
+    const int most = kSm * (cols == 8 ? blocks_per_sm<1>() : cols == 16 ? blocks_per_sm<2>() : blocks_per_sm<4>());
     // no more than the longest lengths that the table can hold would use
     const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
     const long long tiles = rows * a.g / cols + a.batch;
@@ -649,12 +725,14 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int NG, int NT>
 cudaError_t launch(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t st) {
-    constexpr int smem = kWarps * (stages<NT>() * (2 * kCodeBytes + 128 * NG) + 8 * NT * (int)sizeof(float2));
+    constexpr int smem = kWarps * stages<NT>() * (2 * kCodeBytes + 128 * NG);
     static_assert(stages<NT>() * (2 * kCodeBytes + 128 * NG) >= 8 * NT * kOutStride * 4, "a warp's result fits its ring");
-    static_assert(smem <= 47 * 1024, "no opt-in to more shared memory");
-    attn_kernel<NG, NT><<<blocks, kThreads, smem, st>>>(a, sc);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (smem > 46 * 1024)       // above the default limit, with the static part
+        e = cudaFuncSetAttribute(attn_kernel<NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    attn_kernel<NG, NT><<<blocks, kThreads, smem, st>>>(a, sc);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(256);
@@ -692,7 +770,11 @@ cudaError_t launch_qcache_attn(const QAttn &a, void *scratch, cudaStream_t st) {
     sc.ml = reinterpret_cast<float2 *>(p);
     p += align256(n * 2 * cols * sizeof(float2));
     sc.o = reinterpret_cast<float *>(p);
-    return cols == 8 ? launch_groups<1>(a, sc, (int)n, st) : launch_groups<2>(a, sc, (int)n, st);
+    switch (cols) {
+        case 8: return launch_groups<1>(a, sc, (int)n, st);
+        case 16: return launch_groups<2>(a, sc, (int)n, st);
+        default: return launch_groups<4>(a, sc, (int)n, st);
+    }
 }
 
 }  // namespace fp

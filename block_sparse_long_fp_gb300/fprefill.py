@@ -334,12 +334,22 @@ class Layer:
         return out, lse, (row_ptr, col_idx, nnz)
 
 
-def _need(t, name: str, dtypes, device, ndim: int, contiguous: bool = True):
+def _need(t, name: str, dtypes, device: int, ndim: int, contiguous: bool = True):
     """An argument check of the classes below: FprefillError (invalid argument) names the tensor."""
-    if t.dtype not in dtypes or t.dim() != ndim or t.device != device or (contiguous and not t.is_contiguous()):
-        raise FprefillError(FP_ERR_INVALID, f"{name}: {ndim}-d {'contiguous ' if contiguous else ''}tensor of "
-                            f"{' or '.join(str(d) for d in dtypes)} on {device} wanted, got {tuple(t.shape)} {t.dtype} on "
-                            f"{t.device}")
+    if t.dtype in dtypes and t.dim() == ndim and t.get_device() == device and (not contiguous or t.is_contiguous()):
+        return
+    raise FprefillError(FP_ERR_INVALID, f"{name}: {ndim}-d {'contiguous ' if contiguous else ''}tensor of "
+                        f"{' or '.join(str(d) for d in dtypes)} on cuda:{device} wanted, got {tuple(t.shape)} {t.dtype} "
+                        f"on {t.device}")
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream's handle on a device; the short way, where torch has it, saves a microsecond a call."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 class _OnDevice:
@@ -350,19 +360,21 @@ class _OnDevice:
         import torch
         if device.type != "cuda":
             raise FprefillError(FP_ERR_INVALID, f"a CUDA tensor is wanted, got {device}")
+        lib()
         self.device = device
+        self._index = device.index
         self._ws = torch.zeros(FP_WS_HEADER_BYTES // 4, dtype=torch.int32, device=device)
         self._ws_ptr = self._ws.data_ptr()
 
     def _call(self, what: str, *args):
+        """The entry point on the current stream of this object's device."""
         import torch
-        f = getattr(lib(), what)
-        stream = torch.cuda.current_stream(self.device).cuda_stream
-        if torch.cuda.current_device() == self.device.index:
-            s = f(*args, stream)
+        f = getattr(_lib, what)
+        if torch.cuda.current_device() == self._index:
+            s = f(*args, _raw_stream(self._index))
         else:
-            with torch.cuda.device(self.device):
-                s = f(*args, stream)
+            with torch.cuda.device(self._index):
+                s = f(*args, _raw_stream(self._index))
         if s != FP_OK:
             raise FprefillError(s, what)
 
@@ -391,7 +403,7 @@ class PageTables(_OnDevice):
     def __init__(self, block_table, page_size: int, num_pages: int, capacity: int):
         import torch
         super().__init__(block_table.device)
-        _need(block_table, "block_table", (torch.int32,), self.device, 2)
+        _need(block_table, "block_table", (torch.int32,), self._index, 2)
         if capacity < 1:
             raise FprefillError(FP_ERR_INVALID, "capacity")
         self.block_table, self.capacity = block_table, int(capacity)
@@ -414,7 +426,7 @@ class PageTables(_OnDevice):
         free_pages: int32, used from entry free_head (int32 [1], 0 when None)
         on.  Passing this object's own seqlens_k and free_head advances both in
         place."""
-        t, dev, kinds = self._t, self.device, self._int32
+        t, dev, kinds = self._t, self._index, self._int32
         _need(seqlens, "seqlens", kinds, dev, 1)
         _need(new_lens, "new_lens", kinds, dev, 1)
         _need(free_pages, "free_pages", kinds, dev, 1)
@@ -443,7 +455,7 @@ class QCache(_OnDevice):
     def __init__(self, data, page_size: int, group: int = 32):
         import torch
         super().__init__(data.device)
-        _need(data, "data", (torch.uint8,), self.device, 4)
+        _need(data, "data", (torch.uint8,), self._index, 4)
         c = self._c = FpQCache()
         c.data, c.num_pages, c.h_kv, c.d = _ptr(data), data.shape[0], data.shape[1], 128
         c.page_size, c.group = int(page_size), int(group)
@@ -453,7 +465,7 @@ class QCache(_OnDevice):
             raise FprefillError(FP_ERR_INVALID, f"data: [pages, heads, {c.page_size // 16}, {self.chunk_bytes(group)}] "
                                 f"wanted, got {tuple(data.shape)}")
         self.data, self.h_kv, self.page_size, self.group = data, c.h_kv, c.page_size, c.group
-        self._scratch = {}
+        self._scratch, self._scratch_bytes = {}, {}
         self._bf16, self._fp8 = (torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn)
         self._int32, self._fp32 = (torch.int32,), (torch.float32,)
 
@@ -471,7 +483,7 @@ class QCache(_OnDevice):
                                device=device), page_size, group)
 
     def _rows(self, k, v, slots, k_scale, v_scale, out_slots=None):
-        dev, h = self.device, self.h_kv
+        dev, h = self._index, self.h_kv
         fp8 = k_scale is not None or v_scale is not None
         kinds = self._fp8 if fp8 else self._bf16
         _need(k, "k", kinds, dev, 3, False)
@@ -530,7 +542,7 @@ class QCache(_OnDevice):
         cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
         cu_seqlens_q, max_q rows each (total_q / batch by default)."""
         import torch
-        dev = self.device
+        dev = self._index
         _need(q, "q", self._bf16 if q_scale is None else self._fp8, dev, 3, False)
         _need(block_table, "block_table", self._int32, dev, 2)
         _need(seqlens_k, "seqlens_k", self._int32, dev, 1)
@@ -557,36 +569,41 @@ class QCache(_OnDevice):
                           _ptr(cu_seqlens_q), seqlens_k.data_ptr(), block_table.data_ptr(), block_table.shape[1],
                           softmax_scale)
         if out is None:
-            out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=self.device)
         else:
             _need(out, "out", self._bf16, dev, 3)
             if out.shape != q.shape:
                 raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
         if lse is None and want_lse:
-            lse = torch.empty((h_q, total_q), dtype=torch.float32, device=dev)
+            lse = torch.empty((h_q, total_q), dtype=torch.float32, device=self.device)
         elif lse is not None:
             _need(lse, "lse", self._fp32, dev, 2)
             if lse.shape != (h_q, total_q):
                 raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
-        n = int(lib().fp_qcache_attn_scratch_bytes(self._c, Q))
-        scratch = self._scratch_of(n)
-        self._call("fp_qcache_attn", self._c, Q, out.data_ptr(), _ptr(lse), scratch.data_ptr(), n, self._ws_ptr,
+        shape = (batch, h_q, total_q, max_q, cu_seqlens_q is None, block_table.shape[1])
+        n = self._scratch_bytes.get(shape)
+        if n is None:
+            n = self._scratch_bytes[shape] = int(_lib.fp_qcache_attn_scratch_bytes(self._c, Q))
+        self._call("fp_qcache_attn", self._c, Q, out.data_ptr(), _ptr(lse), self._scratch_of(n), n, self._ws_ptr,
                    FP_WS_HEADER_BYTES)
         return out, lse
 
-    def _scratch_of(self, nbytes: int):
+    def _scratch_of(self, nbytes: int) -> int:
         """Scratch of the current stream: calls on two streams share none, and a
         captured call has its own, out of the graph's memory."""
         import torch
-        stream = torch.cuda.current_stream(self.device)
-        with torch.cuda.device(self.device):
+        if torch.cuda.current_device() == self._index:
             capturing = torch.cuda.is_current_stream_capturing()
-        old = None if capturing else self._scratch.get(stream.cuda_stream)
+        else:
+            with torch.cuda.device(self._index):
+                capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            return torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device).data_ptr()
+        stream = _raw_stream(self._index)
+        old = self._scratch.get(stream)
         if old is None or old.numel() < nbytes:
-            old = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
-            if not capturing:
-                self._scratch[stream.cuda_stream] = old
-        return old
+            old = self._scratch[stream] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
+        return old.data_ptr()
 
 
 def layer_from_case(case, device="cuda", params: FpParams | None = None, v_layout: int = 0):
