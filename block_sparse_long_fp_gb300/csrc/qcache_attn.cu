@@ -30,6 +30,8 @@
 // nothing to wait on but its own copies), and join their results at the item's
 // end.  An item cut by a range's end leaves partial results, which the second
 // kernel joins.
+#include <type_traits>
+
 #include "qcache.cuh"
 
 namespace fp {
@@ -38,7 +40,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSm = 152;
-constexpr int kMinChunks = 2 * kWarps;       // fewest chunks worth a thread block
+constexpr int kMinUnits = 2 * kWarps;        // least work worth a thread block
+constexpr int kItemUnits = 8;                // what starting and ending an item costs, in chunks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's result in shared memory
@@ -47,6 +50,9 @@ constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's re
 struct Open {
     int parts, row0, rows, item, tiles;      // item: kv head * tiles + tile
 };
+
+// What a page id out of range, or an empty cache, reads.
+__device__ __align__(16) unsigned char zero_chunk[2 * kCodeBytes + 128 * 4];
 
 struct Scratch {
     Open *open;                              // [blocks]
@@ -69,10 +75,18 @@ __device__ __forceinline__ void mma16(float c[4], uint32_t a0, uint32_t a1, uint
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float c[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(b0));
+// The same from zero: the accumulator needs no clearing.
+__device__ __forceinline__ void mma16_zero(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma8_zero(float d[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 // Transpose of the 8 x 8 fp16 matrix whose row lane / 4 holds the lane's pair.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -262,8 +276,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r8 = lane >> 2, j4 = lane & 3;
 
-    // this block's range of chunks, and the request it starts in
-    const auto units = [&](const Request &q) { return (long long)a.c.h_kv * tiles_of(a, q, kCols) * chunks_of(q); };
+    // this block's range of units of work, and the request it starts in: an item is
+    // kItemUnits for its start and end, then a unit for each chunk
+    const auto units = [&](const Request &q) {
+        return (long long)a.c.h_kv * tiles_of(a, q, kCols) * (kItemUnits + chunks_of(q));
+    };
     Request q = {0, 0, 0, 0};
     if (tid < a.batch) q = request_of(a, tid);
     long long n = units(q), total;
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         block_scan(base + tid < a.batch ? units(request_of(a, base + tid)) : 0, &all, warp_sums);
         total += all;
     }
-    const long long want = (total + kMinChunks - 1) / kMinChunks;
+    const long long want = (total + kMinUnits - 1) / kMinUnits;
     const int blocks = (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
@@ -299,11 +316,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
     }
     __syncthreads();
     int r = s_r;
-    long long item0 = s_at;                       // first chunk of the current item
+    long long item0 = s_at;                       // first unit of the current item
     q = s_q;
     int tiles = tiles_of(a, q, kCols), chunks = chunks_of(q);
-    int item = (int)((first - item0) / chunks);   // kv head and tile
-    item0 += (long long)item * chunks;
+    int item = (int)((first - item0) / (kItemUnits + chunks));   // kv head and tile
+    item0 += (long long)item * (kItemUnits + chunks);
 
     unsigned char *ring = smem + warp * kRing;
     const uint32_t ring_at = smem_addr(ring) + lane * 16;
@@ -318,15 +335,22 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             item = 0;
         }
         const int kv = item / tiles, tile = item - kv * tiles;
-        const int c0 = (int)(at - item0), c1 = (int)(end - item0 < chunks ? end - item0 : chunks);
+        const long long next = item0 + kItemUnits + chunks;
+        const int c0 = (int)max(0ll, at - item0 - kItemUnits);
+        const int c1 = (int)max(0ll, min(end, next) - item0 - kItemUnits);
+        if (c1 <= c0) {                           // the range ends inside the item's start
+            at = item0 = next;
+            ++item;
+            continue;
+        }
         const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
 
         // -- copies ahead: chunk c0 + warp + i * kWarps into stage i % kStages.  Lane l
-        //    looks up the addresses of chunks l, l + 32, ..., zero where there is none.
+        //    looks up the addresses of chunks l, l + 32, ...
         unsigned long long src = 0;
         const auto look_up = [&](int i) {
             const int c = c0 + warp + (i + lane) * kWarps;
-            src = 0;
+            src = (unsigned long long)zero_chunk;
             if (i + lane < mine && q.len > 0) {
                 const int pg = c / per_page, page = a.block_table[(long long)r * a.max_pages + pg];
                 if (page >= 0 && page < a.c.num_pages)
@@ -341,17 +365,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 if (issued && issued % 32 == 0) look_up(issued);
                 const unsigned long long from = __shfl_sync(~0u, src, issued & 31);
                 const uint32_t dst = ring_at + (issued % kStages) * kBytes;
-                if (from) {
-                    const char *p = reinterpret_cast<const char *>(from) + lane * 16;
+                const char *p = reinterpret_cast<const char *>(from) + lane * 16;
 #pragma unroll
-                    for (int i = 0; i < (kBytes + 511) / 512; ++i)
-                        if ((i + 1) * 512 <= kBytes || lane * 16 < kBytes - i * 512) copy16(dst + i * 512, p + i * 512);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < (kBytes + 511) / 512; ++i)
-                        if ((i + 1) * 512 <= kBytes || lane * 16 < kBytes - i * 512)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512), "r"(0) : "memory");
-                }
+                for (int i = 0; i < (kBytes + 511) / 512; ++i)
+                    if ((i + 1) * 512 <= kBytes || lane * 16 < kBytes - i * 512) copy16(dst + i * 512, p + i * 512);
                 ++issued;
             }
             copies_commit();
@@ -411,7 +428,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             sum[t][0] = sum[t][1] = 0.f;
         }
 
-        for (int i = 0; i < mine; ++i) {
+        const auto step = [&](int i, auto edge) {
+            constexpr bool kEdge = decltype(edge)::value;
             copies_wait<kStages - 2>();
             __syncwarp();
             issue();
@@ -434,18 +452,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma8(c, m0, m1, kSharedQ ? s_sum[t][lane] : qs[kSharedQ ? 0 : t].sum);
+                    float c[4];
+                    mma8_zero(c, m0, m1, kSharedQ ? s_sum[t][lane] : qs[kSharedQ ? 0 : t].sum);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[t][e] = c[e] * 0x1p-6f;
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     float acc[NT][4];
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
                     for (int y = g * 4 / NG; y < (g + 1) * 4 / NG; ++y) {
                         uint32_t wa = y == 0 ? ka.x : y == 1 ? ka.y : y == 2 ? ka.z : ka.w;
@@ -455,8 +469,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
                                 const uint2 f = kSharedQ ? s_frag[t][y][u][lane] : qs[kSharedQ ? 0 : t].f[y][u];
-                                mma16(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u, wb & 0x00f000f0u,
-                                      f.x, f.y);
+                                if (y == g * 4 / NG && u == 0)
+                                    mma16_zero(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u,
+                                               wb & 0x00f000f0u, f.x, f.y);
+                                else
+                                    mma16(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u,
+                                          wb & 0x00f000f0u, f.x, f.y);
                             }
                             wa >>= 8;
                             wb >>= 8;
@@ -490,8 +508,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 vm[0] = w.x;
                 vm[1] = w.y;
             }
-            const bool masked = t0 + kChunk > min_keys;
-            if (masked && t0 + kChunk > q.len) {  // behind the last token anything may lie
+            if (kEdge && t0 + kChunk > q.len) {   // behind the last token anything may lie
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = t0 + 8 * h + 2 * j4;
@@ -510,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[t][e] = fmaf(x[t][e], factor[t][e & 1], -base[t][e & 1]);
-            if (masked) {
+            if (kEdge) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -600,7 +617,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     }
                 }
             }
-        }
+        };
+        // chunks that every column sees whole, then those at the causal edge or the end
+        const int whole = min_keys / kChunk - c0 > warp ? (min_keys / kChunk - c0 - warp + kWarps - 1) / kWarps : 0;
+        int i = 0;
+        for (; i < min(whole, mine); ++i) step(i, std::false_type());
+        for (; i < mine; ++i) step(i, std::true_type());
         copies_wait<0>();
         __syncwarp();
 
@@ -658,50 +680,89 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             }
         }
         if (opens && !closes && tid == 0) {
-            const long long last = item0 + chunks - 1;       // and the block that has it
+            const long long last = next - 1;                 // and the block that has it
             const int b = (int)(((last + 1) * blocks - 1) / total);
             sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv * tiles + tile, tiles};
         }
         __syncthreads();
-        at = item0 + c1;
-        item0 += chunks;
+        at = item0 = next;
         ++item;
     }
 }
 
-// Joins the parts of an item that several blocks share: part 0 in its first
+// Joins the parts of the items that several blocks share: part 0 in the first
 // block's second slot, the others in the first slots of the blocks behind it.
-// One warp per column.
+// A task is a column of an open item.  With 8 parts and more to an item a block
+// takes a task, its warps a share of the parts each; else a warp does.
+constexpr int kJoinWarps = 8;
+
 template <int NT>
-__global__ void __launch_bounds__(256) join_kernel(QAttn a, Scratch sc) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch sc, int blocks) {
     constexpr int kCols = 8 * NT;
+    __shared__ int open[kSm * blocks_per_sm<1>()], count[kJoinWarps];
+    __shared__ float4 part_o[kJoinWarps][32];
+    __shared__ float part_l[kJoinWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Open it = sc.open[blockIdx.x];
-    if (it.parts == 0) return;
-    const int lane = threadIdx.x & 31;
-    const int kv = it.item / it.tiles, tile = it.item - kv * it.tiles;
-    for (int col = threadIdx.x / 32; col < kCols; col += 8) {
-        const int cc = tile * kCols + col, i = cc / a.g, head = kv * a.g + cc % a.g;
-        if (i >= it.rows) continue;
-        const auto slot = [&](int p) { return ((long long)(blockIdx.x + p) * 2 + (p == 0)) * kCols + col; };
-        float top = -INFINITY;
-        for (int p = lane; p < it.parts; p += 32) top = fmaxf(top, sc.ml[slot(p)].x);
-#pragma unroll
-        for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = 0; p < it.parts; ++p) {
-            const float2 e = sc.ml[slot(p)];
-            const float4 v = *reinterpret_cast<const float4 *>(sc.o + slot(p) * kHeadDim + 4 * lane);
-            const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
-            l += e.x == -INFINITY ? e.y : f * e.y;
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
+    // the blocks that left an item open, in the same order for every block of this grid
+    int opens = 0;
+    for (int base = 0; base < blocks; base += kJoinWarps * 32) {
+        const int b = base + threadIdx.x;
+        const bool is = b < blocks && sc.open[b].parts > 0;
+        const unsigned vote = __ballot_sync(~0u, is);
+        if (lane == 0) count[warp] = __popc(vote);
+        __syncthreads();
+        int at = opens + __popc(vote & ((1u << lane) - 1));
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w < warp) at += count[w];
+            opens += count[w];
         }
-        store_row(a, it.row0 + i, head, lane, o, top, l);
+        if (is) open[at] = b;
+        __syncthreads();
+    }
+    const bool wide = opens * 8 <= blocks;
+    const int step = wide ? 1 : kJoinWarps, w0 = wide ? warp : 0, dw = wide ? kJoinWarps : 1;
+    for (int task0 = blockIdx.x * step; task0 < opens * kCols; task0 += gridDim.x * step) {
+        const int task = task0 + (wide ? 0 : warp);
+        const bool live = task < opens * kCols;
+        const int b = open[live ? task / kCols : 0], col = task % kCols;
+        const Open it = sc.open[b];
+        const int kv = it.item / it.tiles, tile = it.item - kv * it.tiles;
+        const int cc = tile * kCols + col, i = cc / a.g, head = kv * a.g + cc % a.g;
+        float top = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && i < it.rows) {
+            const auto slot = [&](int p) { return ((long long)(b + p) * 2 + (p == 0)) * kCols + col; };
+            for (int p = lane; p < it.parts; p += 32) top = fmaxf(top, sc.ml[slot(p)].x);
+#pragma unroll
+            for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+#pragma unroll 4
+            for (int p = w0; p < it.parts; p += dw) {
+                const float2 e = sc.ml[slot(p)];
+                const float4 v = *reinterpret_cast<const float4 *>(sc.o + slot(p) * kHeadDim + 4 * lane);
+                const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
+                l += e.x == -INFINITY ? e.y : f * e.y;
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+                o.z = fmaf(f, v.z, o.z);
+                o.w = fmaf(f, v.w, o.w);
+            }
+            if (!wide) store_row(a, it.row0 + i, head, lane, o, top, l);
+        }
+        if (wide) {
+            part_o[warp][lane] = o;
+            if (lane == 0) part_l[warp] = l;
+            __syncthreads();
+            if (warp == 0 && i < it.rows) {
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float4 v = part_o[w][lane];
+                    l += part_l[w];
+                    o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+                }
+                store_row(a, it.row0 + i, head, lane, o, top, l);
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -718,7 +779,8 @@ int blocks_of(const QAttn &a) {
     const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
     const long long tiles = rows * a.g / cols + a.batch;
     const double chunks = (double)a.c.h_kv * tiles * a.max_pages * (a.c.page_size / kChunk);
-    return chunks < (double)most * kMinChunks ? (int)(chunks / kMinChunks) + 1 : most;
+    const double units = chunks + (double)a.c.h_kv * tiles * kItemUnits;
+    return units < (double)most * kMinUnits ? (int)(units / kMinUnits) + 1 : most;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -734,15 +796,15 @@ cudaError_t launch(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     attn_kernel<NG, NT><<<blocks, kThreads, smem, st>>>(a, sc);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(blocks < 2 * kSm ? blocks : 2 * kSm);
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<NT>, a, sc);
+    return cudaLaunchKernelEx(&cfg, join_kernel<NT>, a, sc, blocks);
 }
 
 template <int NT>
