@@ -9,8 +9,6 @@
 namespace fp {
 namespace {
 
-constexpr int kTokens = 8;      // consecutive tokens per thread
-
 struct Plan {
     int cu;        // first row
     int old;       // cached tokens; for a refused request, -1
@@ -40,16 +38,21 @@ __device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2 *sum, lon
     return make_longlong2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
-__device__ __forceinline__ int pages_of(long long tokens, int page_size) {
-    return (int)((tokens + page_size - 1) / page_size);
-}
-
-__global__ void tables_kernel(fp_tables t, int *status) {
+// kTokens: consecutive tokens per thread.
+template <int kTokens>
+__global__ void tables_kernel(fp_tables t, int shift, int *status) {
     extern __shared__ Plan plan[];               // [batch]
     __shared__ longlong2 warp_sums[32];
     __shared__ long long taken;
+    after_previous();
     const int nthr = blockDim.x;
     const bool first = blockIdx.x == 0;
+    // shift: log2 of page_size, or -1 where it is no power of two
+    const auto page_of = [&](int pos) { return shift >= 0 ? pos >> shift : pos / t.page_size; };
+    const auto pages = [&](long long tokens) {
+        tokens += t.page_size - 1;
+        return shift >= 0 ? tokens >> shift : tokens / t.page_size;
+    };
     const int head = t.free_head ? *t.free_head : 0;
     const long long avail = head < 0 ? 0 : (long long)t.num_free - head;
     if (threadIdx.x == 0) taken = 0;
@@ -62,9 +65,9 @@ __global__ void tables_kernel(fp_tables t, int *status) {
         if (r < t.batch) {
             old = t.seqlens[r];
             add = t.new_lens[r];
-            const long long pages = (old + add + t.page_size - 1) / t.page_size;
-            ok = old >= 0 && add >= 0 && pages <= t.max_pages_per_seq;
-            need = ok ? pages - pages_of(old, t.page_size) : 0;
+            const long long all = old >= 0 && add >= 0 ? pages(old + add) : -1;
+            ok = all >= 0 && all <= t.max_pages_per_seq;
+            need = ok ? all - pages(old) : 0;
             if (add < 0) add = 0;
         }
         longlong2 sum;
@@ -96,14 +99,18 @@ __global__ void tables_kernel(fp_tables t, int *status) {
         }
         if (refused || head < 0 || head > t.num_free) set_status(status, FP_ERR_DEVICE_BOUNDS);
     }
-    // new table entries, request by request
+    // new table entries: entry n of the scan belongs to the last request whose first is at or before it
     const int gthreads = gridDim.x * nthr, gthread = blockIdx.x * nthr + threadIdx.x;
-    for (int r = blockIdx.x; r < t.batch; r += gridDim.x) {
-        const Plan p = plan[r];
-        if (p.old < 0) continue;
-        const int used = pages_of(p.old, t.page_size), need = pages_of((long long)p.old + p.len, t.page_size) - used;
-        for (int k = threadIdx.x; k < need; k += nthr)
-            t.block_table[(long long)r * t.max_pages_per_seq + used + k] = t.free_pages[head + p.off + k];
+    const long long entries = min(carry.y, avail);
+    for (long long n = gthread; n < entries; n += gthreads) {
+        int lo = 0, hi = t.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (plan[mid].off <= n) lo = mid; else hi = mid - 1;
+        }
+        const Plan p = plan[lo];
+        if (p.old >= 0)
+            t.block_table[(long long)lo * t.max_pages_per_seq + pages(p.old) + n - p.off] = t.free_pages[head + n];
     }
     // tokens
     for (long long i0 = (long long)gthread * kTokens; i0 < t.capacity; i0 += (long long)gthreads * kTokens) {
@@ -113,27 +120,33 @@ __global__ void tables_kernel(fp_tables t, int *status) {
             if (plan[mid].cu <= i0) lo = mid; else hi = mid - 1;
         }
         int r = lo, pos[kTokens], slot[kTokens];
+        const int *from[kTokens];                // where the token's page id is
         Plan p = plan[r];
 #pragma unroll
         for (int j = 0; j < kTokens; ++j) {
             const long long i = i0 + j;
             while (i - p.cu >= p.len && r + 1 < t.batch) p = plan[++r];
             const long long local = i - p.cu;
-            pos[j] = 0;
-            slot[j] = -1;
-            if (local >= p.len || p.old < 0) continue;
-            pos[j] = p.old + (int)local;
-            const int pg = pos[j] / t.page_size, used = pages_of(p.old, t.page_size);
-            const int id = pg < used ? t.block_table[(long long)r * t.max_pages_per_seq + pg]
-                                     : t.free_pages[head + p.off + pg - used];
-            if (id < 0 || id >= t.num_pages)
-                set_status(status, FP_ERR_DEVICE_BOUNDS);
-            else
-                slot[j] = id * t.page_size + pos[j] % t.page_size;
+            const bool live = local < p.len && p.old >= 0;
+            pos[j] = live ? p.old + (int)local : 0;
+            const int pg = page_of(pos[j]), used = live ? (int)pages(p.old) : 0;
+            from[j] = !live ? nullptr
+                            : pg < used ? t.block_table + (long long)r * t.max_pages_per_seq + pg
+                                        : t.free_pages + head + p.off + pg - used;
         }
-        if (i0 + kTokens <= t.capacity) {
 #pragma unroll
-            for (int j = 0; j < kTokens; j += 4) {
+        for (int j = 0; j < kTokens; ++j) slot[j] = from[j] ? *from[j] : -1;
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j) {
+            const bool in = slot[j] >= 0 && slot[j] < t.num_pages;
+            bad |= from[j] && !in;
+            slot[j] = from[j] && in ? slot[j] * t.page_size + pos[j] - page_of(pos[j]) * t.page_size : -1;
+        }
+        if (bad) set_status(status, FP_ERR_DEVICE_BOUNDS);
+        if (kTokens % 4 == 0 && i0 + kTokens <= t.capacity) {
+#pragma unroll
+            for (int j = 0; j + 3 < kTokens; j += 4) {
                 *reinterpret_cast<int4 *>(t.positions + i0 + j) = make_int4(pos[j], pos[j + 1], pos[j + 2], pos[j + 3]);
                 *reinterpret_cast<int4 *>(t.slots + i0 + j) = make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
             }
@@ -154,18 +167,24 @@ cudaError_t launch_page_tables(const fp_tables &t, int *status, cudaStream_t st)
     // Advancing lengths or the free list in place needs every read before the
     // first write: one block, whose scan ends in a barrier, does that.
     const bool in_place = t.seqlens_k == t.seqlens || t.free_next == t.free_head;
+    // One token per thread while that fills the GPU no more than twice: the call is
+    // bound by the latency of the dependent look-ups (a decode step of 64 requests:
+    // 25 us with 8 tokens per thread in turn).  Longer ones take 8, one scan of the
+    // batch for 2048 tokens.
     const int threads = in_place ? 1024 : 256;
-    const long long per_block = (long long)threads * kTokens;
+    const int tokens = t.capacity <= 2 * 152 * 256 ? 1 : 8;
+    const long long per_block = (long long)threads * tokens;
     long long grid = in_place ? 1 : (t.capacity + per_block - 1) / per_block;
     if (grid > 2 * 152) grid = 2 * 152;
     const size_t smem = (size_t)t.batch * sizeof(Plan);
+    const auto kernel = tokens == 1 ? tables_kernel<1> : tables_kernel<8>;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    FP_TABLES_MAX_BATCH * (int)sizeof(Plan));
         if (e != cudaSuccess) return e;
     }
-    tables_kernel<<<(unsigned)grid, threads, smem, st>>>(t, status);
-    return cudaGetLastError();
+    const int shift = (t.page_size & (t.page_size - 1)) == 0 ? __builtin_ctz(t.page_size) : -1;
+    return launch_chained(kernel, (unsigned)grid, threads, smem, st, t, shift, status);
 }
 
 }  // namespace fp

@@ -37,6 +37,29 @@ __device__ __forceinline__ int v_step_off(int t, int g, int groups) {
     return 2 * kCodeBytes + 64 * groups + ((((t & 7) >> 1) * groups + g) * 4 + (t >> 3) * 2 + (t & 1)) * 2;
 }
 
+// Launches that may begin while the kernel before them in the stream ends: every
+// kernel here waits for it (after_previous) before it touches memory, and lets the
+// next one be set up in turn, which hides most of a launch's latency in a chain of
+// short kernels.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct QRows {
     const void *k, *v;
     long long stride_tok, stride_head;

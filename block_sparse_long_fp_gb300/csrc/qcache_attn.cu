@@ -47,8 +47,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's result in shared memory
 
 // An item that its first thread block leaves open: where, and in how many parts.
-struct Open {
-    int parts, row0, rows, item, tiles;      // item: kv head * tiles + tile
+struct __align__(16) Open {
+    int parts, row0, rows, kv, tile, pad[3];
 };
 
 // What a page id out of range, or an empty cache, reads.
@@ -181,36 +181,57 @@ struct Queries {
     float factor;      // of column lane / 4
 };
 
-template <int NG>
-__device__ __forceinline__ void load_queries(const QAttn &a, const Request &q, int kv, int col, Queries &out) {
+// A column's 32 elements of this lane as they lie in memory (bf16, or e4m3 in the
+// first half), and its scale.
+struct RawQuery {
+    uint4 w[4];
+    float scale;
+};
+
+__device__ __forceinline__ RawQuery fetch_query(const QAttn &a, const Request &q, int kv, int col) {
     const int j4 = threadIdx.x & 3, i = col / a.g, head = kv * a.g + col % a.g;
-    float x[32], top = 0.f, f = a.scale * kLog2e;
+    RawQuery raw;
+    raw.scale = a.scale * kLog2e;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) x[e] = 0.f;
+    for (int y = 0; y < 4; ++y) raw.w[y] = make_uint4(0, 0, 0, 0);
     if (i < q.rows) {
         const long long at = (q.row0 + i) * a.q_stride_tok + head * a.q_stride_head + 8 * j4;
         if (a.q_scale) {
-            f *= a.q_scale[head];
+            raw.scale *= a.q_scale[head];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at + 32 * y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    __nv_fp8_e4m3 c;
-                    c.__x = (__nv_fp8_storage_t)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xff);
-                    x[8 * y + e] = (float)c;
-                }
+                raw.w[y].x = w.x;
+                raw.w[y].y = w.y;
             }
         } else {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at + 32 * y);
-                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            for (int y = 0; y < 4; ++y)
+                raw.w[y] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at + 32 * y);
+        }
+    }
+    return raw;
+}
+
+template <int NG>
+__device__ __forceinline__ void make_queries(const RawQuery &raw, bool fp8, Queries &out) {
+    const int j4 = threadIdx.x & 3;
+    float x[32], top = 0.f, f = raw.scale;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[8 * y + 2 * e] = __uint_as_float(v[e] << 16);
-                    x[8 * y + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
-                }
+    for (int y = 0; y < 4; ++y) {
+        const uint32_t v[4] = {raw.w[y].x, raw.w[y].y, raw.w[y].z, raw.w[y].w};
+        if (fp8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                __nv_fp8_e4m3 c;
+                c.__x = (__nv_fp8_storage_t)((v[e / 4] >> (8 * (e & 3))) & 0xff);
+                x[8 * y + e] = (float)c;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[8 * y + 2 * e] = __uint_as_float(v[e] << 16);
+                x[8 * y + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
             }
         }
     }
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
     __shared__ uint2 s_frag[kSharedQ ? NT : 1][4][2][32];
     __shared__ uint32_t s_sum[kSharedQ ? NT : 1][32];
     __shared__ float s_factor[kSharedQ ? kCols : 1];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r8 = lane >> 2, j4 = lane & 3;
 
     // this block's range of units of work, and the request it starts in: an item is
@@ -348,21 +369,26 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         // -- copies ahead: chunk c0 + warp + i * kWarps into stage i % kStages.  Lane l
         //    looks up the addresses of chunks l, l + 32, ...
         unsigned long long src = 0;
-        const auto look_up = [&](int i) {
-            const int c = c0 + warp + (i + lane) * kWarps;
+        int page = -1, in_page = 0;
+        const auto look_up = [&](int i) {         // the page id of chunk i + lane ...
+            const int c = c0 + warp + (i + lane) * kWarps, pg = c / per_page;
+            page = i + lane < mine && q.len > 0 ? a.block_table[(long long)r * a.max_pages + pg] : -1;
+            in_page = c - pg * per_page;
+        };
+        const auto locate = [&](int i) {          // ... and the chunk's address
             src = (unsigned long long)zero_chunk;
-            if (i + lane < mine && q.len > 0) {
-                const int pg = c / per_page, page = a.block_table[(long long)r * a.max_pages + pg];
-                if (page >= 0 && page < a.c.num_pages)
-                    src = (unsigned long long)(a.c.data + (((long long)page * a.c.h_kv + kv) * per_page + c - pg * per_page) * kBytes);
-                else
-                    set_status(a.status, FP_ERR_DEVICE_BOUNDS);
-            }
+            if (page >= 0 && page < a.c.num_pages)
+                src = (unsigned long long)(a.c.data + (((long long)page * a.c.h_kv + kv) * per_page + in_page) * kBytes);
+            else if (i + lane < mine && q.len > 0)
+                set_status(a.status, FP_ERR_DEVICE_BOUNDS);
         };
         int issued = 0;
         const auto issue = [&]() {
             if (issued < mine) {
-                if (issued && issued % 32 == 0) look_up(issued);
+                if (issued && issued % 32 == 0) {
+                    look_up(issued);
+                    locate(issued);
+                }
                 const unsigned long long from = __shfl_sync(~0u, src, issued & 31);
                 const uint32_t dst = ring_at + (issued % kStages) * kBytes;
                 const char *p = reinterpret_cast<const char *>(from) + lane * 16;
@@ -375,25 +401,33 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         };
         look_up(0);
 
-        // -- queries of this item -----------------------------------------------------
-        Queries qs[kSharedQ ? 1 : NT];
-        if (kSharedQ) {
-            for (int t = warp; t < NT; t += kWarps) {
-                load_queries<NG>(a, q, kv, tile * kCols + t * 8 + r8, qs[0]);
+        // -- queries of this item: their loads go out before the page ids arrive ------
+        constexpr int kOwn = kSharedQ ? (NT + kWarps - 1) / kWarps : NT;       // column octets this warp prepares
+        RawQuery raw[kOwn];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    s_frag[t][y][0][lane] = qs[0].f[y][0];
-                    s_frag[t][y][1][lane] = qs[0].f[y][1];
-                }
-                s_sum[t][lane] = qs[0].sum;
-                if (j4 == 0) s_factor[t * 8 + r8] = qs[0].factor;
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) load_queries<NG>(a, q, kv, tile * kCols + t * 8 + r8, qs[kSharedQ ? 0 : t]);
+        for (int t = 0; t < kOwn; ++t) {
+            const int octet = kSharedQ ? t * kWarps + warp : t;
+            if (octet < NT) raw[t] = fetch_query(a, q, kv, tile * kCols + octet * 8 + r8);
         }
+        locate(0);
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) issue();
+        Queries qs[kOwn];
+#pragma unroll
+        for (int t = 0; t < kOwn; ++t) {
+            const int octet = kSharedQ ? t * kWarps + warp : t;
+            if (octet >= NT) continue;            // whole warps
+            make_queries<NG>(raw[t], a.q_scale != nullptr, qs[t]);
+            if (kSharedQ) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    s_frag[octet][y][0][lane] = qs[t].f[y][0];
+                    s_frag[octet][y][1][lane] = qs[t].f[y][1];
+                }
+                s_sum[octet][lane] = qs[t].sum;
+                if (j4 == 0) s_factor[octet * 8 + r8] = qs[t].factor;
+            }
+        }
         if (kSharedQ) __syncthreads();
         float factor[NT][2];
         int min_keys = 0x7fffffff;
@@ -682,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         if (opens && !closes && tid == 0) {
             const long long last = next - 1;                 // and the block that has it
             const int b = (int)(((last + 1) * blocks - 1) / total);
-            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv * tiles + tile, tiles};
+            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv, tile};
         }
         __syncthreads();
         at = item0 = next;
@@ -699,36 +733,50 @@ constexpr int kJoinWarps = 8;
 template <int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch sc, int blocks) {
     constexpr int kCols = 8 * NT;
-    __shared__ int open[kSm * blocks_per_sm<1>()], count[kJoinWarps];
+    constexpr int kMost = kSm * blocks_per_sm<1>(), kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+    __shared__ Open list[kMost];
+    __shared__ int first[kMost], count[kEach][kJoinWarps];
     __shared__ float4 part_o[kJoinWarps][32];
     __shared__ float part_l[kJoinWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the blocks that left an item open, in the same order for every block of this grid
-    int opens = 0;
-    for (int base = 0; base < blocks; base += kJoinWarps * 32) {
-        const int b = base + threadIdx.x;
-        const bool is = b < blocks && sc.open[b].parts > 0;
-        const unsigned vote = __ballot_sync(~0u, is);
-        if (lane == 0) count[warp] = __popc(vote);
-        __syncthreads();
-        int at = opens + __popc(vote & ((1u << lane) - 1));
-        for (int w = 0; w < kJoinWarps; ++w) {
-            if (w < warp) at += count[w];
-            opens += count[w];
-        }
-        if (is) open[at] = b;
-        __syncthreads();
+    after_previous();
+    // the items that blocks left open, in the same order for every block of this grid
+    Open rec[kEach];
+    unsigned vote[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int b = e * kJoinWarps * 32 + threadIdx.x;
+        rec[e].parts = 0;
+        if (b < blocks) rec[e] = sc.open[b];
     }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        vote[e] = __ballot_sync(~0u, rec[e].parts > 0);
+        if (lane == 0) count[e][warp] = __popc(vote[e]);
+    }
+    __syncthreads();
+    int opens = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        int at = opens + __popc(vote[e] & ((1u << lane) - 1));
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w < warp) at += count[e][w];
+            opens += count[e][w];
+        }
+        if (rec[e].parts > 0) {
+            list[at] = rec[e];
+            first[at] = e * kJoinWarps * 32 + threadIdx.x;
+        }
+    }
+    __syncthreads();
     const bool wide = opens * 8 <= blocks;
     const int step = wide ? 1 : kJoinWarps, w0 = wide ? warp : 0, dw = wide ? kJoinWarps : 1;
     for (int task0 = blockIdx.x * step; task0 < opens * kCols; task0 += gridDim.x * step) {
         const int task = task0 + (wide ? 0 : warp);
         const bool live = task < opens * kCols;
-        const int b = open[live ? task / kCols : 0], col = task % kCols;
-        const Open it = sc.open[b];
-        const int kv = it.item / it.tiles, tile = it.item - kv * it.tiles;
-        const int cc = tile * kCols + col, i = cc / a.g, head = kv * a.g + cc % a.g;
+        const int b = first[live ? task / kCols : 0], col = task % kCols;
+        const Open it = list[live ? task / kCols : 0];
+        const int cc = it.tile * kCols + col, i = cc / a.g, head = it.kv * a.g + cc % a.g;
         float top = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live && i < it.rows) {
@@ -793,18 +841,8 @@ cudaError_t launch(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     if (smem > 46 * 1024)       // above the default limit, with the static part
         e = cudaFuncSetAttribute(attn_kernel<NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    attn_kernel<NG, NT><<<blocks, kThreads, smem, st>>>(a, sc);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks < 2 * kSm ? blocks : 2 * kSm);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<NT>, a, sc, blocks);
+    if ((e = launch_chained(attn_kernel<NG, NT>, blocks, kThreads, smem, st, a, sc)) != cudaSuccess) return e;
+    return launch_chained(join_kernel<NT>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0, st, a, sc, blocks);
 }
 
 template <int NT>

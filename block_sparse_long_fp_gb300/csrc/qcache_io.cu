@@ -67,6 +67,7 @@ __device__ __forceinline__ uint32_t quantise(float x[4], __half *step, __half *l
 
 template <int GROUPS>
 __global__ void __launch_bounds__(kWarps * 32) write_kernel(QCache c, QRows r, int *status) {
+    after_previous();
     const long long unit = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
     if (unit >= (long long)r.rows * c.h_kv) return;
     const int row = (int)(unit / c.h_kv), head = (int)(unit - (long long)row * c.h_kv), l = threadIdx.x & 31;
@@ -120,6 +121,7 @@ __device__ __forceinline__ void store4(void *base, long long elem, const float *
 
 template <int GROUPS>
 __global__ void __launch_bounds__(kWarps * 32) read_kernel(QCache c, QRows r, int *status) {
+    after_previous();
     const long long unit = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
     if (unit >= (long long)r.rows * c.h_kv) return;
     const int row = (int)(unit / c.h_kv), head = (int)(unit - (long long)row * c.h_kv), l = threadIdx.x & 31;
@@ -145,21 +147,19 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(QCache c, QRows r, in
 cudaError_t launch_qcache_write(const QCache &c, const QRows &r, bool, int *status, cudaStream_t st) {
     const unsigned grid = (unsigned)(((long long)r.rows * c.h_kv + kWarps - 1) / kWarps);
     switch (c.groups) {
-        case 4: write_kernel<4><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
-        case 2: write_kernel<2><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
-        default: write_kernel<1><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
+        case 4: return launch_chained(write_kernel<4>, grid, kWarps * 32, 0, st, c, r, status);
+        case 2: return launch_chained(write_kernel<2>, grid, kWarps * 32, 0, st, c, r, status);
+        default: return launch_chained(write_kernel<1>, grid, kWarps * 32, 0, st, c, r, status);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t launch_qcache_read(const QCache &c, const QRows &r, bool, int *status, cudaStream_t st) {
     const unsigned grid = (unsigned)(((long long)r.rows * c.h_kv + kWarps - 1) / kWarps);
     switch (c.groups) {
-        case 4: read_kernel<4><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
-        case 2: read_kernel<2><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
-        default: read_kernel<1><<<grid, kWarps * 32, 0, st>>>(c, r, status); break;
+        case 4: return launch_chained(read_kernel<4>, grid, kWarps * 32, 0, st, c, r, status);
+        case 2: return launch_chained(read_kernel<2>, grid, kWarps * 32, 0, st, c, r, status);
+        default: return launch_chained(read_kernel<1>, grid, kWarps * 32, 0, st, c, r, status);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace fp

@@ -343,15 +343,6 @@ def _need(t, name: str, dtypes, device: int, ndim: int, contiguous: bool = True)
                         f"on {t.device}")
 
 
-def _raw_stream(index: int) -> int:
-    """The current stream's handle on a device; the short way, where torch has it, saves a microsecond a call."""
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(index)
-    except AttributeError:
-        return torch.cuda.current_stream(index).cuda_stream
-
-
 class _OnDevice:
     """What PageTables and QCache share: the status header, and calls on their
     device's current stream whatever device is current."""
@@ -360,34 +351,53 @@ class _OnDevice:
         import torch
         if device.type != "cuda":
             raise FprefillError(FP_ERR_INVALID, f"a CUDA tensor is wanted, got {device}")
-        lib()
+        self._lib = lib()
+        self._torch = torch
         self.device = device
         self._index = device.index
         self._ws = torch.zeros(FP_WS_HEADER_BYTES // 4, dtype=torch.int32, device=device)
         self._ws_ptr = self._ws.data_ptr()
+        self._bf16, self._fp8 = (torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn)
+        self._int32, self._fp32 = torch.int32, torch.float32
+        # the current stream's handle: the short way, where torch has it, saves a microsecond a call
+        self._stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                               lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def _call(self, what: str, *args):
-        """The entry point on the current stream of this object's device."""
-        import torch
-        f = getattr(_lib, what)
-        if torch.cuda.current_device() == self._index:
-            s = f(*args, _raw_stream(self._index))
+    def _call(self, f, what: str, *args):
+        """The entry point f on the current stream of this object's device."""
+        if self._torch.cuda.current_device() == self._index:
+            s = f(*args, self._stream(self._index))
         else:
-            with torch.cuda.device(self._index):
-                s = f(*args, _raw_stream(self._index))
+            with self._torch.cuda.device(self._index):
+                s = f(*args, self._stream(self._index))
         if s != FP_OK:
             raise FprefillError(s, what)
 
+    def _vector(self, t, name: str, n: int) -> int:
+        """The address of an int32 vector of n entries."""
+        if t.dtype is self._int32 and t.shape == (n,) and t.get_device() == self._index and t.is_contiguous():
+            return t.data_ptr()
+        _need(t, name, (self._int32,), self._index, 1)
+        raise FprefillError(FP_ERR_INVALID, f"{name}: {n} entries wanted, got {t.shape[0]}")
+
+    def _scales(self, t, name: str, n: int) -> int:
+        """The address of n fp32 scales."""
+        if t is None:
+            raise FprefillError(FP_ERR_INVALID, f"{name} is missing")
+        _need(t, name, (self._fp32,), self._index, 1)
+        if t.shape[0] != n:
+            raise FprefillError(FP_ERR_INVALID, f"{name}: {n} entries wanted, got {t.shape[0]}")
+        return t.data_ptr()
+
     def device_status(self) -> int:
         """Waits for the current stream; what its kernels found wrong in device data (FP_OK: nothing)."""
-        import torch
         v = c_int(0)
-        with torch.cuda.device(self.device):
+        with self._torch.cuda.device(self.device):
             _check(lib().fp_device_status(self._ws_ptr, _stream_handle(), ctypes.byref(v)), "fp_device_status")
         return v.value
 
     def reset_status(self):
-        self._call("fp_reset_status", self._ws_ptr)
+        self._call(self._lib.fp_reset_status, "fp_reset_status", self._ws_ptr)
 
 
 class PageTables(_OnDevice):
@@ -419,27 +429,20 @@ class PageTables(_OnDevice):
         t.block_table, t.cu_seqlens_q = _ptr(block_table), _ptr(self.cu_seqlens_q)
         t.seqlens_k, t.positions = _ptr(self.seqlens_k), _ptr(self.positions)
         t.slots, t.free_next = _ptr(self.slots), _ptr(self.free_head)
-        self._int32 = (torch.int32,)
+        self._shape = (t.batch, t.page_size, t.num_pages, t.max_pages_per_seq)
+        self._out = (t.block_table, t.cu_seqlens_q, t.seqlens_k, t.positions, t.slots, t.free_next)
+        self._f = self._lib.fp_page_tables
 
     def step(self, seqlens, new_lens, free_pages, free_head=None):
         """One step (returns this object).  seqlens, new_lens: int32 [batch];
         free_pages: int32, used from entry free_head (int32 [1], 0 when None)
         on.  Passing this object's own seqlens_k and free_head advances both in
         place."""
-        t, dev, kinds = self._t, self._index, self._int32
-        _need(seqlens, "seqlens", kinds, dev, 1)
-        _need(new_lens, "new_lens", kinds, dev, 1)
-        _need(free_pages, "free_pages", kinds, dev, 1)
-        if seqlens.shape[0] != t.batch or new_lens.shape[0] != t.batch:
-            raise FprefillError(FP_ERR_INVALID, f"seqlens, new_lens: {t.batch} entries wanted")
-        if free_head is not None:
-            _need(free_head, "free_head", kinds, dev, 1)
-            if free_head.shape[0] != 1:
-                raise FprefillError(FP_ERR_INVALID, "free_head: one entry wanted")
-        t = FpTables(t.batch, t.page_size, t.num_pages, t.max_pages_per_seq, free_pages.shape[0], t.capacity,
-                     seqlens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), _ptr(free_head), t.block_table,
-                     t.cu_seqlens_q, t.seqlens_k, t.positions, t.slots, t.free_next)
-        self._call("fp_page_tables", t, self._ws_ptr, FP_WS_HEADER_BYTES)
+        batch, free = self._shape[0], free_pages.shape[0]
+        t = FpTables(*self._shape, free, self.capacity, self._vector(seqlens, "seqlens", batch),
+                     self._vector(new_lens, "new_lens", batch), self._vector(free_pages, "free_pages", free),
+                     0 if free_head is None else self._vector(free_head, "free_head", 1), *self._out)
+        self._call(self._f, "fp_page_tables", t, self._ws_ptr, FP_WS_HEADER_BYTES)
         return self
 
 
@@ -466,8 +469,8 @@ class QCache(_OnDevice):
                                 f"wanted, got {tuple(data.shape)}")
         self.data, self.h_kv, self.page_size, self.group = data, c.h_kv, c.page_size, c.group
         self._scratch, self._scratch_bytes = {}, {}
-        self._bf16, self._fp8 = (torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn)
-        self._int32, self._fp32 = (torch.int32,), (torch.float32,)
+        L = self._lib
+        self._f = (L.fp_qcache_write, L.fp_qcache_read, L.fp_qcache_attn)
 
     @staticmethod
     def chunk_bytes(group: int = 32) -> int:
@@ -486,49 +489,45 @@ class QCache(_OnDevice):
         dev, h = self._index, self.h_kv
         fp8 = k_scale is not None or v_scale is not None
         kinds = self._fp8 if fp8 else self._bf16
-        _need(k, "k", kinds, dev, 3, False)
-        _need(v, "v", kinds, dev, 3, False)
-        _need(slots, "slots", self._int32, dev, 1)
-        if k.shape != v.shape or k.stride() != v.stride() or k.shape[1:] != (h, 128) or k.stride(2) != 1:
+        shape, strides = k.shape, k.stride()
+        if not (len(shape) == 3 and v.shape == shape and v.stride() == strides and shape[1] == h and shape[2] == 128 and
+                strides[2] == 1 and k.dtype in kinds and v.dtype in kinds and k.get_device() == dev and
+                v.get_device() == dev):
+            _need(k, "k", kinds, dev, 3, False)
+            _need(v, "v", kinds, dev, 3, False)
             raise FprefillError(FP_ERR_INVALID, f"k, v: [rows, {h}, 128] with like strides and contiguous dims wanted, "
-                                f"got {tuple(k.shape)} {k.stride()} and {tuple(v.shape)} {v.stride()}")
-        if fp8:
-            for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
-                if x is None:
-                    raise FprefillError(FP_ERR_INVALID, f"{name} is missing")
-                _need(x, name, self._fp32, dev, 1)
-                if x.shape[0] != h:
-                    raise FprefillError(FP_ERR_INVALID, f"{name}: {h} entries wanted")
-        rows, n = k.shape[0], slots.shape[0]
-        if out_slots is not None:
-            _need(out_slots, "out_slots", self._int32, dev, 1)
-        if (out_slots.shape[0] if out_slots is not None else rows) != n:
-            raise FprefillError(FP_ERR_INVALID, "slots: one for each row (and each of out_slots) wanted")
+                                f"got {tuple(shape)} {strides} and {tuple(v.shape)} {v.stride()}")
+        rows = shape[0]
+        n = rows if out_slots is None else slots.shape[0]
+        slots_at = self._vector(slots, "slots", n)
+        out_at = 0 if out_slots is None else self._vector(out_slots, "out_slots", n)
         # a single row (or head) may carry any stride: the packed one stands for it
-        stride_head = k.stride(1) if h > 1 else 128
-        stride_tok = k.stride(0) if rows > 1 else h * stride_head
-        return FpQCacheRows(n, FP_E4M3 if fp8 else FP_BF16, k.data_ptr(), v.data_ptr(), stride_tok, stride_head,
-                            slots.data_ptr(), _ptr(out_slots), rows, _ptr(k_scale), _ptr(v_scale))
+        stride_head = strides[1] if h > 1 else 128
+        return FpQCacheRows(n, FP_E4M3 if fp8 else FP_BF16, k.data_ptr(), v.data_ptr(),
+                            strides[0] if rows > 1 else h * stride_head, stride_head, slots_at, out_at, rows,
+                            self._scales(k_scale, "k_scale", h) if fp8 else 0,
+                            self._scales(v_scale, "v_scale", h) if fp8 else 0)
 
     def write(self, k, v, slots, k_scale=None, v_scale=None):
         """Quantise rows of k and v (bf16 [rows, h_kv, 128], or e4m3 with one
         scale per head) into `slots` (int32 [rows]; -1: none)."""
-        self._call("fp_qcache_write", self._c, self._rows(k, v, slots, k_scale, v_scale), self._ws_ptr, FP_WS_HEADER_BYTES)
+        self._call(self._f[0], "fp_qcache_write", self._c, self._rows(k, v, slots, k_scale, v_scale), self._ws_ptr, FP_WS_HEADER_BYTES)
 
     def read(self, slots, k_out=None, v_out=None, out_slots=None, k_scale=None, v_scale=None):
         """Bring the tokens at `slots` back into k_out and v_out (bf16 [.., h_kv,
         128], or e4m3 with one scale per head): row i, or row out_slots[i].
         Without k_out and v_out, new bf16 rows, zero where a slot is -1.  A
         paged cache is passed as its rows: k_cache.flatten(0, 1)."""
-        import torch
         if (k_out is None) != (v_out is None):
             raise FprefillError(FP_ERR_INVALID, "k_out and v_out come together")
         if k_out is None:
             if out_slots is not None or k_scale is not None:
                 raise FprefillError(FP_ERR_INVALID, "out_slots and e4m3 want k_out and v_out")
+            torch = self._torch
             k_out, v_out = (torch.zeros((slots.shape[0], self.h_kv, 128), dtype=torch.bfloat16, device=self.device)
                             for _ in range(2))
-        self._call("fp_qcache_read", self._c, self._rows(k_out, v_out, slots, k_scale, v_scale, out_slots), self._ws_ptr, FP_WS_HEADER_BYTES)
+        self._call(self._f[1], "fp_qcache_read", self._c, self._rows(k_out, v_out, slots, k_scale, v_scale, out_slots),
+                   self._ws_ptr, FP_WS_HEADER_BYTES)
         return k_out, v_out
 
     def attn(self, q, block_table, seqlens_k, cu_seqlens_q=None, max_q=None, out=None, lse=None, want_lse=True,
@@ -541,69 +540,67 @@ class QCache(_OnDevice):
         queries' own tokens included).  Request r owns rows cu_seqlens_q[r] ..
         cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
         cu_seqlens_q, max_q rows each (total_q / batch by default)."""
-        import torch
-        dev = self._index
-        _need(q, "q", self._bf16 if q_scale is None else self._fp8, dev, 3, False)
-        _need(block_table, "block_table", self._int32, dev, 2)
-        _need(seqlens_k, "seqlens_k", self._int32, dev, 1)
-        total_q, h_q, d = q.shape
+        torch, dev, h_kv = self._torch, self._index, self.h_kv
+        shape, strides = q.shape, q.stride()
+        kinds = self._bf16 if q_scale is None else self._fp8
+        if not (len(shape) == 3 and q.dtype in kinds and q.get_device() == dev and strides[2] == 1 and shape[2] == 128 and
+                shape[1] % h_kv == 0):
+            _need(q, "q", kinds, dev, 3, False)
+            raise FprefillError(FP_ERR_INVALID, f"q: [rows, a multiple of {h_kv}, 128] with contiguous dims wanted, "
+                                f"got {tuple(shape)} {strides}")
+        total_q, h_q, _ = shape
         batch = seqlens_k.shape[0]
-        if d != 128 or q.stride(2) != 1 or h_q % self.h_kv:
-            raise FprefillError(FP_ERR_INVALID, f"q: [rows, a multiple of {self.h_kv}, 128] with contiguous dims wanted, "
-                                f"got {tuple(q.shape)} {q.stride()}")
-        if block_table.shape[0] != batch:
-            raise FprefillError(FP_ERR_INVALID, "block_table, seqlens_k: as many rows as lengths wanted")
-        if cu_seqlens_q is not None:
-            _need(cu_seqlens_q, "cu_seqlens_q", self._int32, dev, 1)
-            if cu_seqlens_q.shape[0] != batch + 1:
-                raise FprefillError(FP_ERR_INVALID, f"cu_seqlens_q: {batch + 1} entries wanted")
-        if q_scale is not None:
-            _need(q_scale, "q_scale", self._fp32, dev, 1)
-            if q_scale.shape[0] != h_q:
-                raise FprefillError(FP_ERR_INVALID, f"q_scale: {h_q} entries wanted")
+        seqlens_at = self._vector(seqlens_k, "seqlens_k", batch)
+        if not (block_table.dtype is self._int32 and block_table.dim() == 2 and block_table.shape[0] == batch and
+                block_table.get_device() == dev and block_table.is_contiguous()):
+            _need(block_table, "block_table", (self._int32,), dev, 2)
+            raise FprefillError(FP_ERR_INVALID, f"block_table: {batch} rows wanted, one for each length")
+        width = block_table.shape[1]
+        cu_at = 0 if cu_seqlens_q is None else self._vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
         if max_q is None:
             max_q = max(1, total_q // batch if batch and cu_seqlens_q is None else total_q)
-        stride_head = q.stride(1) if h_q > 1 else 128
+        stride_head = strides[1] if h_q > 1 else 128
         Q = FpQCacheQuery(batch, h_q, total_q, max_q, FP_BF16 if q_scale is None else FP_E4M3, q.data_ptr(),
-                          q.stride(0) if total_q > 1 else h_q * stride_head, stride_head, _ptr(q_scale),
-                          _ptr(cu_seqlens_q), seqlens_k.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                          softmax_scale)
+                          strides[0] if total_q > 1 else h_q * stride_head, stride_head,
+                          0 if q_scale is None else self._scales(q_scale, "q_scale", h_q), cu_at, seqlens_at,
+                          block_table.data_ptr(), width, softmax_scale)
         if out is None:
             out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=self.device)
-        else:
+        elif out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
             _need(out, "out", self._bf16, dev, 3)
-            if out.shape != q.shape:
-                raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
-        if lse is None and want_lse:
-            lse = torch.empty((h_q, total_q), dtype=torch.float32, device=self.device)
-        elif lse is not None:
-            _need(lse, "lse", self._fp32, dev, 2)
+            raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
+        if lse is not None:
+            _need(lse, "lse", (self._fp32,), dev, 2)
             if lse.shape != (h_q, total_q):
                 raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
-        shape = (batch, h_q, total_q, max_q, cu_seqlens_q is None, block_table.shape[1])
-        n = self._scratch_bytes.get(shape)
+        elif want_lse:
+            lse = torch.empty((h_q, total_q), dtype=self._fp32, device=self.device)
+        key = (batch, h_q, total_q, max_q, cu_at == 0, width)
+        n = self._scratch_bytes.get(key)
         if n is None:
-            n = self._scratch_bytes[shape] = int(_lib.fp_qcache_attn_scratch_bytes(self._c, Q))
-        self._call("fp_qcache_attn", self._c, Q, out.data_ptr(), _ptr(lse), self._scratch_of(n), n, self._ws_ptr,
-                   FP_WS_HEADER_BYTES)
+            n = self._scratch_bytes[key] = int(self._lib.fp_qcache_attn_scratch_bytes(self._c, Q))
+        args = (self._c, Q, out.data_ptr(), 0 if lse is None else lse.data_ptr())
+        if torch.cuda.current_device() == dev:
+            self._attn(args, n)
+        else:
+            with torch.cuda.device(dev):
+                self._attn(args, n)
         return out, lse
 
-    def _scratch_of(self, nbytes: int) -> int:
-        """Scratch of the current stream: calls on two streams share none, and a
-        captured call has its own, out of the graph's memory."""
-        import torch
-        if torch.cuda.current_device() == self._index:
-            capturing = torch.cuda.is_current_stream_capturing()
-        else:
-            with torch.cuda.device(self._index):
-                capturing = torch.cuda.is_current_stream_capturing()
-        if capturing:
-            return torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device).data_ptr()
-        stream = _raw_stream(self._index)
-        old = self._scratch.get(stream)
-        if old is None or old.numel() < nbytes:
-            old = self._scratch[stream] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
-        return old.data_ptr()
+    def _attn(self, args, n: int):
+        """fp_qcache_attn with n bytes of scratch of the current stream: calls on
+        two streams share none, and a captured call has its own, out of the
+        graph's memory."""
+        torch, stream = self._torch, self._stream(self._index)
+        capturing = torch.cuda.is_current_stream_capturing()
+        scratch = None if capturing else self._scratch.get(stream)
+        if scratch is None or scratch.numel() < n:
+            scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
+            if not capturing:
+                self._scratch[stream] = scratch
+        s = self._f[2](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
+        if s != FP_OK:
+            raise FprefillError(s, "fp_qcache_attn")
 
 
 def layer_from_case(case, device="cuda", params: FpParams | None = None, v_layout: int = 0):
