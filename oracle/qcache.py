@@ -56,20 +56,25 @@ def _places(t: int, group: int):
 
 def write(cache: np.ndarray, page: int, group: int, slots, k, v):
     """Quantise rows k, v [rows, h_kv, 128] into the cache (uint8 [pages, h_kv, page / 16, bytes]), in place."""
+    slots, h, n = np.asarray(slots, np.int64), cache.shape[1], D // group
     parts = [quantise(k, group), quantise(v, group)]
-    for i, slot in enumerate(slots):
-        if not 0 <= slot < cache.shape[0] * page:
+    flat = cache.reshape(cache.shape[0], h, page // 16, -1)
+    for t in range(16):
+        rows = np.nonzero((slots % 16 == t) & (slots >= 0) & (slots < cache.shape[0] * page))[0]
+        if not len(rows):
             continue
-        t = slot % 16
+        at = (slots[rows] // page, slice(None), slots[rows] % page // 16)
+        chunk = flat[at]                                         # [rows, h, bytes]
         kp, vp, ks, km, vs, vm = _places(t, group)
-        for h in range(cache.shape[1]):
-            chunk = cache[slot // page, h, slot % page // 16]
-            for (code, step, low), at, sp, mp in zip(parts, (kp, vp), (ks, vs), (km, vm)):
-                for dim, (b, nib) in enumerate(at):
-                    chunk[b] = (chunk[b] & (0xF0 if nib == 0 else 0x0F)) | (int(code[i, h, dim]) << (4 * nib))
-                for g in range(D // group):
-                    chunk[sp[g]:sp[g] + 2] = np.frombuffer(step[i, h, g].tobytes(), np.uint8)
-                    chunk[mp[g]:mp[g] + 2] = np.frombuffer(low[i, h, g].tobytes(), np.uint8)
+        for (code, step, low), places, sp, mp in zip(parts, (kp, vp), (ks, vs), (km, vm)):
+            b = np.array([x for x, _ in places]).reshape(-1, 2)
+            assert np.all(b[:, 0] == b[:, 1])                    # dims 2 i and 2 i + 1 share a byte
+            c = code[rows]
+            chunk[..., b[:, 0]] = c[..., 0::2] | (c[..., 1::2] << 4)
+            for start, value in ((sp, step), (mp, low)):
+                at16 = np.array([[x, x + 1] for x in start]).ravel()
+                chunk[..., at16] = np.ascontiguousarray(value[rows]).view(np.uint8).reshape(len(rows), h, 2 * n)
+        flat[at] = chunk
 
 
 def read(cache: np.ndarray, page: int, group: int, slots):

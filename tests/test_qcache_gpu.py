@@ -154,6 +154,96 @@ def test_write_of_whole_chunks_from_strided_rows(fp, group):
     assert torch.equal(c.data, d.data)
 
 
+def mixed_slots(seed, rows, pages, page):
+    """Slots of many sequences laid end to end: prompts that start anywhere in a
+    page, single tokens, padding, whole chunks that begin at any row."""
+    rng = np.random.default_rng(seed)
+    order = list(rng.permutation(pages))
+    out = []
+    while len(out) < rows:
+        kind = rng.integers(0, 4)
+        n = int(rng.integers(1, 4 if kind == 0 else 6 * page if kind == 1 else 40))
+        if kind == 2:
+            out += [-1] * n
+            continue
+        start = int(rng.integers(0, page)) if kind != 3 else 0
+        need = -(-(start + n) // page)
+        if need > len(order):
+            out += [-1] * (rows - len(out))
+            break
+        mine = [order.pop() for _ in range(need)]
+        out += [int(mine[p // page]) * page + p % page for p in range(start, start + n)]
+    return np.array(out[:rows])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,h,page,seed", [(4103, 4, 16, 1), (2401, 7, 64, 2), (16400, 1, 128, 3), (2048, 8, 32, 4)])
+def test_many_rows(fp, rows, h, page, seed, group, dtype):
+    """Enough rows for the kernels that take 16 at a time, bit for bit: written,
+    what no row names left alone, read back to mapped and to plain rows."""
+    import torch
+    pages = rows // page + 40
+    slots = mixed_slots(seed, rows, pages, page) if seed != 4 else np.arange(rows) + 5 * page   # whole chunks in order
+    data = np.random.default_rng(seed).integers(0, 256, (pages, h, page // 16, oq.chunk_bytes(group)), dtype=np.uint8)
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    x, x32, ks = source(seed, rows, 3 * h, dtype)
+    k, v = x[:, :h], x[:, 2 * h:]
+    scales = (None, None) if ks is None else (ks[:h].contiguous(), ks[2 * h:].contiguous())
+    c.write(k, v, i32(slots), *scales)
+    oq.write(data, page, group, slots, x32[:, :h], x32[:, 2 * h:])
+    assert np.array_equal(c.data.cpu().numpy(), data)
+    to = np.random.default_rng(seed + 1).permutation(rows + 7)[:rows]
+    for target in (None, to):
+        n = rows if target is None else rows + 7
+        out = [torch.full((n, h, 128), 3, dtype=x.dtype, device="cuda") for _ in range(2)]
+        want = [o.cpu().clone() for o in out]
+        c.read(i32(slots), *out, out_slots=None if target is None else i32(target), k_scale=scales[0], v_scale=scales[1])
+        live = slots >= 0
+        at = torch.from_numpy((np.arange(rows) if target is None else target)[live])
+        for w, val, s in zip(want, oq.read(data, page, group, slots), scales):
+            y = torch.from_numpy(val).float()
+            y = y.bfloat16() if s is None else (y / s.cpu().view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            w[at] = y[torch.from_numpy(live)]
+        for o, w in zip(out, want):
+            assert torch.equal(o.cpu(), w)
+    assert c.device_status() == 0
+    bad = slots.copy()
+    bad[rows // 2], bad[3] = pages * page, -9
+    c.write(k, v, i32(bad), *scales)
+    assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    c.reset_status()
+    c.read(i32(bad), *out, k_scale=scales[0], v_scale=scales[1], out_slots=i32(np.arange(rows)))
+    assert c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    assert np.array_equal(c.data.cpu().numpy(), data)        # the same rows where they were, nothing elsewhere
+
+
+def test_many_rows_of_special_values(fp):
+    """NaN, infinities, constants, ranges below the f16 steps and beyond fp16, in the 16-row kernels."""
+    import torch
+    rng = np.random.default_rng(3)
+    rows = 16400
+    x = rng.normal(size=(rows, 1, 128)).astype(np.float32) * 10.0 ** rng.integers(-9, 7, (rows, 1, 1))
+    x += 10.0 ** rng.integers(-3, 4, (rows, 1, 1)) * rng.integers(-1, 2, (rows, 1, 1))
+    x[::7, 0, 5] = np.nan
+    x[::11, 0, 40] = np.inf
+    x[::13, 0, 100] = -np.inf
+    x[::17] = 2.5
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    slots = np.arange(rows)
+    for group in (32, 64, 128):
+        data = np.zeros((-(-rows // 64), 1, 4, oq.chunk_bytes(group)), np.uint8)
+        c = fp.QCache(torch.from_numpy(data).cuda(), 64, group)
+        c.write(x.cuda(), x.cuda(), i32(slots))
+        oq.write(data, 64, group, slots, x.float().numpy(), x.float().numpy())
+        got = c.data.cpu().numpy()
+        for a, b in zip(oq.read(got, 64, group, slots), oq.read(data, 64, group, slots)):
+            assert np.array_equal(a, b, equal_nan=True)
+        k, v = c.read(i32(slots))
+        want = torch.from_numpy(oq.read(data, 64, group, slots)[0]).float().bfloat16()
+        assert torch.equal(torch.nan_to_num(k.cpu().float(), 7.0), torch.nan_to_num(want.float(), 7.0))
+
+
 def test_write_of_special_values(fp):
     import torch
     x = torch.randn((4, 1, 128))
