@@ -40,8 +40,14 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSm = 152;
-constexpr int kMinUnits = 2 * kWarps;        // least work worth a thread block
-constexpr int kItemUnits = 8;                // what starting and ending an item costs, in chunks
+constexpr int kMinChunks = 2 * kWarps;       // least work worth a thread block
+// Work is cut in units.  What starting and ending an item costs, in chunks, and what a
+// chunk costs by the octets of columns in use (extracting the codes is most of it; with
+// one octet at most there is nothing to tell apart).
+template <int NT>
+constexpr int item_chunks() { return NT == 1 ? 16 : NT == 2 ? 20 : 32; }
+template <int NT>
+__device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 + octets; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's result in shared memory
@@ -60,9 +66,9 @@ struct Scratch {
     float *o;                                // [blocks][2][cols][kHeadDim]
 };
 
-// Blocks per SM (their registers: 128, 168 and 255 a thread) and copies ahead.
-template <int NT>
-constexpr int blocks_per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
+// Blocks per SM (by their registers: 128, 168 and 255 a thread for 4, 3 and 2) and copies ahead.
+template <int NG, int NT>
+constexpr int blocks_per_sm() { return NT == 1 ? 4 : NT == 2 ? (NG == 4 ? 3 : 4) : 2; }
 template <int NT>
 constexpr int stages() { return NT == 4 ? 8 : 4; }
 
@@ -281,10 +287,10 @@ __device__ __forceinline__ void load_halves(const unsigned char *p, float out[NG
 }
 
 template <int NG, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAttn a, Scratch sc) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel(QAttn a, Scratch sc) {
     constexpr int kCols = 8 * NT, kBytes = 2 * kCodeBytes + 128 * NG, kStages = stages<NT>();
-    constexpr int kRing = kStages * kBytes;
-    constexpr bool kSharedQ = NT == 4;            // queries' fragments in shared memory instead of registers
+    constexpr int kRing = kStages * kBytes, kItem = item_chunks<NT>();
+    constexpr bool kSharedQ = NT > 1;          // queries' fragments in shared memory instead of registers
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ long long warp_sums[kWarps];
     __shared__ long long s_at;
@@ -297,10 +303,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
     after_previous();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31, r8 = lane >> 2, j4 = lane & 3;
 
-    // this block's range of units of work, and the request it starts in: an item is
-    // kItemUnits for its start and end, then a unit for each chunk
+    // this block's range of units, and the request it starts in: an item is its start and
+    // end, then its chunks
+    const auto octets_of = [&](const Request &q, int tile) { return (min(kCols, q.rows * a.g - tile * kCols) + 7) / 8; };
     const auto units = [&](const Request &q) {
-        return (long long)a.c.h_kv * tiles_of(a, q, kCols) * (kItemUnits + chunks_of(q));
+        const int tiles = tiles_of(a, q, kCols);
+        if (tiles == 0) return 0ll;
+        return (long long)a.c.h_kv * (kItem + chunks_of(q)) *
+               ((tiles - 1) * chunk_units<NT>(NT) + chunk_units<NT>(octets_of(q, tiles - 1)));
     };
     Request q = {0, 0, 0, 0};
     if (tid < a.batch) q = request_of(a, tid);
@@ -312,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         block_scan(base + tid < a.batch ? units(request_of(a, base + tid)) : 0, &all, warp_sums);
         total += all;
     }
-    const long long want = (total + kMinUnits - 1) / kMinUnits;
-    const int blocks = (int)(want < gridDim.x ? want : gridDim.x);
+    const long long want = total / (kMinChunks * chunk_units<NT>(NT)) + 1;
+    const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
     const long long first = (long long)blockIdx.x * total / blocks, end = (long long)(blockIdx.x + 1) * total / blocks;
@@ -340,28 +350,39 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
     long long item0 = s_at;                       // first unit of the current item
     q = s_q;
     int tiles = tiles_of(a, q, kCols), chunks = chunks_of(q);
-    int item = (int)((first - item0) / (kItemUnits + chunks));   // kv head and tile
-    item0 += (long long)item * (kItemUnits + chunks);
-
+    int kv, tile;                                 // of the current item
+    {
+        const long long full = (long long)(kItem + chunks) * chunk_units<NT>(NT);
+        const long long head =
+            (tiles - 1) * full + (long long)(kItem + chunks) * chunk_units<NT>(octets_of(q, tiles - 1));
+        kv = (int)((first - item0) / head);
+        item0 += kv * head;
+        tile = min((int)((first - item0) / full), tiles - 1);
+        item0 += tile * full;
+    }
     unsigned char *ring = smem + warp * kRing;
     const uint32_t ring_at = smem_addr(ring) + lane * 16;
     const int per_page = a.c.page_size / kChunk;
 
     for (long long at = first; at < end;) {
-        while (item >= a.c.h_kv * tiles) {        // the next request that has rows
+        if (tile == tiles) {
+            tile = 0;
+            ++kv;
+        }
+        while (kv >= a.c.h_kv || tiles == 0) {    // the next request that has rows
             if (++r >= a.batch) return;           // lengths that changed under the kernel
             q = request_of(a, r);
             tiles = tiles_of(a, q, kCols);
             chunks = chunks_of(q);
-            item = 0;
+            kv = tile = 0;
         }
-        const int kv = item / tiles, tile = item - kv * tiles;
-        const long long next = item0 + kItemUnits + chunks;
-        const int c0 = (int)max(0ll, at - item0 - kItemUnits);
-        const int c1 = (int)max(0ll, min(end, next) - item0 - kItemUnits);
+        const int octets = octets_of(q, tile), weight = chunk_units<NT>(octets);
+        const long long next = item0 + (long long)(kItem + chunks) * weight;
+        const int c0 = max(0, (int)((at - item0) / weight) - kItem);
+        const int c1 = max(0, (int)((min(end, next) - item0) / weight) - kItem);
         if (c1 <= c0) {                           // the range ends inside the item's start
             at = item0 = next;
-            ++item;
+            ++tile;
             continue;
         }
         const int mine = c1 - c0 > warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
@@ -462,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             sum[t][0] = sum[t][1] = 0.f;
         }
 
-        const auto step = [&](int i, auto edge) {
+        // L: octets of columns in use (the others of the tile are left out)
+        const auto step = [&](int i, auto edge, auto octets) {
             constexpr bool kEdge = decltype(edge)::value;
+            constexpr int L = decltype(octets)::value;
             copies_wait<kStages - 2>();
             __syncwarp();
             issue();
@@ -471,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             const int t0 = (c0 + warp + i * kWarps) * kChunk;
 
             // logits
-            float x[NT][4];
+            float x[L][4];
             {
                 const uint4 ka = *reinterpret_cast<const uint4 *>(chunk + lane * 16);
                 const uint4 kb = *reinterpret_cast<const uint4 *>(chunk + 512 + lane * 16);
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     m1 = m[(r8 + 8) * NG + j4] * 0x10001u;
                 }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+                for (int t = 0; t < L; ++t) {
                     float c[4];
                     mma8_zero(c, m0, m1, kSharedQ ? s_sum[t][lane] : qs[kSharedQ ? 0 : t].sum);
 #pragma unroll
@@ -493,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    float acc[NT][4];
+                    float acc[L][4];
 #pragma unroll
                     for (int y = g * 4 / NG; y < (g + 1) * 4 / NG; ++y) {
                         uint32_t wa = y == 0 ? ka.x : y == 1 ? ka.y : y == 2 ? ka.z : ka.w;
@@ -501,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) {
+                            for (int t = 0; t < L; ++t) {
                                 const uint2 f = kSharedQ ? s_frag[t][y][u][lane] : qs[kSharedQ ? 0 : t].f[y][u];
                                 if (y == g * 4 / NG && u == 0)
                                     mma16_zero(acc[t], wa & 0x000f000fu, wb & 0x000f000fu, wa & 0x00f000f0u,
@@ -515,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
+                    for (int t = 0; t < L; ++t) {
                         x[t][0] = fmaf(s0[g], acc[t][0], x[t][0]);
                         x[t][1] = fmaf(s0[g], acc[t][1], x[t][1]);
                         x[t][2] = fmaf(s1[g], acc[t][2], x[t][2]);
@@ -556,20 +579,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             for (int g = 0; g < NG; ++g) any_step |= vs[g][0] | vs[g][1];
 
             // weights
-            float y[NT][4], top = -INFINITY;
+            float y[L][4], top = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[t][e] = fmaf(x[t][e], factor[t][e & 1], -base[t][e & 1]);
             if (kEdge) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int t = 0; t < L; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (t0 + r8 + 4 * (e & 2) >= keys_of(t, e & 1)) y[t][e] = -INFINITY;
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, y[t][e]);
             // a maximum to follow, or steps of 2 and more (bit 14 of an fp16 that is >= 0)
@@ -587,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 }
                 if (koff2 != koff || __any_sync(~0u, top > koff + 4.f)) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int t = 0; t < L; ++t)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const bool out0 = y[t][c] == -INFINITY, out1 = y[t][c + 2] == -INFINITY;
@@ -612,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     koff = koff2;
                 }
             }
-            uint32_t p[NT][2];
+            uint32_t p[L][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
+            for (int t = 0; t < L; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[t][e] = fast_exp2(y[t][e]);
                 sum[t][0] += y[t][0] + y[t][2];
@@ -629,9 +652,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             const uint4 vb = *reinterpret_cast<const uint4 *>(chunk + kCodeBytes + 512 + lane * 16);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t ps[NT][2];
+                uint32_t ps[L][2];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
+                for (int t = 0; t < L; ++t) {
                     ps[t][0] = mul_half2(p[t][0], vs[g][0]);
                     ps[t][1] = mul_half2(p[t][1], vs[g][1]);
                 }
@@ -643,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
+                        for (int t = 0; t < L; ++t)
                             mma16(o[t][2 * m + u], wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu,
                                   wb & 0x00f000f0u, ps[t][0], ps[t][1]);
                         wa >>= 8;
@@ -654,9 +677,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         };
         // chunks that every column sees whole, then those at the causal edge or the end
         const int whole = min_keys / kChunk - c0 > warp ? (min_keys / kChunk - c0 - warp + kWarps - 1) / kWarps : 0;
-        int i = 0;
-        for (; i < min(whole, mine); ++i) step(i, std::false_type());
-        for (; i < mine; ++i) step(i, std::true_type());
+        const auto walk = [&](auto octets) {
+            int i = 0;
+            for (; i < min(whole, mine); ++i) step(i, std::false_type(), octets);
+            for (; i < mine; ++i) step(i, std::true_type(), octets);
+        };
+        if (NT == 1 || octets == 1)
+            walk(std::integral_constant<int, 1>());
+        else if (NT == 2 || octets == 2)
+            walk(std::integral_constant<int, NT < 2 ? NT : 2>());
+        else if (octets == 3)
+            walk(std::integral_constant<int, NT < 3 ? NT : 3>());
+        else
+            walk(std::integral_constant<int, NT>());
         copies_wait<0>();
         __syncwarp();
 
@@ -720,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         }
         __syncthreads();
         at = item0 = next;
-        ++item;
+        ++tile;
     }
 }
 
@@ -733,7 +766,7 @@ constexpr int kJoinWarps = 8;
 template <int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch sc, int blocks) {
     constexpr int kCols = 8 * NT;
-    constexpr int kMost = kSm * blocks_per_sm<1>(), kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+    constexpr int kMost = kSm * 4, kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
     __shared__ Open list[kMost];
     __shared__ int first[kMost], count[kEach][kJoinWarps];
     __shared__ float4 part_o[kJoinWarps][32];
@@ -821,14 +854,16 @@ int tile_columns(const QAttn &a) {
 }
 
 int blocks_of(const QAttn &a) {
-    const int cols = tile_columns(a);
-    const int most = kSm * (cols == 8 ? blocks_per_sm<1>() : cols == 16 ? blocks_per_sm<2>() : blocks_per_sm<4>());
+    const int cols = tile_columns(a), ng = a.c.groups;
+    const int per_sm = cols == 8    ? blocks_per_sm<4, 1>()
+                       : cols == 16 ? (ng == 4 ? blocks_per_sm<4, 2>() : blocks_per_sm<1, 2>())
+                                    : blocks_per_sm<4, 4>();
     // no more than the longest lengths that the table can hold would use
     const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
-    const long long tiles = rows * a.g / cols + a.batch;
-    const double chunks = (double)a.c.h_kv * tiles * a.max_pages * (a.c.page_size / kChunk);
-    const double units = chunks + (double)a.c.h_kv * tiles * kItemUnits;
-    return units < (double)most * kMinUnits ? (int)(units / kMinUnits) + 1 : most;
+    const double items = (double)a.c.h_kv * (rows * a.g / cols + a.batch);
+    const double chunks = items * ((double)a.max_pages * (a.c.page_size / kChunk) + item_chunks<4>());
+    const int most = kSm * per_sm;
+    return chunks < (double)most * kMinChunks ? (int)(chunks / kMinChunks) + 1 : most;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
