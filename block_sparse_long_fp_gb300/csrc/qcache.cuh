@@ -83,6 +83,7 @@ struct QAttn {
     __nv_bfloat16 *out;
     float *lse;
     int *status;
+    bool whole;                                // no item is cut (set by the launch)
 };
 size_t qcache_attn_scratch_bytes(const QAttn &a);
 cudaError_t launch_qcache_attn(const QAttn &a, void *scratch, cudaStream_t st);

@@ -63,7 +63,7 @@ def check_tables(fp, table, old, new, free, head, page, pool, capacity, in_place
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("batch,old_max,new_max,page", [
     (1, 0, 1, 16), (1, 0, 5000, 16), (5, 300, 0, 64), (64, 3000, 1, 64), (7, 100, 900, 256), (300, 50, 40, 32),
-    (1500, 20, 9, 16), (4096, 6, 3, 128), (3, 70000, 40000, 128)])
+    (1500, 20, 9, 16), (4096, 6, 3, 128), (3, 70000, 40000, 128), (40, 2000, 3000, 384)])
 def test_page_tables(fp, batch, old_max, new_max, page, in_place):
     table, old, new, free, pool, cap = tables_case(batch + page, batch, old_max, new_max, page)
     check_tables(fp, table, old, new, free, 2, page, pool, cap, in_place)
@@ -390,16 +390,22 @@ def check_attn(fp, case, lens, lq, page, group, ragged, scale=None, max_q=None):
     cu = i32(np.concatenate([[0], np.cumsum(lq)])) if ragged else None
     out, lse = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=max_q if max_q else max(1, max(lq)), q_scale=qs,
                       softmax_scale=scale or 0.0)
+    # a table that has room for long caches has its items cut between thread blocks, a narrow one may not
+    wide = np.full((len(lens), max(table.shape[1], 1 + 1024 // page)), 10 ** 6)
+    wide[:, :table.shape[1]] = table
+    cut, cut_lse = c.attn(q, i32(wide), i32(lens), cu_seqlens_q=cu, max_q=max_q if max_q else max(1, max(lq)), q_scale=qs,
+                          softmax_scale=scale or 0.0)
     ref_o, ref_lse = oq.attention(q32, data, page, group, table, lens, lq, scale)
     tol_o, tol_lse = tolerances(q32, data, group, ref_o, ref_lse, scale or 128 ** -0.5)
-    got, got_lse = out.float().cpu().numpy(), lse.cpu().numpy()
     assert c.device_status() == 0
-    assert np.isfinite(got).all()
-    assert np.all(np.abs(got - ref_o) <= tol_o), float((np.abs(got - ref_o) / tol_o).max())
-    empty = np.isneginf(ref_lse)
-    assert np.array_equal(empty, np.isneginf(got_lse))
-    assert np.all(np.abs(got_lse[~empty] - ref_lse[~empty]) <= tol_lse[~empty])
-    assert np.all(got.transpose(1, 0, 2)[empty] == 0)
+    for o, l in ((out, lse), (cut, cut_lse)):
+        got, got_lse = o.float().cpu().numpy(), l.cpu().numpy()
+        assert np.isfinite(got).all()
+        assert np.all(np.abs(got - ref_o) <= tol_o), float((np.abs(got - ref_o) / tol_o).max())
+        empty = np.isneginf(ref_lse)
+        assert np.array_equal(empty, np.isneginf(got_lse))
+        assert np.all(np.abs(got_lse[~empty] - ref_lse[~empty]) <= tol_lse[~empty])
+        assert np.all(got.transpose(1, 0, 2)[empty] == 0)
     return out, lse
 
 
@@ -407,7 +413,7 @@ def check_attn(fp, case, lens, lq, page, group, ragged, scale=None, max_q=None):
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("lens,h_q,h,page", [
     ([1], 1, 1, 16), ([2, 0, 15, 16, 17], 4, 1, 16), ([700], 16, 2, 64), ([33, 129, 1, 0, 64, 300], 6, 2, 32),
-    ([257, 256, 255], 15, 3, 256), ([1000, 31], 40, 2, 128)])
+    ([257, 256, 255], 15, 3, 256), ([1000, 31], 40, 2, 128), ([400, 385, 100], 6, 2, 384)])
 def test_decode(fp, lens, h_q, h, page, group, dtype):
     lq = [1] * len(lens)
     check_attn(fp, attn_case(len(lens) + h_q, lens, lq, h_q, h, page, group, dtype), lens, lq, page, group, False)
@@ -427,11 +433,23 @@ def test_ragged_queries(fp, lens, lq, h_q, h, page, group):
     assert (a[0].float() - b[0].float()).abs().max() <= 2 ** -6
 
 
-@pytest.mark.parametrize("lq", [2, 3, 5, 8])
-def test_uniform_runs_of_queries(fp, lq):
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("lq,h_q,h", [(2, 16, 2), (3, 16, 2), (5, 16, 2), (8, 16, 2), (1, 32, 2), (1, 12, 1), (4, 20, 4)])
+def test_uniform_runs_of_queries(fp, lq, h_q, h, group):
+    """Every number of column octets: 16, 24, 40, 64, 16, 12 and 20 columns a kv head."""
     lens = [70, 400, lq]
-    case = attn_case(lq, lens, [lq] * 3, 16, 2, 64, 64)
-    check_attn(fp, case, lens, [lq] * 3, 64, 64, False)
+    case = attn_case(lq, lens, [lq] * 3, h_q, h, 64, group)
+    check_attn(fp, case, lens, [lq] * 3, 64, group, False)
+
+
+def test_more_requests_than_a_block_scans_at_once(fp):
+    """Ragged rows of 300 requests, some without rows and some without tokens, and the blocks' cuts among them."""
+    rng = np.random.default_rng(21)
+    lens = rng.integers(0, 60, 300)
+    lq = np.minimum(rng.integers(0, 4, 300), np.maximum(lens, 1))
+    lens[::17] = 0
+    case = attn_case(21, list(lens), list(lq), 6, 2, 16, 64)
+    check_attn(fp, case, list(lens), list(lq), 16, 64, True)
 
 
 @pytest.mark.parametrize("batch,length", [(1, 20000), (3, 5000), (150, 40)])
@@ -480,7 +498,8 @@ def test_q_strides_and_rows_behind_the_last_request(fp):
     assert none is None and torch.equal(out2, a)
 
 
-def test_bad_device_data_is_reported(fp):
+@pytest.mark.parametrize("width", [0, 80])
+def test_bad_device_data_is_reported(fp, width):
     """Page ids out of range read as zeros, lengths out of range as an empty
     cache, rows outside q are left out.  Another length moves the cuts between
     the thread blocks, and with them the rounding of every request: the results
@@ -488,6 +507,8 @@ def test_bad_device_data_is_reported(fp):
     import torch
     lens, lq = [90, 200, 40], [1, 1, 1]
     data, table, q, q32, _ = attn_case(4, lens, lq, 8, 2, 16, 32)
+    if width > table.shape[1]:
+        table = np.concatenate([table, np.full((3, width - table.shape[1]), 10 ** 6)], 1)
     c = fp.QCache(torch.from_numpy(data).cuda(), 16, 32)
 
     def check(out, lse, table, lens, rows=3):
@@ -506,7 +527,7 @@ def test_bad_device_data_is_reported(fp):
         bad = table.copy()
         bad[1, 3] = value
         check(*c.attn(q, i32(bad), i32(lens)), bad, lens)
-    for value in (-3, table.shape[1] * 16 + 1, 2 ** 31 - 1):
+    for value in (-3, table.shape[1] * 16 + 1, 2 ** 31 - 1):             # (a narrow table is not cut, a wide one is)
         out, lse = c.attn(q, i32(table), i32([90, value, 40]))
         assert (out[1] == 0).all()
         check(out, lse, table, [90, 0, 40])
@@ -528,6 +549,103 @@ def test_repeated_calls_are_bit_identical(fp):
     for _ in range(5):
         again, l2 = c.attn(q, i32(table), i32(lens))
         assert torch.equal(first, again) and torch.equal(l1, l2)
+
+
+def test_pages_shared_by_requests(fp):
+    """Two requests with a common prefix point at the same pages."""
+    lens, lq = [150, 140, 64], [1, 1, 1]
+    data, table, q, q32, _ = attn_case(31, lens, lq, 8, 2, 32, 32, poison=False)
+    table[1, :3] = table[0, :3]
+    table[2, :2] = table[0, :2]
+    check_attn(fp, (data, table, q, q32, None), lens, lq, 32, 32, False)
+
+
+def test_offsets_past_32_bits(fp):
+    """A cache of 4.7 GB: chunks behind 2^32 bytes are written, read and attended."""
+    import torch
+    page, h, group, pages = 128, 8, 64, 2 ** 32 // (8 * 8 * 2304) + 3000
+    c = fp.QCache.empty(pages, page, h, group)
+    assert c.data.numel() > 2 ** 32 + 3000 * 8 * 8 * 2304 - 2 ** 20
+    rng = np.random.default_rng(5)
+    mine = np.array([pages - 1, 3, pages - 700, pages - 2])
+    lens, lq, rows = [350, 100], [1, 1], 450
+    table = np.array([[mine[0], mine[1], mine[2]], [mine[3], 0, 0]])
+    t = np.arange(350)
+    slots = np.concatenate([table[0, t // page] * page + t % page, mine[3] * page + np.arange(100)])
+    k, k32, _ = source(1, rows, h, "bf16")
+    v, v32, _ = source(2, rows, h, "bf16")
+    for part in (slice(0, 449), slice(449, 450)):
+        c.write(k[part], v[part], i32(slots[part]))
+    # the oracle's cache has just these pages
+    small = np.zeros((4, h, page // 16, oq.chunk_bytes(group)), np.uint8)
+    to_small = {int(p): i for i, p in enumerate(mine)}
+    small_slots = [to_small[int(s) // page] * page + int(s) % page for s in slots]
+    oq.write(small, page, group, small_slots, k32, v32)
+    for i, p in enumerate(mine):
+        n = [128, 128, 94, 100][i]
+        rows_i = np.arange(n) + i * page
+        for a, b in zip(oq.read(c.data[int(p):int(p) + 1].cpu().numpy(), page, group, np.arange(n)),
+                        oq.read(small, page, group, rows_i)):
+            assert np.array_equal(a, b)
+    back = c.read(i32(slots))
+    for got, want in zip(back, oq.read(small, page, group, small_slots)):
+        assert torch.equal(got.cpu(), torch.from_numpy(want).float().bfloat16())
+    q, q32, _ = source(3, 2, 16, "bf16")
+    out, lse = c.attn(q, i32(table), i32(lens))
+    ref_o, ref_lse = oq.attention(q32, small, page, group, np.array([[0, 1, 2], [3, 0, 0]]), lens, lq)
+    tol_o, tol_lse = tolerances(q32, small, group, ref_o, ref_lse, 128 ** -0.5)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
+    assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
+    assert c.device_status() == 0
+
+
+def test_python_checks_its_tensors(fp):
+    import torch
+    E = fp.FprefillError
+    c = fp.QCache.empty(4, 16, 2, 64)
+    x = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    s = i32([1, 2, 3])
+    scale = torch.ones(2, device="cuda")
+    for bad in (lambda: c.write(x.float(), x.float(), s), lambda: c.write(x, x[:2], s), lambda: c.write(x[:, :1], x[:, :1], s),
+                lambda: c.write(x, x, s.long()), lambda: c.write(x, x, s[:2]), lambda: c.write(x, x, s.cpu()),
+                lambda: c.write(x.cpu(), x.cpu(), s), lambda: c.write(x[..., :64], x[..., :64], s),
+                lambda: c.write(x, x.transpose(0, 1).contiguous().transpose(0, 1), s), lambda: c.write(x, x, s, scale, scale),
+                lambda: c.write(x.to(torch.uint8), x.to(torch.uint8), s, scale),
+                lambda: c.write(x.to(torch.uint8), x.to(torch.uint8), s, scale, scale[:1]),
+                lambda: c.read(s, x), lambda: c.read(s, x, x, out_slots=s[:2]), lambda: c.read(s[:2], x, x),
+                lambda: c.read(s, out_slots=s), lambda: c.write(x[..., ::2].repeat(1, 1, 2)[..., ::2], x, s)):
+        with pytest.raises(E):
+            bad()
+    table, lens = i32([[0, 1], [2, 3]]), i32([5, 6])
+    q = torch.zeros((2, 4, 128), dtype=torch.bfloat16, device="cuda")
+    for bad in (lambda: c.attn(q[:, :3], table, lens), lambda: c.attn(q, table[:1], lens), lambda: c.attn(q, table.long(), lens),
+                lambda: c.attn(q, table, lens.float()), lambda: c.attn(q, table, lens, cu_seqlens_q=i32([0, 1])),
+                lambda: c.attn(q.float(), table, lens), lambda: c.attn(q, table, lens, max_q=2),
+                lambda: c.attn(q, table, lens, out=q[:1]), lambda: c.attn(q, table, lens, lse=torch.zeros((2, 4), device="cuda")),
+                lambda: c.attn(q, table, lens, q_scale=scale), lambda: c.attn(q, table.cpu(), lens),
+                lambda: c.attn(q[..., :64], table, lens), lambda: c.attn(q, table.t(), lens), lambda: c.attn(q, table, lens, max_q=0)):
+        with pytest.raises(E):
+            bad()
+    with pytest.raises(E):
+        fp.QCache(c.data, 32, 64)
+    with pytest.raises(E):
+        fp.QCache(c.data, 16, 32)
+    p = fp.PageTables(table, 16, 4, 8)
+    for bad in (lambda: p.step(lens[:1], lens, s), lambda: p.step(lens, lens.long(), s), lambda: p.step(lens, lens, s.cpu()),
+                lambda: p.step(lens, lens, s, i32([0, 1]))):
+        with pytest.raises(E):
+            bad()
+    assert c.device_status() == 0
+    # e4m3 as torch's own type is the same as its codes
+    f = torch.randn((3, 2, 128), device="cuda").to(torch.float8_e4m3fn)
+    c.write(f, f, s, scale, scale)
+    a = c.data.clone()
+    c.write(f.view(torch.uint8), f.view(torch.uint8), s, scale, scale)
+    assert torch.equal(a, c.data)
+    # nothing to do
+    c.write(x[:0], x[:0], s[:0])
+    out, lse = c.attn(q[:0], table, i32([0, 0]), cu_seqlens_q=i32([0, 0, 0]), max_q=1)
+    assert out.shape == (0, 4, 128) and lse.shape == (4, 0) and c.device_status() == 0
 
 
 # -- together -----------------------------------------------------------------------------
@@ -628,3 +746,59 @@ def test_two_streams_and_another_current_stream(fp):
                 got.append(c.attn(x, bt, ln)[0])
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_graphs_of_one_cache_replayed_at_once(fp):
+    """Each captured call has its own scratch: two graphs on two streams do not meet in it."""
+    import torch
+    lens = [9000, 4000]
+    data, table, q, q32, _ = attn_case(9, lens, [1, 1], 16, 2, 64, 32)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 64, 32)
+    bt, ln = i32(table), i32(lens)
+    qs = [q, q * 2]
+    want = [c.attn(x, bt, ln)[0].clone() for x in qs]
+    outs = [torch.zeros_like(x) for x in qs]
+    graphs = []
+    for x, o in zip(qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                c.attn(x, bt, ln, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = c.attn(qs[0], bt, ln)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[0]) and all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_two_threads_share_a_cache(fp):
+    """Calls from two threads, each on a stream of its own."""
+    import threading
+    import torch
+    data, table, q, q32, _ = attn_case(9, [3000, 700], [1, 1], 16, 2, 64, 32)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 64, 32)
+    bt, ln = i32(table), i32([3000, 700])
+    qs = [q, q * 2]
+    want = [c.attn(x, bt, ln)[0].clone() for x in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x, w):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                if not torch.equal(c.attn(x, bt, ln)[0], w):
+                    wrong.append(1)
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
