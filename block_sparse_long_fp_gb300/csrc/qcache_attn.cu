@@ -45,7 +45,7 @@ constexpr int kMinChunks = 2 * kWarps;       // least work worth a thread block
 // chunk costs by the octets of columns in use (extracting the codes is most of it; with
 // one octet at most there is nothing to tell apart).
 template <int NT>
-constexpr int item_chunks() { return NT == 1 ? 16 : NT == 2 ? 20 : 32; }
+constexpr int item_chunks() { return NT == 1 ? 24 : NT == 2 ? 28 : 32; }
 template <int NT>
 __device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 + octets; }
 // Longest cache, by the width of its table, that is not cut.  64 requests of up to 1024
@@ -316,38 +316,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
         return (long long)a.c.h_kv * (kItem + chunks_of(q)) *
                ((tiles - 1) * chunk_units<NT>(NT) + chunk_units<NT>(octets_of(q, tiles - 1)));
     };
+    const int each = (a.batch + kThreads - 1) / kThreads;      // requests a thread adds up
     Request q = {0, 0, 0, 0};
-    if (tid < a.batch) q = request_of(a, tid);
-    long long n = units(q), total;
-    if (tid >= a.batch) n = 0;
+    long long n = 0, total;
+    for (int r = tid * each; r < min(a.batch, (tid + 1) * each); ++r) n += units(q = request_of(a, r));
     long long low = block_scan(n, &total, warp_sums);
-    for (int base = kThreads; base < a.batch; base += kThreads) {
-        long long all;
-        block_scan(base + tid < a.batch ? units(request_of(a, base + tid)) : 0, &all, warp_sums);
-        total += all;
-    }
     const long long want = a.whole ? total : total / (kMinChunks * chunk_units<NT>(NT)) + 1;
     const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0 && !a.whole) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
     const long long first = (long long)blockIdx.x * total / blocks, end = (long long)(blockIdx.x + 1) * total / blocks;
-    long long before = 0;
-    for (int base = 0; base < a.batch; base += kThreads) {
-        if (base) {
-            n = 0;
-            if (base + tid < a.batch) n = units(q = request_of(a, base + tid));
-            long long all;
-            low = before + block_scan(n, &all, warp_sums);
-            before += all;
-        } else if (a.batch > kThreads) {
-            block_scan(n, &before, warp_sums);
-        }
-        if (low <= first && first < low + n) {
-            s_r = base + tid;
-            s_at = low;
-            s_q = q;
-        }
-        if (before > first) break;
+    if (low <= first && first < low + n) {
+        int r = tid * each;
+        if (each > 1)
+            for (;; ++r) {
+                n = units(q = request_of(a, r));
+                if (first < low + n || r + 1 == a.batch) break;
+                low += n;
+            }
+        s_r = r;
+        s_at = low;
+        s_q = q;
     }
     __syncthreads();
     int r = s_r;
@@ -455,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
         }
         if (kSharedQ) __syncthreads();
         float factor[NT][2];
-        int min_keys = 0x7fffffff;
+        const int min_keys = min(q.len, q.len - q.lq + tile * kCols / a.g + 1);     // of the tile's first query
         // keys that column c of this lane (of 8 t + 2 j4 + e) may see
         const auto keys_of = [&](int t, int e) {
             const int i = (tile * kCols + t * 8 + 2 * j4 + e) / a.g;
@@ -467,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
             for (int e = 0; e < 2; ++e)
                 factor[t][e] = kSharedQ ? s_factor[t * 8 + 2 * j4 + e]
                                         : __shfl_sync(~0u, qs[kSharedQ ? 0 : t].factor, (2 * j4 + e) * 4);
-        min_keys = min(q.len, q.len - q.lq + tile * kCols / a.g + 1);     // of the tile's first query
 
         float o[NT][8][4];                        // O^T: 8 tiles of 16 dims
         float z[NT][4];                           // the minima's part, a row per group
@@ -777,6 +765,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch 
     __shared__ float part_l[kJoinWarps];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     after_previous();
+    let_next();
     // the items that blocks left open, in the same order for every block of this grid
     Open rec[kEach];
     unsigned vote[kEach];
