@@ -297,9 +297,9 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
     return y;
 }
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
     unsigned long long y;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
     return y;
 }
 
@@ -318,23 +318,66 @@ __device__ __forceinline__ float reciprocal(float s) {
     return fmaf(fmaf(-s, y, 1.f), y, y);
 }
 
-// Sixteen codes (the first in the low bits), their group's step and minimum.  A
-// group's least and greatest value say whether any of it needs the clamps.
-template <int GROUPS>
-__device__ __forceinline__ uint2 quantise16(float x[16], __half *step, __half *low) {
-    float mn = x[0], mx = x[0];
+// Eight codes, the first in the low bits, of eight values: (x - minimum) / step to the
+// nearest, by adding 1.5 2^23, which leaves the code in the sum's low bits.  Products and
+// sums stay apart: a fused one would round a tie that the product's rounding makes
+// otherwise.  The assembler joins a packed product and the sum behind it into one rounding
+// for all that both say .rn, and a fused product with a zero that it can see is a product
+// to it: `zeros`, a pair of -0, comes from where it cannot.  Without `clamp` the codes are
+// known to be in 0 .. 15.
+__device__ __forceinline__ uint32_t codes8(const unsigned long long x[4], float low, float inv, unsigned long long zeros,
+                                           bool clamp) {
+    const unsigned long long minus = pair(-low, -low), by = pair(inv, inv), magic = pair(12582912.f, 12582912.f);
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 1; i < 16; i += 2) {
-        const float b = x[i], c = x[i + 1 < 16 ? i + 1 : i];
-        mn = min_nan(mn, b, c);
-        mx = max_nan(mx, b, c);
+    for (int i = 3; i >= 0; --i) {
+        unsigned long long y = fma2(add2(x[i], minus), by, zeros);
+        if (clamp) {
+            const float2 v = unpair(y);
+            y = pair(fminf(fmaxf(v.x, 0.f), 15.f), fminf(fmaxf(v.y, 0.f), 15.f));
+        }
+        const float2 v = unpair(add2(y, magic));
+        w = w * 256 + __float_as_uint(v.y) * 16 + __float_as_uint(v.x);
+    }
+    return w - 0x4b400000u * 0x11111111u;        // the magic's own bits, eight times
+}
+
+// Sixteen codes of a lane, their group's step and minimum.  The group's least and greatest
+// value say whether any of it needs the clamps, which are a path of their own.
+template <int GROUPS, bool FP8>
+__device__ __forceinline__ uint2 quantise16(const Raw<FP8> &raw, float scale, unsigned long long zeros, __half *step,
+                                            __half *low) {
+    float mn, mx;
+    if (FP8) {
+        float x[16];
+        unpack16<FP8>(raw, scale, x);
+        mn = mx = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; i += 2) {
+            const float b = x[i], c = x[i + 1 < 16 ? i + 1 : i];
+            mn = min_nan(mn, b, c);
+            mx = max_nan(mx, b, c);
+        }
+    } else {                                     // bf16 two at a time, as they lie
+        const uint4 a = raw.w[0], b = raw.w[FP8 ? 0 : 1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162 *>(&w[0]), hi = lo;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            lo = __hmin2_nan(lo, *reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+            hi = __hmax2_nan(hi, *reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        }
+        const float2 l = __bfloat1622float2(lo), h = __bfloat1622float2(hi);
+        mn = min_nan(l.x, l.y, l.y);
+        mx = max_nan(h.x, h.y, h.y);
     }
 #pragma unroll
     for (int d = 1; d < 8 / GROUPS; d *= 2) {
         mn = min_nan(mn, mn, __shfl_xor_sync(~0u, mn, d));
         mx = max_nan(mx, mx, __shfl_xor_sync(~0u, mx, d));
     }
-    if (!(mn >= -65504.f && mx <= 65504.f)) {
+    const bool far = !(mn >= -65504.f && mx <= 65504.f);
+    if (far) {
         if (mn != mn) {                          // a NaN in the group
             *step = __ushort_as_half(0);
             *low = __ushort_as_half(0x7e00);
@@ -342,8 +385,6 @@ __device__ __forceinline__ uint2 quantise16(float x[16], __half *step, __half *l
         }
         mn = fminf(fmaxf(mn, -65504.f), 65504.f);
         mx = fminf(fmaxf(mx, -65504.f), 65504.f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
     }
     const __half m = __float2half_rn(mn);
     const float mf = __half2float(m);
@@ -352,31 +393,33 @@ __device__ __forceinline__ uint2 quantise16(float x[16], __half *step, __half *l
     const float inv = sf > 0.f ? reciprocal(sf) : 0.f;
     *step = s;
     *low = m;
-    // rint by adding 1.5 2^23: the code is the sum's low bits.  Products and sums stay
-    // apart: a fused one would round a tie that the product's rounding makes otherwise.
-    const unsigned long long minus = pair(-mf, -mf), by = pair(inv, inv), magic = pair(12582912.f, 12582912.f);
-    unsigned long long y[8];
+    const bool clamp =
+        far || __fmul_rn(__fsub_rn(mn, mf), inv) < -0.5f || __fmul_rn(__fsub_rn(mx, mf), inv) >= 15.5f;
+    uint32_t code[2];
+    if (clamp) {
+        float x[16];
+        unpack16<FP8>(raw, scale, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = mul2(add2(pair(x[2 * i], x[2 * i + 1]), minus), by);
-    if (__fmul_rn(__fsub_rn(mn, mf), inv) < -0.5f || __fmul_rn(__fsub_rn(mx, mf), inv) >= 15.5f) {
+        for (int h = 0; h < 2; ++h) {
+            unsigned long long y[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 v = unpair(y[i]);
-            y[i] = pair(fminf(fmaxf(v.x, 0.f), 15.f), fminf(fmaxf(v.y, 0.f), 15.f));
+            for (int i = 0; i < 4; ++i)
+                y[i] = pair(fminf(fmaxf(x[8 * h + 2 * i], -65504.f), 65504.f),
+                            fminf(fmaxf(x[8 * h + 2 * i + 1], -65504.f), 65504.f));
+            code[h] = codes8(y, mf, inv, zeros, true);
+        }
+    } else {
+        float x[16];
+        unpack16<FP8>(raw, scale, x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            unsigned long long y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = pair(x[8 * h + 2 * i], x[8 * h + 2 * i + 1]);
+            code[h] = codes8(y, mf, inv, zeros, false);
         }
     }
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        w[h] = 0;
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-            const float2 v = unpair(add2(y[4 * h + i], magic));
-            w[h] = w[h] * 256 + __float_as_uint(v.y) * 16 + __float_as_uint(v.x);
-        }
-        w[h] -= 0x4b400000u * 0x11111111u;       // the magic's own bits, eight times
-    }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(code[0], code[1]);
 }
 
 // The rows of a warp, 16 at a time: body(first row, rows, slot of row lane & 15, its
@@ -400,24 +443,25 @@ __device__ __forceinline__ void write_half(const QCache &c, const QRows &r, int 
     using H = Half<GROUPS, V>;
     const int lane = threadIdx.x & 31, sub = lane / 8, part = lane % 8;      // row of four, 16 dims of the row
     const void *src = V ? r.v : r.k;
+    const float zero = r.rows > 0 ? -0.f : 1.f;
+    const unsigned long long zeros = pair(zero, zero);
     const float scale = FP8 ? (V ? r.v_scale : r.k_scale)[head] : 1.f;
     for_owned(c, r, w, head, [&](int row0, int n, int mine, unsigned char *chunk) {
         const auto load = [&](int i) {
             return load16<FP8>(src, (long long)(row0 + 4 * i + sub) * r.stride_tok + head * r.stride_head + 16 * part,
                                4 * i + sub < n);
         };
-        // rolled, two steps' loads ahead: unrolled, the instructions do not fit their cache
+        // two steps a turn, with the loads two steps ahead (four steps unrolled do not fit the
+        // instruction cache; one: 141 us for 64K tokens written and read, two: 138)
         Raw<FP8> raw = load(0), next = load(1);
-#pragma unroll 1
+#pragma unroll 2
         for (int i = 0; i < 4; ++i) {
             const Raw<FP8> behind = load(i + 2);
             const int t = 4 * i + sub;
-            float x[16];
             __half s, m;
-            unpack16<FP8>(raw, scale, x);
+            const uint2 code = quantise16<GROUPS, FP8>(raw, scale, zeros, &s, &m);
             raw = next;
             next = behind;
-            const uint2 code = quantise16<GROUPS>(x, &s, &m);
             unsigned char *p = img + H::code(t, part * 4);
             if (V) {                             // dims 16 part .. + 15: four rows of four
                 *reinterpret_cast<uint16_t *>(p) = (uint16_t)code.x;
