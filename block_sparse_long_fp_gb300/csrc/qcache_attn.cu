@@ -98,6 +98,33 @@ __device__ __forceinline__ void mma8_zero(float d[4], uint32_t a0, uint32_t a1, 
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
+// Two fp32 in one register pair.
+using float_pair = unsigned long long;
+__device__ __forceinline__ float_pair pair(float lo, float hi) {
+    float_pair y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
+    return y;
+}
+__device__ __forceinline__ float2 unpair(float_pair x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ float_pair fma2(float_pair a, float_pair b, float_pair c) {
+    float_pair y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ float_pair add2(float_pair a, float_pair b) {
+    float_pair y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
+    float_pair y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
 // Transpose of the 8 x 8 fp16 matrix whose row lane / 4 holds the lane's pair.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -485,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
             const unsigned char *chunk = ring + (i % kStages) * kBytes;
             const int t0 = (c0 + warp + i * kWarps) * kChunk;
 
-            // logits
-            float x[L][4];
+            // logits: rows r8 and r8 + 8, two columns each
+            float_pair x[L][2];
             {
                 const uint4 ka = *reinterpret_cast<const uint4 *>(chunk + lane * 16);
                 const uint4 kb = *reinterpret_cast<const uint4 *>(chunk + 512 + lane * 16);
@@ -503,8 +530,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
                 for (int t = 0; t < L; ++t) {
                     float c[4];
                     mma8_zero(c, m0, m1, kSharedQ ? s_sum[t][lane] : qs[kSharedQ ? 0 : t].sum);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[t][e] = c[e] * 0x1p-6f;
+                    x[t][0] = mul2(pair(c[0], c[1]), pair(0x1p-6f, 0x1p-6f));
+                    x[t][1] = mul2(pair(c[2], c[3]), pair(0x1p-6f, 0x1p-6f));
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
@@ -531,10 +558,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
                     }
 #pragma unroll
                     for (int t = 0; t < L; ++t) {
-                        x[t][0] = fmaf(s0[g], acc[t][0], x[t][0]);
-                        x[t][1] = fmaf(s0[g], acc[t][1], x[t][1]);
-                        x[t][2] = fmaf(s1[g], acc[t][2], x[t][2]);
-                        x[t][3] = fmaf(s1[g], acc[t][3], x[t][3]);
+                        x[t][0] = fma2(pair(s0[g], s0[g]), pair(acc[t][0], acc[t][1]), x[t][0]);
+                        x[t][1] = fma2(pair(s1[g], s1[g]), pair(acc[t][2], acc[t][3]), x[t][1]);
                     }
                 }
             }
@@ -575,7 +600,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
 #pragma unroll
             for (int t = 0; t < L; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[t][e] = fmaf(x[t][e], factor[t][e & 1], -base[t][e & 1]);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 v = unpair(fma2(x[t][h], pair(factor[t][0], factor[t][1]), pair(-base[t][0], -base[t][1])));
+                    y[t][2 * h] = v.x;
+                    y[t][2 * h + 1] = v.y;
+                }
             if (kEdge) {
 #pragma unroll
                 for (int t = 0; t < L; ++t)
@@ -606,8 +635,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const bool out0 = y[t][c] == -INFINITY, out1 = y[t][c + 2] == -INFINITY;
-                            const float l0 = out0 ? -INFINITY : x[t][c] * factor[t][c];
-                            const float l1 = out1 ? -INFINITY : x[t][c + 2] * factor[t][c];
+                            const float2 x0 = unpair(x[t][0]), x1 = unpair(x[t][1]);
+                            const float l0 = out0 ? -INFINITY : (c ? x0.y : x0.x) * factor[t][c];
+                            const float l1 = out1 ? -INFINITY : (c ? x1.y : x1.x) * factor[t][c];
                             float m = fmaxf(l0, l1);
 #pragma unroll
                             for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
@@ -632,8 +662,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
             for (int t = 0; t < L; ++t) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[t][e] = fast_exp2(y[t][e]);
-                sum[t][0] += y[t][0] + y[t][2];
-                sum[t][1] += y[t][1] + y[t][3];
+                const float2 v = unpair(add2(pair(sum[t][0], sum[t][1]), add2(pair(y[t][0], y[t][1]), pair(y[t][2], y[t][3]))));
+                sum[t][0] = v.x;
+                sum[t][1] = v.y;
                 p[t][0] = transpose8(pack_half2(y[t][0], y[t][1]));
                 p[t][1] = transpose8(pack_half2(y[t][2], y[t][3]));
                 mma16(z[t], vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
