@@ -67,7 +67,7 @@ __global__ void tables_kernel(fp_tables t, int shift, int *status) {
         if (r < t.batch) {
             old = t.seqlens[r];
             add = t.new_lens[r];
-            const long long all = old >= 0 && add >= 0 ? pages(old + add) : -1;
+            const long long all = old >= 0 && add >= 0 && old + add <= 0x7fffffffll ? pages(old + add) : -1;
             ok = all >= 0 && all <= t.max_pages_per_seq;
             need = ok ? all - pages(old) : 0;
             if (add < 0) add = 0;

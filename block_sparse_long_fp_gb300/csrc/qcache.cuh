@@ -80,6 +80,7 @@ struct QAttn {
     const int *cu;                             // null: max_q rows each
     const int *seqlens_k, *block_table;
     int max_pages;
+    int max_len;                               // what the table holds, short of what an int's arithmetic can
     float scale;                               // logit scale
     __nv_bfloat16 *out;
     float *lse;

@@ -58,7 +58,7 @@ fp_status check_rows(const fp_qcache *c, const fp_qcache_rows *r, bool read, QCa
     if (!strides_ok(r->stride_tok, r->stride_head, c->h_kv, r->dtype == FP_E4M3 ? 1 : 2)) return FP_ERR_INVALID;
     if (r->dtype == FP_E4M3 && (!r->k_scale || !r->v_scale)) return FP_ERR_INVALID;
     if (read && (r->out_rows < 0 || (!r->out_slots && r->out_rows < r->rows))) return FP_ERR_INVALID;
-    if ((long long)r->rows * c->h_kv > (1ll << 33)) return FP_ERR_UNSUPPORTED;
+    if (r->rows > (1 << 30) || (long long)r->rows * c->h_kv > (1ll << 33)) return FP_ERR_UNSUPPORTED;
     *rows = QRows{r->k, r->v, r->stride_tok, r->stride_head, r->slots, read ? r->out_slots : nullptr, r->rows,
                   r->out_rows, r->dtype == FP_E4M3 ? r->k_scale : nullptr, r->dtype == FP_E4M3 ? r->v_scale : nullptr};
     return FP_OK;
@@ -89,6 +89,8 @@ fp_status check_query(const fp_qcache *c, const fp_qcache_query *q, QAttn *a) {
     a->seqlens_k = q->seqlens_k;
     a->block_table = q->block_table;
     a->max_pages = q->max_pages_per_seq;
+    const long long held = (long long)q->max_pages_per_seq * c->page_size, most = (1ll << 31) - 64;
+    a->max_len = (int)(held < most ? held : most);
     a->scale = q->softmax_scale > 0.f ? q->softmax_scale : 1.f / sqrtf((float)kHeadDim);
     return FP_OK;
 }

@@ -173,7 +173,7 @@ __device__ __forceinline__ Request request_of(const QAttn &a, int r) {
         q.lq = q.rows = a.max_q;
     }
     q.len = a.seqlens_k[r];
-    if (q.len < 0 || q.len > (long long)a.max_pages * a.c.page_size) {
+    if (q.len < 0 || q.len > a.max_len) {
         set_status(a.status, FP_ERR_DEVICE_BOUNDS);
         q.len = 0;
     }

@@ -364,8 +364,8 @@ fp_status fp_dense_attn(const fp_problem *p, const fp_params *prm, void *out, fl
  *   *free_next = head + sum_r need_r
  * positions and slots behind the last token, up to capacity, are 0 and -1.
  * The other entries of block_table stay as they are.
- * A request that cannot be served -- a negative length, more than
- * max_pages_per_seq pages, a free list or a capacity that does not reach --
+ * A request that cannot be served -- a negative length, more than 2^31 - 1
+ * tokens or max_pages_per_seq pages, a free list or a capacity that does not reach --
  * is refused as a whole: it takes no page, seqlens_k[r] = seqlens[r], its
  * slots are -1 and its positions 0 (its rows stay counted in cu_seqlens_q
  * unless new_lens[r] < 0, and saturate at 2^31 - 1), and the status says so.  When free list or
@@ -455,7 +455,7 @@ fp_status fp_qcache_write(const fp_qcache *c, const fp_qcache_rows *r, void *ws,
  *   (s * c + m) / scale[head], saturated at 448.  With out_slots a slot map of
  *   a bf16 / e4m3 paged cache, its pages are what the prefill entry points read.
  *   Rows with a slot of -1 in either map are left as they were; another value
- *   out of range too, with the status set. */
+ *   out of range too, with the status set.  No row of k and v may be named twice. */
 fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
@@ -471,8 +471,12 @@ fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, 
  *   out (device bf16 [total_q, h_q, d], contiguous), lse_opt (device fp32
  *   [h_q, total_q], natural log; may be NULL).
  *   Rows behind the last request, up to total_q, are left as they were.
- *   A page id outside [0, num_pages) reads as zeros; a length below 0 or above
- *   max_pages_per_seq * page_size reads as an empty cache; query rows outside
+ *   Queries are finite and below 2^115 in magnitude; a NaN or an infinity makes
+ *   its row NaN.  So does a NaN that the cache keeps in a key that the row attends,
+ *   or in a value that any row of its request in the call does (a weight of zero
+ *   times NaN is NaN); what lies behind a request's last token may be anything.
+ *   A page id outside [0, num_pages) reads as zeros; a length below 0, above
+ *   max_pages_per_seq * page_size or above 2^31 - 64 reads as an empty cache; query rows outside
  *   [0, total_q) are left out: each sets the status.
  *   scratch: fp_qcache_attn_scratch_bytes() bytes (partial results of requests
  *   that several thread blocks share); it holds nothing between calls.

@@ -140,7 +140,7 @@ def page_tables(block_table, seqlens, new_lens, free_pages, head: int, page: int
     refused = head < 0 or head > len(free_pages)
     for r in range(batch):
         old, new = int(seqlens[r]), int(new_lens[r])
-        ok = old >= 0 and new >= 0 and -(-(old + new) // page) <= width
+        ok = old >= 0 and new >= 0 and old + new <= 2 ** 31 - 1 and -(-(old + new) // page) <= width
         need = -(-(old + new) // page) - -(-old // page) if ok else 0
         start = int(cu[r])
         cu[r + 1] = start + max(0, new)

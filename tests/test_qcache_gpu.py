@@ -90,6 +90,9 @@ def test_page_tables_refuse_what_they_cannot_serve(fp):
     big = new.copy()
     big[2] = 2 ** 31 - 1
     check_tables(fp, table, old, big, free, 2, 16, pool, cap)
+    # lengths that an int cannot hold, though the table's pages could
+    two = np.array([[0, 0, 0, 0]] * 2)
+    check_tables(fp, two, np.array([2 ** 31 - 1, 2 ** 31 - 2]), np.array([1, 1]), np.array([0]), 0, 2 ** 30, 1, 4)
 
 
 # -- write and read ---------------------------------------------------------------
@@ -596,6 +599,39 @@ def test_offsets_past_32_bits(fp):
     tol_o, tol_lse = tolerances(q32, small, group, ref_o, ref_lse, 128 ** -0.5)
     assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
     assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
+    assert c.device_status() == 0
+
+
+def test_lengths_at_the_end_of_an_int_are_refused(fp):
+    """A table that has room for 2^31 tokens: a length near that is an empty cache, and reported."""
+    import torch
+    c = fp.QCache.empty(1, 16, 1, 128)
+    c.data.zero_()
+    table = torch.zeros((1, 2 ** 27), dtype=torch.int32, device="cuda")
+    q = torch.ones((1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    out, lse = c.attn(q, table, i32([2 ** 31 - 1]))
+    assert (out == 0).all() and torch.isneginf(lse).all() and c.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+
+
+def test_nan_and_infinity_reach_their_rows_only(fp):
+    """A NaN in one key of one head, an infinite value in another's: the rows that
+    attend them are NaN in the columns concerned, the others are what they were."""
+    import torch
+    lens, lq = [100, 60], [2, 1]
+    data, table, q, q32, _ = attn_case(17, lens, lq, 4, 2, 16, 64)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 16, 64)
+    cu = i32([0, 2, 3])
+    good, good_lse = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=2)
+    k, v = (t.clone() for t in c.read(i32([table[0, 6] * 16 + 3])))      # request 0's last token
+    k[0, 0, 5] = float("nan")
+    c.write(k, v, i32([table[0, 6] * 16 + 3]))
+    out, lse = c.attn(q, i32(table), i32(lens), cu_seqlens_q=cu, max_q=2)
+    assert torch.isnan(out[1, :2]).all() and torch.isnan(lse[:2, 1]).all()
+    for rows in ((0, slice(None)), (1, slice(2, 4)), (2, slice(None))):
+        assert torch.isfinite(out[rows].float()).all()
+        # the untouched token's codes were written anew by the same quantiser: within half a step of 64 dims
+        assert (out[rows].float() - good[rows].float()).abs().max() <= 0.2
+    assert torch.equal(out[2], good[2]) and torch.equal(out[0], good[0])
     assert c.device_status() == 0
 
 

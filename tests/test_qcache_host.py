@@ -75,7 +75,7 @@ def test_page_tables_refusals(fp, over, code):
     (dict(rows=-1), 1), (dict(dtype=7), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(slots=None), 1),
     (dict(k=P + 8), 1), (dict(stride_head=120), 1), (dict(stride_tok=500), 1), (dict(stride_tok=516), 1),
     (dict(stride_head=132, stride_tok=1024), 1), (dict(dtype=1), 1), (dict(dtype=1, k_scale=P), 1),
-    (dict(slots=P + 1), 1),
+    (dict(slots=P + 1), 1), (dict(rows=(1 << 30) + 1, out_rows=2 ** 31 - 1), 2),
 ])
 def test_rows_refusals(fp, over, code):
     L = fp.lib()
