@@ -508,6 +508,9 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
     const int lane = threadIdx.x & 31, sub = lane / 8, part = lane % 8;
     void *out = const_cast<void *>(V ? r.v : r.k);
     const float scale = FP8 ? (V ? r.v_scale : r.k_scale)[head] : 1.f;
+    // a scale whose quotients and remainders could leave the normal numbers is divided by plainly
+    const bool plain = !(fabsf(scale) >= 0x1p-60f && fabsf(scale) <= 0x1p60f);
+    const float inverse = 1.f / scale;
     for_owned(c, r, w, head, [&](int row0, int n, int mine, unsigned char *chunk) {
         // target of row row0 + (lane & 15), -1 where nothing is to be written
         int to = -1;
@@ -556,13 +559,22 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
             if (target < 0) continue;
             const long long at = target * r.stride_tok + head * r.stride_head + 16 * part;
             if (FP8) {
+                if (plain) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] /= scale;
+                } else {                         // the same quotients by the rounded reciprocal (Markstein 1990)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float f = __fmul_rn(x[e], inverse);
+                        x[e] = fmaf(fmaf(-f, scale, x[e]), inverse, f);
+                    }
+                }
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * e] / scale, x[4 * e + 1] / scale), __NV_SATFINITE,
-                                                    __NV_E4M3) |
-                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * e + 2] / scale, x[4 * e + 3] / scale),
-                                                              __NV_SATFINITE, __NV_E4M3) << 16;
+                    y[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * e], x[4 * e + 1]), __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * e + 2], x[4 * e + 3]), __NV_SATFINITE,
+                                                              __NV_E4M3) << 16;
                 *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(out) + at) = make_uint4(y[0], y[1], y[2], y[3]);
             } else {
                 uint32_t y[8];

@@ -221,6 +221,33 @@ def test_many_rows(fp, rows, h, page, seed, group, dtype):
     assert np.array_equal(c.data.cpu().numpy(), data)        # the same rows where they were, nothing elsewhere
 
 
+def test_read_to_e4m3_divides_by_the_scale(fp):
+    """Scales from 2^-100 to 2^100, negative, zero, infinite and NaN: the quotient is
+    fp32's, rounded to e4m3 and saturated, in both read kernels."""
+    import torch
+    rng = np.random.default_rng(8)
+    rows, page, group = 2 ** 11, 64, 64
+    scales = np.array([0.0137, 2.0 ** -8, -0.05, 1e-3, 2.0 ** -70, 2.0 ** 70, 0.0, np.inf, np.nan, 3.1e-39], np.float32)
+    h = len(scales)
+    x = torch.from_numpy(rng.normal(size=(rows, h, 128)).astype(np.float32) * np.where(np.abs(scales) < 1e-3, 1e-3, 1)[:, None])
+    x = x.to(torch.bfloat16)
+    c = fp.QCache.empty(rows // page, page, h, group)
+    slots = i32(np.arange(rows))
+    c.write(x.cuda(), x.cuda(), slots)
+    values = torch.from_numpy(oq.read(c.data.cpu().numpy(), page, group, np.arange(rows))[0]).float()
+    s = torch.from_numpy(scales)
+    q = values / s.view(-1, 1)
+    want = q.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for n in (rows, 40):
+        out = [torch.zeros((n, h, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        c.read(slots[:n].contiguous(), *out, k_scale=s.cuda(), v_scale=s.cuda())
+        for o in out:
+            o = o.cpu()
+            nan = torch.isnan(q[:n])
+            assert ((o[nan] & 0x7f) == 0x7f).all()
+            assert torch.equal(o[~nan], want[:n][~nan])
+
+
 def test_many_rows_of_special_values(fp):
     """NaN, infinities, constants, ranges below the f16 steps and beyond fp16, in the 16-row kernels."""
     import torch
