@@ -456,17 +456,21 @@ __device__ __forceinline__ void write_half(const QCache &c, const QRows &r, int 
             return load16<FP8>(src, (long long)(row0 + 4 * i + sub) * r.stride_tok + head * r.stride_head + 16 * part,
                                4 * i + sub < n);
         };
-        // two steps a turn, with the loads two steps ahead (four steps unrolled do not fit the
-        // instruction cache; one: 141 us for 64K tokens written and read, two: 138)
-        Raw<FP8> raw = load(0), next = load(1);
+        // two steps a turn, as four unrolled do not fit the instruction cache (64K tokens of
+        // bf16 written and read: 135 us, two 127, one 135), with the loads of e4m3, half as
+        // many registers, two steps ahead (two 131 us, one 133)
+        constexpr int kAhead = FP8 ? 2 : 1;
+        Raw<FP8> raw[kAhead + 1];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) raw[i] = load(i);
 #pragma unroll 2
         for (int i = 0; i < 4; ++i) {
-            const Raw<FP8> behind = load(i + 2);
+            raw[kAhead] = load(i + kAhead);
             const int t = 4 * i + sub;
             __half s, m;
-            const uint2 code = quantise16<GROUPS, FP8>(raw, scale, zeros, &s, &m);
-            raw = next;
-            next = behind;
+            const uint2 code = quantise16<GROUPS, FP8>(raw[0], scale, zeros, &s, &m);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) raw[k] = raw[k + 1];
             unsigned char *p = img + H::code(t, part * 4);
             if (V) {                             // dims 16 part .. + 15: four rows of four
                 *reinterpret_cast<uint16_t *>(p) = (uint16_t)code.x;
@@ -592,8 +596,16 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
     });
 }
 
+// Blocks an SM.  The kernels wait for memory and for their own arithmetic in turn, so that
+// warps count for more than a few registers spilled: bf16 written at 8, 9, 10, 11, 13 blocks
+// (64K tokens, and read back) 142, 134, 133, 127, 140 us; read at 7, 8, 9, 10 (128K tokens)
+// 69, 65.5, 64, 66 us.  e4m3 written at 8, 10, 11: 131, 129, 129 us, but 5003 tokens, which
+// leave SMs unfilled, 12.6, 13.9, 14.1 us.
+template <bool FP8, bool READ>
+constexpr int rows_blocks() { return FP8 ? 8 : READ ? 9 : 11; }
+
 template <int GROUPS, bool FP8, bool READ>
-__global__ void __launch_bounds__(kWarps * 32, 8) rows_kernel(QCache c, QRows r, int *status) {
+__global__ void __launch_bounds__(kWarps * 32, (rows_blocks<FP8, READ>())) rows_kernel(QCache c, QRows r, int *status) {
     __shared__ __align__(16) unsigned char image[kWarps][Half<GROUPS, false>::kImage];
     after_previous();
     const long long unit = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
