@@ -514,7 +514,8 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
     const float scale = FP8 ? (V ? r.v_scale : r.k_scale)[head] : 1.f;
     // a scale whose quotients and remainders could leave the normal numbers is divided by plainly
     const bool plain = !(fabsf(scale) >= 0x1p-60f && fabsf(scale) <= 0x1p60f);
-    const float inverse = 1.f / scale;
+    const float inverse = 1.f / scale, zero = r.rows > 0 ? -0.f : 1.f;
+    const unsigned long long by = pair(inverse, inverse), minus = pair(-scale, -scale), zeros = pair(zero, zero);
     for_owned(c, r, w, head, [&](int row0, int n, int mine, unsigned char *chunk) {
         // target of row row0 + (lane & 15), -1 where nothing is to be written
         int to = -1;
@@ -539,7 +540,7 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
             move_tokens<GROUPS, V, false>(to >= 0 ? (unsigned long long)qcache_chunk(c, mine, head) + mine % kChunk : 0, img);
         }
         __syncwarp();
-#pragma unroll
+#pragma unroll 1                                 // registers and instruction cache again
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * i + sub, target = __shfl_sync(~0u, to, t);
             const unsigned char *p = img + H::code(t, part * 4);
@@ -554,37 +555,45 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
             }
             const __half *q = reinterpret_cast<const __half *>(img + H::step(t, part * GROUPS / 8));
             const float s = __half2float(q[0]), m = __half2float(q[16 * GROUPS]);
-            float x[16];
+            // Two codes at a time: a code 4 k bits up in the mantissa of 2^23 stands for 16^k
+            // times itself, which the step's 16^-k takes back without a rounding.
+            const unsigned long long steps[2] = {pair(s, s * 0x1p-4f), pair(s * 0x1p-8f, s * 0x1p-12f)};
+            const unsigned long long less = pair(-8388608.f, -8388608.f), low = pair(m, m);
+            unsigned long long x[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {       // a code in the low bits of 2^23
-                const float f = __uint_as_float(((code[e / 8] >> (4 * (e & 7))) & 15u) | 0x4b000000u) - 8388608.f;
-                x[e] = fmaf(s, f, m);
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t c4 = code[e / 4] >> (e & 2 ? 16 : 0), k = 8 * (e & 1);
+                const float lo = __uint_as_float((c4 & 15u << k) | 0x4b000000u), hi = __uint_as_float((c4 & 240u << k) | 0x4b000000u);
+                x[e] = fma2(steps[e & 1], add2(pair(lo, hi), less), low);
             }
             if (target < 0) continue;
             const long long at = target * r.stride_tok + head * r.stride_head + 16 * part;
             if (FP8) {
                 if (plain) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] /= scale;
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 v = unpair(x[e]);
+                        x[e] = pair(v.x / scale, v.y / scale);
+                    }
                 } else {                         // the same quotients by the rounded reciprocal (Markstein 1990)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float f = __fmul_rn(x[e], inverse);
-                        x[e] = fmaf(fmaf(-f, scale, x[e]), inverse, f);
+                    for (int e = 0; e < 8; ++e) {
+                        const unsigned long long f = fma2(x[e], by, zeros);
+                        x[e] = fma2(fma2(f, minus, x[e]), by, f);
                     }
                 }
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * e], x[4 * e + 1]), __NV_SATFINITE, __NV_E4M3) |
-                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[4 * e + 2], x[4 * e + 3]), __NV_SATFINITE,
-                                                              __NV_E4M3) << 16;
+                    y[e] = __nv_cvt_float2_to_fp8x2(unpair(x[2 * e]), __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(unpair(x[2 * e + 1]), __NV_SATFINITE, __NV_E4M3) << 16;
                 *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(out) + at) = make_uint4(y[0], y[1], y[2], y[3]);
             } else {
                 uint32_t y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+                    const float2 v = unpair(x[e]);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
                     y[e] = *reinterpret_cast<const uint32_t *>(&h);
                 }
                 uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at);
@@ -597,12 +606,14 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
 }
 
 // Blocks an SM.  The kernels wait for memory and for their own arithmetic in turn, so that
-// warps count for more than a few registers spilled: bf16 written at 8, 9, 10, 11, 13 blocks
-// (64K tokens, and read back) 142, 134, 133, 127, 140 us; read at 7, 8, 9, 10 (128K tokens)
-// 69, 65.5, 64, 66 us.  e4m3 written at 8, 10, 11: 131, 129, 129 us, but 5003 tokens, which
-// leave SMs unfilled, 12.6, 13.9, 14.1 us.
+// warps count for more than a few registers spilled.  bf16 written at 8, 9, 10, 11, 13 blocks
+// (64K tokens, and read back): 142, 134, 133, 127, 140 us; e4m3 at 8, 10, 11: 131, 129, 129 us,
+// but 5003 tokens, which leave SMs unfilled: 12.6, 13.9, 14.1 us.  Read at 8, 9, 10, 11, 14
+// blocks, 128K tokens to bf16: 66.7, 64.2, 64.0, 62.7, 73 us; 51327 tokens to e4m3: 49.4, 47.5,
+// 47.7, 48.9, 58 us, 64K: 68, 66, 64, 63, 81 us.  (A warp that takes several heads in turn, the
+// next one's loads ahead, has to spill for it: 63 us for 128K tokens, 133 us for 64K written.)
 template <bool FP8, bool READ>
-constexpr int rows_blocks() { return FP8 ? 8 : READ ? 9 : 11; }
+constexpr int rows_blocks() { return READ ? (FP8 ? 10 : 11) : FP8 ? 8 : 11; }
 
 template <int GROUPS, bool FP8, bool READ>
 __global__ void __launch_bounds__(kWarps * 32, (rows_blocks<FP8, READ>())) rows_kernel(QCache c, QRows r, int *status) {
