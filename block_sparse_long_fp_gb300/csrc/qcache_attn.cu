@@ -327,6 +327,12 @@ __device__ __forceinline__ void load_halves(const unsigned char *p, float out[NG
     }
 }
 
+// a / b of two that are not negative.  A division of 64 bits is a call of some 100
+// dependent instructions, and a block's start would have six of them.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 template <int NG, int NT>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel(QAttn a, Scratch sc) {
     constexpr int kCols = 8 * NT, kBytes = 2 * kCodeBytes + 128 * NG, kStages = stages<NT>();
@@ -362,7 +368,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
     const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0 && !a.whole) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
-    const long long first = (long long)blockIdx.x * total / blocks, end = (long long)(blockIdx.x + 1) * total / blocks;
+    // the first `longer` blocks have `share` + 1 units, the others `share`
+    const long long share = quotient(total, blocks);
+    const int longer = (int)(total - share * blocks);
+    const long long first = blockIdx.x * share + min((int)blockIdx.x, longer), end = first + share + ((int)blockIdx.x < longer);
     if (low <= first && first < low + n) {
         int r = tid * each;
         if (each > 1)
@@ -385,9 +394,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
         const long long full = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<NT>(NT);
         const long long last = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<NT>(octets_of(q, tiles - 1));
         const long long head = (tiles - 1) * full + last;
-        kv = (int)((first - item0) / head);
+        kv = (int)quotient(first - item0, head);
         item0 += kv * head;
-        tile = min((int)((first - item0) / full), tiles - 1);
+        tile = min((int)quotient(first - item0, full), tiles - 1);
         item0 += tile * full;
     }
     unsigned char *ring = smem + warp * kRing;
@@ -408,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
         }
         const int octets = octets_of(q, tile), weight = chunk_units<NT>(octets);
         const long long next = a.whole ? item0 + 1 : item0 + (long long)(kItem + chunks) * weight;
-        const int c0 = a.whole ? 0 : max(0, (int)((at - item0) / weight) - kItem);
-        const int c1 = a.whole ? chunks : max(0, (int)((min(end, next) - item0) / weight) - kItem);
+        const int c0 = a.whole ? 0 : max(0, (int)((uint32_t)(at - item0) / weight) - kItem);    // an item is below 2^30 units
+        const int c1 = a.whole ? chunks : max(0, (int)((uint32_t)(min(end, next) - item0) / weight) - kItem);
         if (c1 <= c0) {                           // the range ends inside the item's start
             at = item0 = next;
             ++tile;
@@ -781,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel
         }
         if (opens && !closes && tid == 0) {
             const long long last = next - 1;                 // and the block that has it
-            const int b = (int)(((last + 1) * blocks - 1) / total);
+            const long long ends = longer * (share + 1);       // of the longer blocks
+            const int b = (int)(last < ends ? quotient(last, share + 1) : longer + quotient(last - ends, share));
             sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv, tile};
         }
         __syncthreads();
