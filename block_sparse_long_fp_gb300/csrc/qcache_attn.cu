@@ -55,7 +55,7 @@ constexpr int kMinChunks = 2 * kWarps;       // least work worth a thread block
 // chunk costs by the octets of columns in use (extracting the codes is most of it; with
 // one octet at most there is nothing to tell apart).
 template <int NT>
-constexpr int item_chunks() { return NT == 1 ? 24 : NT == 2 ? 28 : 32; }
+constexpr int item_chunks() { return NT == 1 ? 24 : NT == 2 ? 28 : 40; }
 template <int NT>
 __device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 + octets; }
 // Longest cache, by the width of its table, that is not cut.  64 requests of up to 1024
@@ -80,9 +80,12 @@ struct Scratch {
     float *o;                                // [blocks][2][cols][kHeadDim]
 };
 
-// Blocks per SM (by their registers: 128, 168 and 255 a thread for 4, 3 and 2) and copies ahead.
-template <int NG, int NT>
-constexpr int blocks_per_sm() { return NT == 1 ? 4 : NT == 2 ? (NG == 4 ? 3 : 4) : 2; }
+// Blocks per SM, by their registers (168 a thread for 3, 255 for 2), and copies ahead.  8
+// columns, 64 requests up to 16384 tokens / one of 262144 / 256 up to 2048: 62 / 61 / 75 us;
+// with 4 blocks 66 / 66 / 73, with 2 66 / 61 / 103, with 3 and 6 copies 65 / 65 / 78.  16
+// columns, 32 requests up to 8192: 53 us; with 4 blocks, which spill, 59, with 2 55.
+template <int NT>
+constexpr int blocks_per_sm() { return NT == 1 ? 3 : NT == 2 ? 3 : 2; }
 template <int NT>
 constexpr int stages() { return NT == 4 ? 8 : 4; }
 
@@ -334,7 +337,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 template <int NG, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<NG, NT>()) attn_kernel(QAttn a, Scratch sc) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAttn a, Scratch sc) {
     constexpr int kCols = 8 * NT, kBytes = 2 * kCodeBytes + 128 * NG, kStages = stages<NT>();
     constexpr int kRing = kStages * kBytes, kItem = item_chunks<NT>();
     constexpr bool kSharedQ = NT > 1;          // queries' fragments in shared memory instead of registers
@@ -898,10 +901,8 @@ int tile_columns(const QAttn &a) {
 }
 
 int blocks_of(const QAttn &a) {
-    const int cols = tile_columns(a), ng = a.c.groups;
-    const int per_sm = cols == 8    ? blocks_per_sm<4, 1>()
-                       : cols == 16 ? (ng == 4 ? blocks_per_sm<4, 2>() : blocks_per_sm<1, 2>())
-                                    : blocks_per_sm<4, 4>();
+    const int cols = tile_columns(a);
+    const int per_sm = cols == 8 ? blocks_per_sm<1>() : cols == 16 ? blocks_per_sm<2>() : blocks_per_sm<4>();
     // no more than the longest lengths that the table can hold would use
     const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
     const double items = (double)a.c.h_kv * (rows * a.g / cols + a.batch);
