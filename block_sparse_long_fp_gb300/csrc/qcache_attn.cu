@@ -895,9 +895,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch 
 }
 
 // The narrowest tile that holds a kv head's (query, head) pairs, or the widest.
+// Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32.
+// Where the rows differ, what most of them fill, by the mean that the host knows: 32
+// requests up to 8192 of 4 heads a kv head, with 1 to n tokens each, take with tiles of 8, 16
+// and 32 columns 37, 41, 49 us (n = 2), 44, 46, 53 (3), 51, 48, 57 (4), 76, 65, 71 (8),
+// 123, 98, 100 (16); all with 6 tokens 83 with 16 and 70 with 32, with 8 92 and 87.
 int tile_columns(const QAttn &a) {
-    const long long cols = (long long)a.max_q * a.g;
-    return cols <= 8 ? 8 : cols <= 16 ? 16 : 32;
+    const long long cols = (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
+    const bool ragged = a.cu && a.total_q != (long long)a.batch * a.max_q;
+    if (cols <= 8 || (ragged && all <= 8ll * a.batch)) return 8;
+    return cols <= 16 || (ragged && all <= 32ll * a.batch) ? 16 : 32;
 }
 
 int blocks_of(const QAttn &a) {

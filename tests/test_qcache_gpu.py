@@ -472,6 +472,17 @@ def test_uniform_runs_of_queries(fp, lq, h_q, h, group):
     check_attn(fp, case, lens, [lq] * 3, 64, group, False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("lens,lq", [
+    ([90, 300, 5, 1, 0, 64, 33, 200], [1, 9, 1, 1, 1, 1, 1, 1]),     # 8 columns a request in the mean: 36 in tiles of 8
+    ([500, 77, 3, 161], [1, 12, 3, 5]),                              # 21: 48 in tiles of 16
+    ([40, 610, 6], [6, 6, 6])])                                      # rows that do not differ: 24 in a tile of 32
+def test_tiles_by_what_most_requests_fill(fp, lens, lq, group, dtype):
+    case = attn_case(31 + sum(lq), lens, lq, 8, 2, 32, group, dtype)
+    check_attn(fp, case, lens, lq, 32, group, True)
+
+
 def test_more_requests_than_a_block_scans_at_once(fp):
     """Ragged rows of 300 requests, some without rows and some without tokens, and the blocks' cuts among them."""
     rng = np.random.default_rng(21)
