@@ -33,13 +33,11 @@
 //
 // Bounds.  One octet of columns: memory, with about 270 instructions a chunk (88 of them
 // take codes apart) that leave little slack: 64 requests of up to 16384 tokens (32/4 heads,
-// groups of 32) 66 us, one of 262144 (32/8) 66 us, 5.0 TB/s each, 0.74 of the measured
-// copy rate.  Timer stamps inside one block set: 4 us to the first chunk, then 7 TB/s until
-// the first blocks end at 39 us, the last at 60 (SMs of some GPCs get an eighth less of a
-// saturated memory, and an SM's warps end 8 us apart), 4 us to join.  More octets: each adds
-// about 85 instructions a chunk, and the registers leave two blocks an SM; 32 columns (8
-// tokens of 4 heads) over 32 requests of 4096 on average: 88 us, where the products alone
-// need 33.
+// groups of 32) 62 us, one of 262144 (32/8) 61 us, 5.4 TB/s each, 0.8 of the measured copy
+// rate; 4 us of it pass before the first chunk and 4 in the join.  More octets: each adds
+// about 85 instructions a chunk, and a warp's instructions follow each other at 5 to 8 cycles
+// whatever the occupancy that the registers leave.  16 columns (4 tokens of 4 heads) over 32
+// requests of 4096 on average: 53 us, 32 columns: 87 us, where the products alone need 33.
 #include <type_traits>
 
 #include "qcache.cuh"
