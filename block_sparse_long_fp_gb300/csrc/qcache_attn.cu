@@ -810,7 +810,7 @@ constexpr int kJoinWarps = 8;
 template <int NT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch sc, int blocks) {
     constexpr int kCols = 8 * NT;
-    constexpr int kMost = kSm * 4, kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+    constexpr int kMost = kSm * blocks_per_sm<1>(), kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
     __shared__ Open list[kMost];
     __shared__ int first[kMost], count[kEach][kJoinWarps];
     __shared__ float4 part_o[kJoinWarps][32];
