@@ -3,9 +3,9 @@
 //
 // Both are bound by memory where there are many rows: per (token, head) 512 bytes of bf16
 // on one side and 128 + 1024 / G bytes of cache on the other.  65536 tokens of 8 heads
-// (groups of 32) are written in 72 us, 4.9 TB/s, 0.72 of the measured copy rate (two thirds
-// of the issue slots go to the quantisation), and 131072 of 4 heads read in 65 us, 5.4 TB/s,
-// 0.80.  Few rows are bound by the latency of one dependent chain (slot, row, extremes,
+// (groups of 32) are written in 64 us, 5.5 TB/s, 0.81 of the measured copy rate (three
+// quarters of the issue slots go to the quantisation), and 131072 of 4 heads read in 63 us,
+// 5.6 TB/s, 0.83.  Few rows are bound by the latency of one dependent chain (slot, row, extremes,
 // store), 2 us, and take a warp per (row, kv head): four dims per lane, so that a group of G
 // dims is G / 4 neighbouring lanes and its extremes take log2(G / 4) shuffles.
 #include <type_traits>
