@@ -373,7 +373,8 @@ fp_status fp_dense_attn(const fp_problem *p, const fp_params *prm, void *out, fl
  * too.  A page id outside [0, num_pages) in either list gives slots of -1 and
  * the status.
  * seqlens_k may be seqlens, and free_next free_head: the step then advances
- * them in place (and runs in one thread block).
+ * them in place, whatever the capacity (and runs in one thread block, which is
+ * for steps of few tokens: 524288 take 327 us, and 8 us with arrays apart).
  * ------------------------------------------------------------------------- */
 typedef struct {
     int batch;                    /* 1 .. FP_TABLES_MAX_BATCH */

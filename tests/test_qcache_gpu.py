@@ -876,3 +876,29 @@ def test_two_threads_share_a_cache(fp):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# -- the tables of many tokens, and batches at the default limit of shared memory ---------------
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("batch,old_max,new_max,page,capacity", [
+    (64, 3000, 2600, 64, 100003), (1, 0, 90000, 16, 90001), (2000, 60, 80, 32, 120000), (5, 70000, 30000, 384, 160007)])
+def test_page_tables_of_many_tokens(fp, batch, old_max, new_max, page, capacity, in_place):
+    """More than 77824 tokens, which the kernel takes eight a thread; capacities that are no multiple of 8."""
+    table, old, new, free, pool, cap = tables_case(batch + page, batch, old_max, new_max, page)
+    check_tables(fp, table, old, new, free, 2, page, pool, max(cap, capacity), in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_page_tables_of_many_tokens_refuse_what_they_cannot_serve(fp, in_place):
+    table, old, new, free, pool, cap = tables_case(12, 40, 2000, 6000, 32)
+    assert cap > 77829 + 8
+    check_tables(fp, table, old, new, free[:len(free) // 2], 2, 32, pool, cap, in_place)     # the free list runs out
+    check_tables(fp, table, old, new, free, 2, 32, pool, 77829, in_place)                    # the slot map runs out
+    check_tables(fp, table[:, :100], old, new, free, 2, 32, pool, cap, in_place)             # the table is too narrow
+    bad = new.copy()
+    bad[[3, 17]] = -1, 2 ** 31 - 1
+    check_tables(fp, table, old, bad, free, 2, 32, pool, cap, in_place)
+    bad = free.copy()
+    bad[5] = pool
+    check_tables(fp, table, old, new, bad, 2, 32, pool, cap, in_place)
