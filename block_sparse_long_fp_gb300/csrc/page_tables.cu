@@ -186,7 +186,7 @@ cudaError_t launch_page_tables(const fp_tables &t, int *status, cudaStream_t st)
     if (grid > 2 * 152) grid = 2 * 152;
     const size_t smem = (size_t)t.batch * sizeof(Plan);
     const auto kernel = tokens == 1 ? tables_kernel<1> : tables_kernel<8>;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {      // the limit without leave is 48 KB, with the static part of 528 bytes
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    FP_TABLES_MAX_BATCH * (int)sizeof(Plan));
         if (e != cudaSuccess) return e;

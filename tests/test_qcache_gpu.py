@@ -902,3 +902,23 @@ def test_page_tables_of_many_tokens_refuse_what_they_cannot_serve(fp, in_place):
     bad = free.copy()
     bad[5] = pool
     check_tables(fp, table, old, new, bad, 2, 32, pool, cap, in_place)
+
+
+def test_page_tables_of_any_batch_in_a_fresh_process(fp):
+    """The scan's 16 bytes a request and the kernel's own arrays pass 48 KB together at 3040
+    requests.  A process that has had no larger batch takes them all the same."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import test_qcache_gpu as t\n"
+            "from block_sparse_long_fp_gb300 import fprefill as fp\n"
+            "for batch in (3039, 3040, 3060, 3072, 3073):\n"
+            "    for in_place in (False, True):\n"
+            "        table, old, new, free, pool, cap = t.tables_case(batch, batch, 5, 3, 16)\n"
+            "        for capacity in (cap, 77900):\n"
+            "            t.check_tables(fp, table, old, new, free, 2, 16, pool, capacity, in_place)\n")
+    path = os.pathsep.join([root, os.path.join(root, "tests")] + [p for p in [os.environ.get("PYTHONPATH")] if p])
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, PYTHONPATH=path), capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
