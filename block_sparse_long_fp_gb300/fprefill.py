@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 from ctypes import POINTER, Structure, c_float, c_int, c_longlong, c_size_t, c_uint64, c_void_p
 
 import numpy as np
@@ -485,7 +486,7 @@ class QCache(_OnDevice):
             raise FprefillError(FP_ERR_INVALID, f"data: [pages, heads, {c.page_size // 16}, {self.chunk_bytes(group)}] "
                                 f"wanted, got {tuple(data.shape)}")
         self.data, self.h_kv, self.page_size, self.group = data, c.h_kv, c.page_size, c.group
-        self._scratch, self._scratch_bytes = {}, {}
+        self._scratch, self._scratch_bytes, self._lock = {}, {}, threading.Lock()
         self._bytes = bytes(c)
         self._f = self._entry("fp_qcache_write", 5), self._entry("fp_qcache_read", 5), self._entry("fp_qcache_attn", 9)
 
@@ -608,15 +609,17 @@ class QCache(_OnDevice):
     def _attn(self, args, n: int):
         """fp_qcache_attn with n bytes of scratch of the current stream: calls on
         two streams share none, and a captured call has its own, out of the
-        graph's memory."""
+        graph's memory.  The library enqueues two kernels that hand partial
+        results over in it: of threads on one stream, one enqueues at a time."""
         torch, stream = self._torch, self._stream(self._index)
         capturing = torch.cuda.is_current_stream_capturing()
-        scratch = None if capturing else self._scratch.get(stream)
-        if scratch is None or scratch.numel() < n:
-            scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
-            if not capturing:
-                self._scratch[stream] = scratch
-        s = self._f[2](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
+        with self._lock:
+            scratch = None if capturing else self._scratch.get(stream)
+            if scratch is None or scratch.numel() < n:
+                scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
+                if not capturing:
+                    self._scratch[stream] = scratch
+            s = self._f[2](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
         if s != FP_OK:
             raise FprefillError(s, "fp_qcache_attn")
 

@@ -480,7 +480,10 @@ fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, 
  *   max_pages_per_seq * page_size or above 2^31 - 64 reads as an empty cache; query rows outside
  *   [0, total_q) are left out: each sets the status.
  *   scratch: fp_qcache_attn_scratch_bytes() bytes (partial results of requests
- *   that several thread blocks share); it holds nothing between calls.
+ *   that several thread blocks share); it holds nothing between calls.  A call
+ *   enqueues two kernels that hand these over: calls that may run at once, or
+ *   that two threads enqueue on one stream with no lock around each call, need
+ *   scratch of their own.
  *   max_q is the callers' bound of lq_r, which picks the kernel's tile: the
  *   result does not depend on it beyond rounding.  Long chunks (lq_r in the
  *   hundreds) are better served by fp_qcache_read and the prefill kernels.

@@ -922,3 +922,30 @@ def test_page_tables_of_any_batch_in_a_fresh_process(fp):
     r = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, PYTHONPATH=path), capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_two_threads_on_one_stream_share_a_cache(fp):
+    """Both threads on the default stream, where the calls share scratch: batches, rows and columns
+    that differ, long enough to be cut."""
+    import threading
+    import torch
+    data, table, q, q32, _ = attn_case(9, [3000, 700], [3, 3], 16, 2, 64, 32)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 64, 32)
+    bt, ln = i32(table), i32([3000, 700])
+    calls = [(q, bt, ln, 3), (q[:2].contiguous(), bt, ln, 1), (q[:1].contiguous(), bt[:1].contiguous(), ln[:1].contiguous(), 1)]
+    want = [tuple(t.clone() for t in c.attn(x, b, n, max_q=m)) for x, b, n, m in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(call, w):
+        x, b, n, m = call
+        for _ in range(200):
+            got = c.attn(x, b, n, max_q=m)
+            if not all(torch.equal(a, y) for a, y in zip(got, w)):
+                wrong.append(m)
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and c.device_status() == 0

@@ -132,6 +132,34 @@ def test_python_refuses_host_tensors(fp):
         fp.QCache.empty(1, 64, 1, group=48, device="cpu")
 
 
+def test_one_call_at_a_time_fills_a_streams_scratch(fp):
+    """The attention enqueues two kernels that hand partial results over in scratch.  Two threads
+    on one stream share it, so that no second call may come between a first one's kernels."""
+    import threading
+    import time
+    import types
+    import torch
+    c = object.__new__(fp.QCache)
+    cuda = types.SimpleNamespace(is_current_stream_capturing=lambda: False)
+    busy, met = set(), []
+
+    def entry(*args):                          # stands in for the library: enqueues, waits, enqueues
+        scratch = args[-5]
+        met.append(scratch in busy)
+        busy.add(scratch)
+        time.sleep(0.002)
+        busy.discard(scratch)
+        return fp.FP_OK
+    c.__dict__.update(_torch=types.SimpleNamespace(cuda=cuda, empty=torch.empty, uint8=torch.uint8), device="cpu", _index=0,
+                      _stream=lambda index: 7, _scratch={}, _lock=threading.Lock(), _f=(None, None, entry), _ws_ptr=P)
+    threads = [threading.Thread(target=lambda: [c._attn((b"", b"", P, 0), 1000) for _ in range(20)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(met) == 80 and not any(met)
+
+
 # -- pins of the oracle ---------------------------------------------------------
 
 @pytest.mark.parametrize("group", [32, 64, 128])
