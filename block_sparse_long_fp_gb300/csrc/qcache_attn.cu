@@ -38,6 +38,8 @@
 // about 85 instructions a chunk, and a warp's instructions follow each other at 5 to 8 cycles
 // whatever the occupancy that the registers leave.  16 columns (4 tokens of 4 heads) over 32
 // requests of 4096 on average: 53 us, 32 columns: 87 us, where the products alone need 33.
+#include <limits.h>
+
 #include <type_traits>
 
 #include "qcache.cuh"
@@ -610,6 +612,42 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                     vm[h] &= keep;
 #pragma unroll
                     for (int g = 0; g < NG; ++g) vs[g][h] &= keep;
+                }
+            }
+            if (kEdge) {
+                // A weight of zero does not keep a NaN out of a product, so what is not finite (all
+                // ones in an fp16's exponent: the top bit of each half) leaves the operands here, and
+                // the columns that attend such a token get their NaN in its group's minima.
+                const auto not_finite = [](uint32_t w) { return ((w & 0x7fff7fffu) + 0x04000400u) & 0x80008000u; };
+                const auto halves = [](uint32_t top_bits) { return (top_bits >> 15) * 0xffffu; };
+                uint32_t lost = not_finite(vm[0]) | not_finite(vm[1]);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) lost |= not_finite(vs[g][0]) | not_finite(vs[g][1]);
+                if (__any_sync(~0u, lost)) {
+                    int first = INT_MAX;          // such token of group r8
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int tok = t0 + 8 * h + 2 * j4;
+                        lost = not_finite(vm[h]);
+                        vm[h] &= ~halves(lost);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const uint32_t x = not_finite(vs[g][h]);
+                            vs[g][h] &= ~halves(x);
+                            if (g == r8) lost |= x;
+                        }
+                        if (lost >> 31) first = min(first, tok + 1);
+                        if (lost & 0x8000u) first = min(first, tok);
+                    }
+                    first = min(first, __shfl_xor_sync(~0u, first, 1));
+                    first = min(first, __shfl_xor_sync(~0u, first, 2));
+                    if (r8 < NG) {
+#pragma unroll
+                        for (int t = 0; t < L; ++t)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (first < keys_of(t, c)) z[t][c] = __int_as_float(0x7fffffff);
+                    }
                 }
             }
 #pragma unroll

@@ -473,9 +473,10 @@ fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, 
  *   [h_q, total_q], natural log; may be NULL).
  *   Rows behind the last request, up to total_q, are left as they were.
  *   Queries are finite and below 2^115 in magnitude; a NaN or an infinity makes
- *   its row NaN.  So does a NaN that the cache keeps in a key that the row attends,
- *   or in a value that any row of its request in the call does (a weight of zero
- *   times NaN is NaN); what lies behind a request's last token may be anything.
+ *   its row NaN.  So does a NaN that the cache keeps in a key that the row attends;
+ *   in a value that it attends, it makes the dims of the NaN's group NaN.  Keys and
+ *   values that a row does not attend -- later tokens of its request, what lies behind
+ *   the last one -- may be anything.
  *   A page id outside [0, num_pages) reads as zeros; a length below 0, above
  *   max_pages_per_seq * page_size or above 2^31 - 64 reads as an empty cache; query rows outside
  *   [0, total_q) are left out: each sets the status.

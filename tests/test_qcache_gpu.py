@@ -949,3 +949,77 @@ def test_two_threads_on_one_stream_share_a_cache(fp):
     for t in threads:
         t.join()
     assert not wrong and c.device_status() == 0
+
+
+# -- what may lie in a value that a row does not attend ------------------------------------------
+
+@pytest.mark.parametrize("value", ["nan", "inf", "nan step", "nan key"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("lens,lq,h_q,h,page", [
+    ([100, 60], [3, 2], 4, 2, 16),             # 8 columns
+    ([77, 130], [4, 4], 6, 2, 64),             # 16
+    ([300, 33], [8, 8], 8, 2, 32),             # 32
+    ([90, 16], [40, 16], 4, 2, 16)])           # several tiles, whose keys end chunks apart
+def test_values_behind_a_row_do_not_reach_it(fp, lens, lq, h_q, h, page, group, value):
+    """NaN and infinite minima, NaN steps in the last tokens' values (drafts that other rows of the
+    request come before): the rows that attend them lose the dims of their group, no other row
+    loses anything.  In a key: those rows lose everything, and the others nothing."""
+    import torch
+    data, table, q, q32, _ = attn_case(23 + sum(lq), lens, lq, h_q, h, page, group)
+    n, rng = 128 // group, np.random.default_rng(4)
+    clean = data.copy()
+    hit = []                                   # (request, token, group), of head 0
+    for r in range(2):
+        for back in sorted({0, 1, lq[r] // 2}):
+            t, g = lens[r] - 1 - back, int(rng.integers(0, n))
+            _, _, _, km, vs, vm = oq._places(t % 16, group)
+            at = (vs if value == "nan step" else km if value == "nan key" else vm)[g]
+            data[table[r, t // page], 0, t % page // 16, at:at + 2] = [0, 0x7c if value == "inf" else 0x7e]
+            hit.append((r, t, g))
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    cu = i32(np.concatenate([[0], np.cumsum(lq)]))
+    wide = np.full((2, max(table.shape[1], 1 + 1024 // page)), 10 ** 6)
+    wide[:, :table.shape[1]] = table
+    ref_o, ref_lse = oq.attention(q32, clean, page, group, table, lens, lq)
+    tol_o, tol_lse = tolerances(q32, clean, group, ref_o, ref_lse, 128 ** -0.5)
+    lost = np.zeros(ref_o.shape, bool)
+    for r, t, g in hit:
+        for i in range(lq[r]):
+            if lens[r] - lq[r] + i >= t:
+                lost[sum(lq[:r]) + i, :h_q // h, slice(None) if value == "nan key" else slice(g * group, (g + 1) * group)] = True
+    assert lost.any() and not lost.all()
+    for bt in (table, wide):
+        out, lse = c.attn(q, i32(bt), i32(lens), cu_seqlens_q=cu, max_q=max(lq))
+        got, got_lse = out.float().cpu().numpy(), lse.cpu().numpy()
+        assert np.array_equal(~np.isfinite(got), lost)
+        assert np.all(np.abs(got - ref_o)[~lost] <= tol_o[~lost])
+        if value == "nan key":
+            assert np.isnan(got_lse[lost[:, :, 0].T]).all()
+        live = ~lost[:, :, 0].T if value == "nan key" else np.ones(ref_lse.shape, bool)
+        assert np.array_equal(np.isneginf(got_lse[live]), np.isneginf(ref_lse[live]))
+        live &= np.isfinite(ref_lse)
+        assert np.all(np.abs(got_lse - ref_lse)[live] <= tol_lse[live])
+    assert c.device_status() == 0
+
+
+def test_infinite_values_are_written_as_the_largest_finite(fp):
+    """An infinity in a value is held as 65504, and reaches its group's dims as that."""
+    import torch
+    lens, lq = [100, 60], [2, 1]
+    data, table, q, q32, _ = attn_case(18, lens, lq, 4, 2, 16, 64)
+    c = fp.QCache(torch.from_numpy(data).cuda(), 16, 64)
+    slot = i32([table[0, 6] * 16 + 3])                                   # request 0's last token
+    k, v = (t.clone() for t in c.read(slot))
+    v[0, 1, 70], v[0, 1, 80] = float("inf"), -float("inf")
+    c.write(k, v, slot)
+    data = c.data.cpu().numpy()
+    assert oq.read(data, 16, 64, slot.tolist())[1][0, 1, 80] == -65504
+    out, lse = c.attn(q, i32(table), i32(lens), cu_seqlens_q=i32([0, 2, 3]), max_q=2)
+    ref_o, ref_lse = oq.attention(q32, data, 16, 64, table, lens, lq)
+    half = np.nan_to_num(np.ascontiguousarray(data[..., 2048:]).view(np.float16).astype(np.float64))
+    vs = half[..., 64:96].max()
+    assert vs > 4000 and np.abs(ref_o).max() > 1
+    tol_o, tol_lse = tolerances(q32, data, 64, ref_o, ref_lse, 128 ** -0.5)
+    assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
+    assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
+    assert c.device_status() == 0
