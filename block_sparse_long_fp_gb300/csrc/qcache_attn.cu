@@ -18,10 +18,14 @@
 // within 2^-29 of the row's largest), logits, weights' sums and outputs are fp32,
 // weights are fp16 (2^-11 each, as is their product with a step).
 //
-// Weights are exp2(logit - m + koff), m a maximum that only follows when the
-// logits pass it by 4 (a warp vote), koff = 11 - e, 2^e (e >= 1) above every V
-// step so far: weight times step stays below 2^15, and what fp16 flushes is
-// below 2^-35 of the largest weight, or 2^-31 of an output a token.
+// Weights are exp2(logit - m + 10), m a maximum that only follows when the logits pass
+// it by 4 (a warp vote), so that the largest weight so far is between 2^10 and 2^14.  V
+// steps meet them times a power of two of their group, which sums take back at the item's
+// end and which only falls: where a step times it would reach 2, it is set anew, to bring
+// the group's largest of that chunk to 2^-2 .. 2^-1, and the group's sums with it.  Weight
+// times step stays below 2^15, and fp16 flushes weights below 2^-35 of the largest, and
+// products below 2^-33 of the largest weight times its group's largest step, whatever the
+// steps of the other groups are.
 //
 // Work.  The (request, kv head, column tile) items laid end to end, each as long as its
 // start and end cost plus its chunks of 16 tokens, are cut into equal ranges, one per
@@ -37,7 +41,7 @@
 // rate; 4 us of it pass before the first chunk and 4 in the join.  More octets: each adds
 // about 85 instructions a chunk, and a warp's instructions follow each other at 5 to 8 cycles
 // whatever the occupancy that the registers leave.  16 columns (4 tokens of 4 heads) over 32
-// requests of 4096 on average: 53 us, 32 columns: 87 us, where the products alone need 33.
+// requests of 4096 on average: 53 us, 32 columns: 92 us, where the products alone need 33.
 #include <limits.h>
 
 #include <type_traits>
@@ -63,6 +67,7 @@ __device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 
 // launch less.  Up to 2048, four requests: 18.1 and 11.2 us.
 constexpr int kWholeChunks = 64;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTop = 10.f, kSlack = 4.f;   // log2 of the largest weight, where its maximum is set and where it follows
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kOutStride = kHeadDim + 4;     // floats per column of a warp's result in shared memory
 
@@ -151,6 +156,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     const __half2 h = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+// The exponent of a power of two in fp16 (both halves alike), and the pair of one.
+__device__ __forceinline__ int exponent_of(uint32_t x) {
+    return (__float_as_int(__half2float(__ushort_as_half((unsigned short)x))) >> 23) - 127;
+}
+__device__ __forceinline__ uint32_t power_pair(int e) { return pack_half2(pow2f(e), pow2f(e)); }
+__device__ __forceinline__ uint32_t shared_word(uint32_t at) {
+    uint32_t x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
+    return x;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -510,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
         float z[NT][4];                           // the minima's part, a row per group
         float base[NT][2];                        // log2 of what weight 1 stands for (-inf: no key yet)
         float sum[NT][2];                         // this lane's share of the weights
-        float koff = 10.f;
-        uint32_t v_limit = 0x40004000u;           // every V step so far is below it: 2^e, koff = 11 - e, e >= 1
+        uint32_t up[NG];                          // what a group's V steps are multiplied by, as a pair
+#pragma unroll
+        for (int g = 0; g < NG; ++g) up[g] = 0x78007800u;             // 2^15
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -651,7 +667,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 }
             }
 #pragma unroll
-            for (int g = 0; g < NG; ++g) any_step |= vs[g][0] | vs[g][1];
+            for (int g = 0; g < NG; ++g) {
+                vs[g][0] = mul_half2(vs[g][0], up[g]);
+                vs[g][1] = mul_half2(vs[g][1], up[g]);
+                any_step |= vs[g][0] | vs[g][1];
+            }
 
             // weights
             float y[L][4], top = -INFINITY;
@@ -674,46 +694,58 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, y[t][e]);
-            // a maximum to follow, or steps of 2 and more (bit 14 of an fp16 that is >= 0)
-            if (__any_sync(~0u, top > koff + 4.f || (any_step & 0x40004000u))) {
-                uint32_t v_top = 0;
+            // a maximum to follow, or scaled steps of 2 and more (bit 14 of an fp16 that is >= 0)
+            if (__any_sync(~0u, top > kTop + kSlack || (any_step & 0x40004000u))) {
+                if (__any_sync(~0u, any_step & 0x40004000u)) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) v_top = max(v_top, max(max(vs[g][0] & 0xffffu, vs[g][0] >> 16),
-                                                                    max(vs[g][1] & 0xffffu, vs[g][1] >> 16)));
-                v_top = __reduce_max_sync(~0u, v_top);
-                float koff2 = koff;
-                if (v_top >= (v_limit & 0xffffu)) {                   // the power of two above the step
-                    const int e = min((int)(v_top >> 10) - 14, 16);
-                    koff2 = 11.f - e;
-                    v_limit = e >= 16 ? 0x7fff7fffu : (uint32_t)(e + 15) * 0x04000400u;
-                }
-                if (koff2 != koff || __any_sync(~0u, top > koff + 4.f)) {
+                    for (int g = 0; g < NG; ++g) {
+                        uint32_t raw[2], most = 0;                    // the steps themselves, 0 where masked
 #pragma unroll
-                    for (int t = 0; t < L; ++t)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const bool out0 = y[t][c] == -INFINITY, out1 = y[t][c + 2] == -INFINITY;
-                            const float2 x0 = unpair(x[t][0]), x1 = unpair(x[t][1]);
-                            const float l0 = out0 ? -INFINITY : (c ? x0.y : x0.x) * factor[t][c];
-                            const float l1 = out1 ? -INFINITY : (c ? x1.y : x1.x) * factor[t][c];
-                            float m = fmaxf(l0, l1);
-#pragma unroll
-                            for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-                            const float old = base[t][c], b = fmaxf(old + koff, m) - koff2;
-                            const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
-                            base[t][c] = b;
-                            sum[t][c] *= keep;
-                            z[t][c] *= keep;
-#pragma unroll
-                            for (int d = 0; d < 8; ++d) {
-                                o[t][d][c] *= keep;
-                                o[t][d][c + 2] *= keep;
-                            }
-                            y[t][c] = out0 ? -INFINITY : l0 - b;
-                            y[t][c + 2] = out1 ? -INFINITY : l1 - b;
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t used = (vs[g][h] & 0x7fffu ? 0xffffu : 0u) | (vs[g][h] & 0x7fff0000u ? 0xffff0000u : 0u);
+                            raw[h] = shared_word(smem_addr(v_meta) + 8 * g + 4 * h) & used;
+                            most = max(most, max(raw[h] & 0x7fffu, raw[h] >> 16 & 0x7fffu));
                         }
-                    koff = koff2;
+                        const int e = (int)(__reduce_max_sync(~0u, most) >> 10) - 15;    // of the largest
+                        const int old = exponent_of(up[g]);
+                        if (e + old >= 1) {
+                            const float less = pow2f(-2 - e - old);
+                            up[g] = power_pair(-2 - e);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) vs[g][h] = mul_half2(raw[h], up[g]);
+#pragma unroll
+                            for (int t = 0; t < L; ++t)
+#pragma unroll
+                                for (int m = 2 * (g * 4 / NG); m < 2 * ((g + 1) * 4 / NG); ++m)
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) o[t][m][x] *= less;
+                        }
+                    }
                 }
+#pragma unroll
+                for (int t = 0; t < L; ++t)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const bool out0 = y[t][c] == -INFINITY, out1 = y[t][c + 2] == -INFINITY;
+                        const float2 x0 = unpair(x[t][0]), x1 = unpair(x[t][1]);
+                        const float l0 = out0 ? -INFINITY : (c ? x0.y : x0.x) * factor[t][c];
+                        const float l1 = out1 ? -INFINITY : (c ? x1.y : x1.x) * factor[t][c];
+                        float m = fmaxf(l0, l1);
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+                        const float old = base[t][c], b = fmaxf(old, m - kTop);
+                        const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
+                        base[t][c] = b;
+                        sum[t][c] *= keep;
+                        z[t][c] *= keep;
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) {
+                            o[t][d][c] *= keep;
+                            o[t][d][c + 2] *= keep;
+                        }
+                        y[t][c] = out0 ? -INFINITY : l0 - b;
+                        y[t][c + 2] = out1 ? -INFINITY : l1 - b;
+                    }
             }
             uint32_t p[L][2];
 #pragma unroll
@@ -789,10 +821,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 for (int m = 0; m < 4; ++m) {
                     const float low_part = __shfl_sync(~0u, z[t][c], (m * NG / 4) * 4 + j4);
                     float4 v;
-                    v.x = fmaf(o[t][2 * m][c], 0x1p24f, low_part);
-                    v.y = fmaf(o[t][2 * m][c + 2], 0x1p20f, low_part);
-                    v.z = fmaf(o[t][2 * m + 1][c], 0x1p24f, low_part);
-                    v.w = fmaf(o[t][2 * m + 1][c + 2], 0x1p20f, low_part);
+                    const float high = pow2f(24 - exponent_of(up[m * NG / 4])), low = high * 0x1p-4f;
+                    v.x = fmaf(o[t][2 * m][c], high, low_part);
+                    v.y = fmaf(o[t][2 * m][c + 2], low, low_part);
+                    v.z = fmaf(o[t][2 * m + 1][c], high, low_part);
+                    v.w = fmaf(o[t][2 * m + 1][c + 2], low, low_part);
                     *reinterpret_cast<float4 *>(mine_o + col * kOutStride + 32 * m + 4 * r8) = v;
                 }
             }

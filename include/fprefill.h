@@ -480,6 +480,10 @@ fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, 
  *   A page id outside [0, num_pages) reads as zeros; a length below 0, above
  *   max_pages_per_seq * page_size or above 2^31 - 64 reads as an empty cache; query rows outside
  *   [0, total_q) are left out: each sets the status.
+ *   Logits, weights' sums and outputs are summed in fp32.  Weights enter the sum of
+ *   values in fp16 (2^-11 of each; nothing below 2^-35 of the row's largest), and so do
+ *   their products with a value's step (nothing below 2^-33 of the largest weight times
+ *   the largest step of that group of dims).
  *   scratch: fp_qcache_attn_scratch_bytes() bytes (partial results of requests
  *   that several thread blocks share); it holds nothing between calls.  A call
  *   enqueues two kernels that hand these over: calls that may run at once, or

@@ -1023,3 +1023,91 @@ def test_infinite_values_are_written_as_the_largest_finite(fp):
     assert np.all(np.abs(out.float().cpu().numpy() - ref_o) <= tol_o)
     assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
     assert c.device_status() == 0
+
+
+# -- steps of very different sizes in one head's groups ------------------------------------------
+
+@pytest.mark.parametrize("rows,h_q", [(1, 1), (1, 12), (2, 12)])          # 8, 16 and 32 columns
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("big", [16.0, 2000.0])
+def test_groups_of_small_steps_beside_large_ones(fp, group, big, rows, h_q):
+    """A dominant key in each of the first four chunks (a warp's share each) and a tail of weights
+    near 2^-21 of theirs, whose values are all that the first group has, at steps near 2^-11;
+    elsewhere in the head, beside the dominant keys, steps of `big`.  400 requests over the same
+    pages, so that a warp walks most of its share of a request.
+
+    Every term of the first group's sum is positive (minima of zero, no code in the dominant keys), so
+    that roundings of its terms are relative to the sum.  Counted: bf16's half step, 2^-8; the weight
+    and its product with the step in fp16, half a step 2^-11 each, and as much again for what the
+    second rounds below fp16's normal numbers; twice a logit's error (tolerances) in each weight, and
+    as much for the shared sum."""
+    import torch
+    L, page, batch = 4096, 64, 400
+    rng = np.random.default_rng(int(big) + group)
+    pages = L // page
+    table = rng.permutation(pages + 1)[None, :pages]
+    q32 = np.repeat(rng.normal(size=(1, 1, 128)), rows * h_q, 1).reshape(rows, h_q, 128)
+    q = torch.from_numpy(q32.astype(np.float32)).to(torch.bfloat16)
+    q32 = q.float().numpy()
+    scale = 1 / 12.0
+    x = q32[0, 0].astype(np.float64)
+    # keys: multiples of the query, so that scale q.k spreads around -21 ln 2 of the dominant ones' 6
+    want = 6 - 21 * np.log(2) + rng.uniform(-0.7, 0.7, L)
+    want[:64:16] = 6
+    k = (want / (scale * x @ x))[:, None, None] * x
+    v = np.zeros((L, 1, 128))
+    data = np.zeros((pages + 1, 1, page // 16, oq.chunk_bytes(group)), np.uint8)
+    t = np.arange(L)
+    slots = table[0, t // page] * page + t % page
+    v[:, 0, 0:group] = np.arange(group) % 16 * (2.0 ** -11 * rng.uniform(0.8, 1.2, (L, 1)))
+    v[:64:16, 0, :group] = 0
+    v[:, 0, group:] = rng.normal(size=(L, 128 - group))
+    v[7:64:16, 0, group:2 * group] = np.arange(group) % 16 * big
+    oq.write(data, page, group, slots, k.astype(np.float32), v.astype(np.float32))
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    out, lse = c.attn(q.cuda().repeat(batch, 1, 1), i32(np.repeat(table, batch, 0)), i32([L] * batch), max_q=rows,
+                      softmax_scale=scale)
+    ref_o, ref_lse = oq.attention(q32, data, page, group, table, [L], [rows], scale)
+    tol_o, tol_lse = tolerances(q32, data, group, ref_o, ref_lse, scale)
+    got = out.float().cpu().numpy().reshape(batch, rows, h_q, 128)
+    got_lse = lse.cpu().numpy().reshape(h_q, batch, rows).transpose(1, 0, 2)
+    assert np.all(np.abs(got - ref_o) <= tol_o) and np.all(np.abs(got_lse - ref_lse) <= tol_lse)
+    d = tol_lse.max()
+    small, ref = got[..., :group], ref_o[..., :group]
+    assert ref.max() > 2.0 ** -11 * 15 * 2.0 ** -13    # the tail, 2^-11 of all the weights, is what the group has
+    assert np.all(np.abs(small - ref) <= ref * (2.0 ** -8 + 4 * 2.0 ** -11 + 4 * d)), \
+        float((np.abs(small - ref) / np.maximum(ref, 1e-30)).max())
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("rows,h_q", [(1, 2), (1, 24), (2, 24)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_steps_that_grow_and_fall_along_a_request(fp, group, rows, h_q):
+    """Values from 2^-12 to 2^12 of one, each group of dims by a course of its own."""
+    import torch
+    L, page, h = 700, 64, 2
+    data, table, q, q32, _ = attn_case(14, [L], [rows], h_q, h, page, group, poison=False, q_scale=0.3)
+    rng = np.random.default_rng(15)
+    t = np.arange(L)
+    v = rng.normal(size=(L, h, 128)) + 0.5
+    for g in range(128 // group):
+        course = 12 * np.sin(t / (40 + 25 * g) + 2 * g)
+        v[:, 0, g * group:(g + 1) * group] *= 2.0 ** course[:, None]
+        v[:, 1, g * group:(g + 1) * group] *= 2.0 ** -course[::-1, None]
+    slots = table[0, t // page] * page + t % page
+    k = oq.read(data, page, group, slots)[0]
+    oq.write(data, page, group, slots, k.astype(np.float32), v.astype(np.float32))
+    out, lse = check_attn(fp, (data, table, q, q32, None), [L], [rows], page, group, False)
+    # each group by its own steps: a group that others' tolerance would hide
+    ref_o, ref_lse = oq.attention(q32, data, page, group, table, [L], [rows])
+    got = out.float().cpu().numpy()
+    half = np.ascontiguousarray(data[..., 2048:]).view(np.float16).astype(np.float64)
+    n = 128 // group
+    bounds = [np.abs(half[..., i * 16 * n:(i + 1) * 16 * n]).max() for i in (0, 1)]
+    x = oq.read(data, page, group, slots)[1]
+    for a in range(h):
+        for g in range(n):
+            dims, heads = slice(g * group, (g + 1) * group), slice(a * h_q // h, (a + 1) * h_q // h)
+            span = np.abs(x[:, a, dims]).max()
+            tol = tolerances(q32, data, group, ref_o, ref_lse, 128 ** -0.5, (*bounds, 2 * span / 15, span))[0]
+            assert np.all(np.abs(got - ref_o)[:, heads, dims] <= tol[:, heads, dims])
