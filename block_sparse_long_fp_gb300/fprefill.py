@@ -557,7 +557,9 @@ class QCache(_OnDevice):
         block_table int32 [batch, max_pages], seqlens_k int32 [batch] (the
         queries' own tokens included).  Request r owns rows cu_seqlens_q[r] ..
         cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
-        cu_seqlens_q, max_q rows each (total_q / batch by default)."""
+        cu_seqlens_q, max_q rows each (by default total_q / batch, which has to
+        be a whole number).  Rows behind the last request's are not written:
+        in an `out` of this call's own they are what the memory held."""
         torch, dev, h_kv = self._torch, self._index, self.h_kv
         shape, strides = q.shape, q.stride()
         kinds = self._bf16 if q_scale is None else self._fp8
@@ -576,6 +578,9 @@ class QCache(_OnDevice):
         width = block_table.shape[1]
         cu_at = 0 if cu_seqlens_q is None else self._vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
         if max_q is None:
+            if cu_seqlens_q is None and batch and total_q % batch:
+                raise FprefillError(FP_ERR_INVALID, f"{total_q} rows are no equal share of {batch} requests: cu_seqlens_q or "
+                                    "max_q wanted")
             max_q = max(1, total_q // batch if batch and cu_seqlens_q is None else total_q)
         stride_head = strides[1] if h_q > 1 else 128
         Q = _PACK_QUERY.pack(batch, h_q, total_q, max_q, FP_BF16 if q_scale is None else FP_E4M3, q.data_ptr(),

@@ -1111,3 +1111,20 @@ def test_steps_that_grow_and_fall_along_a_request(fp, group, rows, h_q):
             span = np.abs(x[:, a, dims]).max()
             tol = tolerances(q32, data, group, ref_o, ref_lse, 128 ** -0.5, (*bounds, 2 * span / 15, span))[0]
             assert np.all(np.abs(got - ref_o)[:, heads, dims] <= tol[:, heads, dims])
+
+
+def test_rows_that_the_requests_do_not_share_evenly_are_refused(fp):
+    """Without offsets or max_q every request has total_q / batch rows: 7 rows of 3 requests, 2 of 3."""
+    import torch
+    c = fp.QCache.empty(4, 16, 2, 64)
+    c.data.zero_()
+    table, lens = i32([[0, 1], [2, 3], [0, 2]]), i32([5, 6, 7])
+    q = torch.zeros((7, 4, 128), dtype=torch.bfloat16, device="cuda")
+    for x in (q, q[:2]):
+        with pytest.raises(fp.FprefillError):
+            c.attn(x, table, lens)
+    out, lse = c.attn(q[:6], table, lens)
+    assert (out == 0).all() and torch.isfinite(lse).all()
+    out, lse = c.attn(q, table, lens, max_q=2, out=torch.full_like(q, 3), lse=torch.full((4, 7), 3.0, device="cuda"))
+    assert (out[:6] == 0).all() and (out[6] == 3).all() and (lse[:, 6] == 3).all()
+    assert c.device_status() == 0
