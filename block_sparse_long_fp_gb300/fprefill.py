@@ -601,6 +601,8 @@ class QCache(_OnDevice):
         key = (batch, h_q, total_q, max_q, cu_at == 0, width)
         n = self._scratch_bytes.get(key)
         if n is None:
+            if len(self._scratch_bytes) >= 512:        # a server's rows may take any number of shapes
+                self._scratch_bytes.clear()
             n = self._scratch_bytes[key] = int(
                 self._lib.fp_qcache_attn_scratch_bytes(self._c, FpQCacheQuery.from_buffer_copy(Q)))
         args = (self._bytes, Q, out.data_ptr(), 0 if lse is None else lse.data_ptr())

@@ -1128,3 +1128,15 @@ def test_rows_that_the_requests_do_not_share_evenly_are_refused(fp):
     out, lse = c.attn(q, table, lens, max_q=2, out=torch.full_like(q, 3), lse=torch.full((4, 7), 3.0, device="cuda"))
     assert (out[:6] == 0).all() and (out[6] == 3).all() and (lse[:, 6] == 3).all()
     assert c.device_status() == 0
+
+
+def test_sizes_kept_for_shapes_are_bounded(fp):
+    """A cache object remembers the scratch that a shape takes, of some hundreds of shapes."""
+    import torch
+    c = fp.QCache.empty(1, 16, 1, 128)
+    c.data.zero_()
+    table, lens, cu = i32([[0]]), i32([9]), i32([0, 1])
+    q = torch.ones((1, 1, 128), dtype=torch.bfloat16, device="cuda")
+    for max_q in range(1, 1200):
+        out, lse = c.attn(q, table, lens, cu_seqlens_q=cu, max_q=max_q)
+    assert (out == 0).all() and len(c._scratch_bytes) <= 512 and c.device_status() == 0
