@@ -62,9 +62,16 @@ template <int NT>
 constexpr int item_chunks() { return NT == 1 ? 24 : NT == 2 ? 28 : 40; }
 template <int NT>
 __device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 + octets; }
-// Longest cache, by the width of its table, that is not cut.  64 requests of up to 1024
-// tokens (32/8 heads): 18.1 us whole, 24.2 us cut; one request of 700: 9.1 and 8.1 us, but a
-// launch less.  Up to 2048, four requests: 18.1 and 11.2 us.
+// Longest cache, by the width of its table, that is not cut (one launch instead of two).
+// Microseconds whole / cut, 32/8 heads, with 8, 16, 32 columns, tables filled:
+//   up to 1024, 1 request    10.8 /  8.4   15.5 / 10.3   22.6 / 15.7
+//               16           11.0 / 13.1   15.9 / 17.4   23.0 / 26.8
+//               64           22.5 / 24.1   34.2 / 36.2   54.4 / 60.5
+//   up to 2048, 1            16.8 /  8.6   24.4 / 11.2   35.3 / 15.3
+//               16           17.1 / 15.9   24.9 / 21.3   36.5 / 34.7
+// and filled to 0.3:
+//   up to 1024, 1             6.8 /  8.2    9.4 /  9.9   13.5 / 14.9
+//   up to 2048, 1             8.7 /  7.9   12.2 / 10.1   17.4 / 14.2
 constexpr int kWholeChunks = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 10.f, kSlack = 4.f;   // log2 of the largest weight, where its maximum is set and where it follows
@@ -968,7 +975,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch 
 // Where the rows differ, what most of them fill, by the mean that the host knows: 32
 // requests up to 8192 of 4 heads a kv head, with 1 to n tokens each, take with tiles of 8, 16
 // and 32 columns 37, 41, 49 us (n = 2), 44, 46, 53 (3), 51, 48, 57 (4), 76, 65, 71 (8),
-// 123, 98, 100 (16); all with 6 tokens 83 with 16 and 70 with 32, with 8 92 and 87.
+// 123, 98, 100 (16); all with 6 tokens 83 with 16 and 73 with 32, with 8 92 and 92.  64 up to
+// 4096, most of which have one token: 63 and one of 128 90, 84, 96 us, 60 and four of 64
+// 115, 102, 112, 56 and eight of 16 73, 70, 82, one token each 42, 45, 54.
 int tile_columns(const QAttn &a) {
     const long long cols = (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
     const bool ragged = a.cu && a.total_q != (long long)a.batch * a.max_q;

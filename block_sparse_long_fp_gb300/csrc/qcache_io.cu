@@ -16,8 +16,18 @@ namespace fp {
 namespace {
 
 constexpr int kWarps = 4;
-// (row, head) pairs from which on a warp takes 16 rows of a head.  25480 e4m3 pairs written
-// and read: 18.8 us a warp each, 12.9 us 16 a warp; 12288 read to e4m3: 5.5 and 8.1 us.
+// (row, head) pairs from which on a warp takes 16 rows of a head.  Microseconds with a warp a
+// pair / with 16 rows a warp, for 8 heads in groups of 32, at 4096, 8192, 16384, 32768 pairs:
+//   slots in order:  bf16 written  3.2 / 3.8   4.4 / 4.0   7.5 / 4.7  13.3 /  6.4
+//                    bf16 read     2.3 / 2.7   3.1 / 3.0   4.7 / 3.8   8.3 /  5.3
+//                    e4m3 written  3.2 / 3.3   4.8 / 3.6   8.0 / 4.4  14.5 /  6.0
+//                    e4m3 read     3.4 / 3.2   4.6 / 3.5   7.4 / 4.3  12.5 /  5.8
+//   a page each:     bf16 written  3.2 / 5.0   4.5 / 5.6   7.7 / 7.3  15.4 / 15.2
+//                    bf16 read     2.3 / 4.6   3.1 / 4.9   5.7 / 8.0  11.5 / 14.6
+//                    e4m3 written  3.2 / 4.1   4.8 / 4.4   8.0 / 5.5  15.8 / 11.8
+//                    e4m3 read     3.4 / 5.2   4.7 / 5.5   7.6 / 7.7  13.5 / 14.5
+// The host does not know the slots: the number is where single tokens of many requests stop
+// losing by it when written, above where prompts begin to gain.
 constexpr long long kManyRows = 16384;
 
 __device__ __forceinline__ void load4(const void *base, long long elem, const float *scale, int head, float x[4]) {
@@ -310,8 +320,8 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 
 // d / 15 and 1 / s as correctly rounded quotients need them: a quotient by the rounded
 // reciprocal, corrected by its fused remainder (Markstein 1990), and a Newton step on the
-// approximate reciprocal.  Equal to the division for every d of two binades (all 2^24, the
-// others scale) and for every positive fp16 s.
+// approximate reciprocal.  Equal to the division: the first for all 2^24 d of two binades
+// (the others scale), the second in every code of ties by each fp16 s, which the tests take.
 __device__ __forceinline__ float fifteenth(float d) {
     constexpr float kR = 1.f / 15.f;
     const float q = __fmul_rn(d, kR);
@@ -606,7 +616,8 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
 }
 
 // Blocks an SM.  The kernels wait for memory and for their own arithmetic in turn, so that
-// warps count for more than a few registers spilled.  bf16 written at 8, 9, 10, 11, 13 blocks
+// warps count for more than registers: the bf16 write spills 240 to 250 bytes a thread, the
+// reads 90 to 140, the e4m3 write 40.  bf16 written at 8, 9, 10, 11, 13 blocks
 // (64K tokens, and read back): 142, 134, 133, 127, 140 us; e4m3 at 8, 10, 11: 131, 129, 129 us,
 // but 5003 tokens, which leave SMs unfilled: 12.6, 13.9, 14.1 us.  Read at 8, 9, 10, 11, 14
 // blocks, 128K tokens to bf16: 66.7, 64.2, 64.0, 62.7, 73 us; 51327 tokens to e4m3: 49.4, 47.5,

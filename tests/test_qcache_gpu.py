@@ -1140,3 +1140,50 @@ def test_sizes_kept_for_shapes_are_bounded(fp):
     for max_q in range(1, 1200):
         out, lse = c.attn(q, table, lens, cu_seqlens_q=cu, max_q=max_q)
     assert (out == 0).all() and len(c._scratch_bytes) <= 512 and c.device_status() == 0
+
+
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("which", ["steps", "borders"])
+def test_quotients_of_every_step(fp, which, group):
+    """The 16-row kernel takes 1 / s and (max - min) / 15 by reciprocals and corrections of its own,
+    the other divides: both give the definition's codes, steps and minima.  One row whose heads have
+    a scale each: for every f16 step s that a positive range can have, values k s and (k + 1/2) s,
+    whose codes are ties that the last bit of 1 / s decides; and ranges within two fp32 steps of 15
+    times the border between two f16 steps, which the last bit of the quotient decides."""
+    import torch
+    rng = np.random.default_rng(6)
+    if which == "steps":
+        s = np.arange(1, 0x7c00, dtype=np.uint16).view(np.float16).astype(np.float32)
+        s = s[15 * s <= 65504]                           # the values are clamped there
+        codes = np.array([16 * k for k in range(16)] + [8 * (2 * k + 1) for k in range(8)] + [0] * 8, np.float32)
+        x = np.tile(codes, 4)[None].repeat(len(s), 0)
+        x[:, 32:] = rng.permuted(x[:, 32:], axis=1)
+        scale = s / 16
+    else:
+        f16 = np.arange(1, 0x7bff, dtype=np.uint16).view(np.float16).astype(np.float64)
+        border = (f16[:-1] + f16[1:]) / 2
+        border = rng.choice(border[15 * border < 65500], 20000, replace=False)
+        d = (15 * border).astype(np.float32)
+        d = (d.view(np.int32) + rng.integers(-2, 3, d.shape)).astype(np.int32).view(np.float32)
+        x = rng.integers(0, 16, (len(d), 128)).astype(np.float32) * 16
+        x[:, ::32], x[:, 1::32] = 0, 256
+        scale = d / 256
+    h = len(scale)
+    e4m3 = torch.from_numpy(x).to(torch.float8_e4m3fn)
+    assert torch.equal(e4m3.float(), torch.from_numpy(x)) and h >= 16384
+    x32 = (x * scale[:, None])[None]
+    data = np.zeros((1, h, 1, oq.chunk_bytes(group)), np.uint8)
+    oq.write(data, 16, group, [9], x32, x32)
+    code, step, _ = oq.quantise(x32, group)
+    if which == "steps":
+        assert np.array_equal(step[0, :, 0].astype(np.float32), s)
+    k = e4m3.view(torch.uint8)[None].cuda()
+    sc = torch.from_numpy(scale).cuda()
+    for part in (h, 10000):                              # the 16-row kernel, then the one for few rows
+        for at in range(0, h, part):
+            n = min(part, h - at)
+            c = fp.QCache(torch.zeros((1, n, 1, oq.chunk_bytes(group)), dtype=torch.uint8, device="cuda"), 16, group)
+            kk, ss = k[:, at:at + n].contiguous(), sc[at:at + n].contiguous()
+            c.write(kk, kk, i32([9]), ss, ss)
+            got = c.data.cpu().numpy()
+            assert np.array_equal(got, data[:, at:at + n]), np.nonzero((got != data[:, at:at + n]).any((0, 2, 3)))[0][:5]
