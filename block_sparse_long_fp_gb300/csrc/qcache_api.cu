@@ -56,7 +56,8 @@ fp_status check_rows(const fp_qcache *c, const fp_qcache_rows *r, bool read, QCa
     if (!r->k || !r->v || !r->slots || !aligned(r->k, 16) || !aligned(r->v, 16)) return FP_ERR_INVALID;
     if (!aligned(r->slots, 4) || !aligned(r->out_slots, 4)) return FP_ERR_INVALID;
     if (!strides_ok(r->stride_tok, r->stride_head, c->h_kv, r->dtype == FP_E4M3 ? 1 : 2)) return FP_ERR_INVALID;
-    if (r->dtype == FP_E4M3 && (!r->k_scale || !r->v_scale)) return FP_ERR_INVALID;
+    if (r->dtype == FP_E4M3 && (!r->k_scale || !r->v_scale || !aligned(r->k_scale, 4) || !aligned(r->v_scale, 4)))
+        return FP_ERR_INVALID;
     if (read && (r->out_rows < 0 || (!r->out_slots && r->out_rows < r->rows))) return FP_ERR_INVALID;
     if (r->rows > (1 << 30) || (long long)r->rows * c->h_kv > (1ll << 33)) return FP_ERR_UNSUPPORTED;
     *rows = QRows{r->k, r->v, r->stride_tok, r->stride_head, r->slots, read ? r->out_slots : nullptr, r->rows,
@@ -164,7 +165,7 @@ fp_status fp_qcache_attn(const fp_qcache *c, const fp_qcache_query *q, void *out
     if (q->total_q > 0) {
         if (!q->q || !aligned(q->q, 16) || !out || !aligned(out, 16) || !aligned(lse_opt, 4)) return FP_ERR_INVALID;
         if (!strides_ok(q->q_stride_tok, q->q_stride_head, q->h_q, q->dtype == FP_E4M3 ? 1 : 2)) return FP_ERR_INVALID;
-        if (q->dtype == FP_E4M3 && !q->q_scale) return FP_ERR_INVALID;
+        if (q->dtype == FP_E4M3 && (!q->q_scale || !aligned(q->q_scale, 4))) return FP_ERR_INVALID;
     }
     if ((s = check_ws(ws, ws_bytes)) != FP_OK) return s;
     if (!scratch || !aligned(scratch, 16) || scratch_bytes < qcache_attn_scratch_bytes(a)) return FP_ERR_WORKSPACE;

@@ -528,7 +528,8 @@ class QCache(_OnDevice):
 
     def write(self, k, v, slots, k_scale=None, v_scale=None):
         """Quantise rows of k and v (bf16 [rows, h_kv, 128], or e4m3 with one
-        scale per head) into `slots` (int32 [rows]; -1: none)."""
+        scale per head; k and v of like strides) into `slots` (int32 [rows];
+        -1: none; none twice)."""
         self._call(self._f[0], "fp_qcache_write", self._bytes, self._rows(k, v, slots, k_scale, v_scale), self._ws_ptr, FP_WS_HEADER_BYTES)
 
     def read(self, slots, k_out=None, v_out=None, out_slots=None, k_scale=None, v_scale=None):

@@ -431,7 +431,8 @@ size_t fp_qcache_bytes(const fp_qcache *c);
  *   c = min(15, max(0, rint((x' - m) * (1 / s))))   (0 where s = 0), in fp32.
  *   A NaN in a group makes its minimum NaN, so all of the group reads as NaN.
  *   k, v (device): row i, head h at  i * stride_tok + h * stride_head  elements
- *     (pointers and strides multiples of 16 bytes), dtype FP_BF16, or FP_E4M3
+ *     (pointers and strides multiples of 16 bytes, stride_head >= d,
+ *     stride_tok >= stride_head * (h_kv - 1) + d), dtype FP_BF16, or FP_E4M3
  *     codes times k_scale / v_scale [h_kv].
  *   slots (device int32 [rows]): where row i goes; -1 skips the row, another
  *     value outside the cache skips it and sets the status.  No slot may appear
@@ -500,7 +501,7 @@ typedef struct {
     int max_q;                    /* >= 1 */
     fp_dtype dtype;               /* of q */
     const void *q;                /* DEVICE [total_q, h_q, d] at the strides below */
-    long long q_stride_tok, q_stride_head;  /* elements; rows 16-byte aligned */
+    long long q_stride_tok, q_stride_head;  /* elements, as in fp_qcache_rows */
     const float *q_scale;         /* [h_q], FP_E4M3 only */
     const int *cu_seqlens_q;      /* DEVICE [batch + 1], or NULL */
     const int *seqlens_k;         /* DEVICE [batch] */

@@ -109,6 +109,16 @@ def test_attention_refusals(fp, over, code):
     assert fp.lib().fp_qcache_attn(cache(fp), query(fp, **over), P, None, P, 1 << 40, P, 256, None) == code
 
 
+def test_scales_that_are_not_aligned_are_refused(fp):
+    L = fp.lib()
+    for over in (dict(k_scale=P + 2, v_scale=P), dict(k_scale=P, v_scale=P + 1)):
+        r = rows(fp, dtype=fp.FP_E4M3, **over)
+        assert L.fp_qcache_write(cache(fp), r, P, 256, None) == fp.FP_ERR_INVALID
+        assert L.fp_qcache_read(cache(fp), r, P, 256, None) == fp.FP_ERR_INVALID
+    q = query(fp, dtype=fp.FP_E4M3, q_scale=P + 2)
+    assert L.fp_qcache_attn(cache(fp), q, P, None, P, 1 << 40, P, 256, None) == fp.FP_ERR_INVALID
+
+
 def test_workspaces_are_checked(fp):
     L = fp.lib()
     for ws, n in ((None, 256), (P, 255)):
