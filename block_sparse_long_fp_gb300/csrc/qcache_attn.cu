@@ -15,8 +15,9 @@
 // long side of the instruction and 8 columns suffice for a decode step: with
 // tokens on the short side half of every instruction would be padding.
 // Queries enter as fp16 under a power of two per row (exact for bf16 and e4m3
-// within 2^-29 of the row's largest), logits, weights' sums and outputs are fp32,
-// weights are fp16 (2^-11 each, as is their product with a step).
+// within 2^-29 of the row's largest), logits, weights' sums and outputs are fp32 (a
+// chunk's products join them by an addition of their own), weights are fp16 (2^-11 each,
+// as is their product with a step).
 //
 // Weights are exp2(logit - m + 10), m a maximum that only follows when the logits pass
 // it by 4 (a warp vote), so that the largest weight so far is between 2^10 and 2^14.  V
@@ -41,7 +42,7 @@
 // rate; 4 us of it pass before the first chunk and 4 in the join.  More octets: each adds
 // about 85 instructions a chunk, and a warp's instructions follow each other at 5 to 8 cycles
 // whatever the occupancy that the registers leave.  16 columns (4 tokens of 4 heads) over 32
-// requests of 4096 on average: 53 us, 32 columns: 92 us, where the products alone need 33.
+// requests of 4096 on average: 55 us, 32 columns: 93 us, where the products alone need 33.
 #include <limits.h>
 
 #include <type_traits>
@@ -149,6 +150,16 @@ __device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
     float_pair y;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
     return y;
+}
+// Sums over the length are added in fp32, rounded to nearest: chained on the tensor cores,
+// which cut the bits below their largest term off, they lose some 2^-25 of themselves a
+// product, always towards zero.  Codes are positive and minima make up for it, so that the
+// outputs of 262144 tokens in one block, of values of zero mean, were off by 0.023 of
+// themselves, and are by 0.002 now, the output's own rounding.
+__device__ __forceinline__ void add_to(float &a, float &b, float x, float y) {
+    const float2 v = unpair(add2(pair(a, b), pair(x, y)));
+    a = v.x;
+    b = v.y;
 }
 // Transpose of the 8 x 8 fp16 matrix whose row lane / 4 holds the lane's pair.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                                         : __shfl_sync(~0u, qs[kSharedQ ? 0 : t].factor, (2 * j4 + e) * 4);
 
         float o[NT][8][4];                        // O^T: 8 tiles of 16 dims
-        float z[NT][4];                           // the minima's part, a row per group
+        float z[NT][2];                           // the minima's part, a row per group
         float base[NT][2];                        // log2 of what weight 1 stands for (-inf: no key yet)
         float sum[NT][2];                         // this lane's share of the weights
         uint32_t up[NG];                          // what a group's V steps are multiplied by, as a pair
@@ -541,8 +552,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
             for (int m = 0; m < 8; ++m)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][m][e] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[t][e] = 0.f;
+            z[t][0] = z[t][1] = 0.f;
             base[t][0] = base[t][1] = -INFINITY;
             sum[t][0] = sum[t][1] = 0.f;
         }
@@ -764,7 +774,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                 sum[t][1] = v.y;
                 p[t][0] = transpose8(pack_half2(y[t][0], y[t][1]));
                 p[t][1] = transpose8(pack_half2(y[t][2], y[t][3]));
-                mma16(z[t], vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
+                float low[4];
+                mma16_zero(low, vm[0], 0, vm[1], 0, p[t][0], p[t][1]);
+                add_to(z[t][0], z[t][1], low[0], low[1]);
             }
 
             // values
@@ -786,9 +798,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                        for (int t = 0; t < L; ++t)
-                            mma16(o[t][2 * m + u], wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu,
-                                  wb & 0x00f000f0u, ps[t][0], ps[t][1]);
+                        for (int t = 0; t < L; ++t) {
+                            float v[4], *sums = o[t][2 * m + u];
+                            mma16_zero(v, wa & 0x000f000fu, wa & 0x00f000f0u, wb & 0x000f000fu, wb & 0x00f000f0u, ps[t][0],
+                                       ps[t][1]);
+                            add_to(sums[0], sums[1], v[0], v[1]);
+                            add_to(sums[2], sums[3], v[2], v[3]);
+                        }
                         wa >>= 8;
                         wb >>= 8;
                     }

@@ -1187,3 +1187,45 @@ def test_quotients_of_every_step(fp, which, group):
             c.write(kk, kk, i32([9]), ss, ss)
             got = c.data.cpu().numpy()
             assert np.array_equal(got, data[:, at:at + n]), np.nonzero((got != data[:, at:at + n]).any((0, 2, 3)))[0][:5]
+
+
+@pytest.mark.parametrize("rows,h_q", [(1, 8), (2, 8), (4, 8)])            # tiles of 8, 16 and 32 columns
+def test_sums_of_a_long_request_in_one_block(fp, rows, h_q):
+    """456 requests of 262144 tokens over the same pages, which leaves each to a block or two, of
+    values of zero mean: what the codes add up to is 300 times the output, and the minima take it
+    back.  Counted in each element: bf16's half step, 2^-8.  Two roundings of each weight to fp16,
+    2^-11, and the logit's error d (tolerances), which is 2 d of a weight: independent of token to
+    token, they add as their roots do, and six times that is taken.  Of the sums of codes and of
+    minima, 2^-17: 4096 roundings of at most 2^-24 in each of four warps, of sums that grow, are 2^-20.6
+    of them in the spread, six times that 2^-18, and a product's own sum of 16 drops 2^-21."""
+    import torch
+    n, page, group, batch = 262144, 64, 32, 456
+    gen = torch.Generator("cuda").manual_seed(rows)
+    pages = n // page
+    c = fp.QCache.empty(pages, page, 1, group)
+    table = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32).view(1, -1)
+    slots = (table[0].long().repeat_interleave(page) * page + torch.arange(n, device="cuda") % page).to(torch.int32)
+    k, v = (torch.randn((n, 1, 128), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    c.write(k, v, slots)
+    q = (torch.randn((rows, h_q, 128), generator=gen, device="cuda") * 1.5).to(torch.bfloat16)
+    out, lse = c.attn(q.repeat(batch, 1, 1), table.repeat(batch, 1).contiguous(),
+                      torch.full((batch,), n, dtype=torch.int32, device="cuda"), max_q=rows)
+    data = c.data.cpu().numpy()
+    k, v = (torch.from_numpy(x[:, 0]).cuda() for x in oq.read(data, page, group, slots.cpu().numpy()))
+    got, got_lse = out.view(batch, rows, h_q, 128).double(), lse.view(h_q, batch, rows).double()
+    low = v.view(n, 128 // group, group).amin(-1, keepdim=True).expand(-1, -1, group).reshape(n, 128)
+    half = np.ascontiguousarray(data[..., 2048:]).view(np.float16).astype(np.float64)
+    ks, km = (np.abs(half[..., x * 64:(x + 1) * 64]).max() for x in (0, 1))
+    d = 2.0 ** -18 * 128 ** -0.5 * float(q.double().abs().sum(-1).max()) * (15 * ks + km) + 2.0 ** -20
+    for i in range(rows):
+        z = (q[i].double() @ k.t()) / 128 ** 0.5
+        z[:, n - rows + i + 1:] = -float("inf")
+        want_lse = torch.logsumexp(z, -1)
+        w = torch.exp(z - want_lse.unsqueeze(-1))
+        ref = w @ v
+        spread = 2.0 ** -11 * torch.sqrt((w * w) @ ((v - low) ** 2 + v ** 2)) + 2 * d * torch.sqrt((w * w) @ v ** 2)
+        tol = 2.0 ** -8 * ref.abs() + 6 * spread + 2.0 ** -17 * (w @ (v - low) + w @ low.abs())
+        for r in (0, 1, 200, batch - 1):
+            assert ((got[r, i] - ref).abs() <= tol).all(), float(((got[r, i] - ref).abs() / tol).max())
+            assert ((got_lse[:, r, i] - want_lse).abs() <= d + 2.0 ** -22 * want_lse.abs()).all()
+    assert c.device_status() == 0
