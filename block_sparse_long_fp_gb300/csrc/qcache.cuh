@@ -61,6 +61,33 @@ cudaError_t launch_chained(void (*kernel)(P...), unsigned grid, unsigned block, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Two fp32 in one register pair, each rounded by itself.
+using float_pair = unsigned long long;
+__device__ __forceinline__ float_pair pair(float lo, float hi) {
+    float_pair y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
+    return y;
+}
+__device__ __forceinline__ float2 unpair(float_pair x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ float_pair fma2(float_pair a, float_pair b, float_pair c) {
+    float_pair y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ float_pair add2(float_pair a, float_pair b) {
+    float_pair y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
+    float_pair y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
 struct QRows {
     const void *k, *v;
     long long stride_tok, stride_head;

@@ -124,33 +124,6 @@ __device__ __forceinline__ void mma8_zero(float d[4], uint32_t a0, uint32_t a1, 
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
-// Two fp32 in one register pair.
-using float_pair = unsigned long long;
-__device__ __forceinline__ float_pair pair(float lo, float hi) {
-    float_pair y;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
-    return y;
-}
-__device__ __forceinline__ float2 unpair(float_pair x) {
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
-    return y;
-}
-__device__ __forceinline__ float_pair fma2(float_pair a, float_pair b, float_pair c) {
-    float_pair y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
-    return y;
-}
-__device__ __forceinline__ float_pair add2(float_pair a, float_pair b) {
-    float_pair y;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
-__device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
-    float_pair y;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
 // Sums over the length are added in fp32, rounded to nearest: chained on the tensor cores,
 // which cut the bits below their largest term off, they lose some 2^-25 of themselves a
 // product, always towards zero.  Codes are positive and minima make up for it, so that the

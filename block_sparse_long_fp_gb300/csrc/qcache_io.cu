@@ -296,28 +296,6 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return y;
 }
 
-// Two fp32 at a time, each rounded by itself.
-__device__ __forceinline__ unsigned long long pair(float lo, float hi) {
-    unsigned long long y;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
-    return y;
-}
-__device__ __forceinline__ float2 unpair(unsigned long long x) {
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
-    return y;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long y;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
-    return y;
-}
-
 // d / 15 and 1 / s as correctly rounded quotients need them: a quotient by the rounded
 // reciprocal, corrected by its fused remainder (Markstein 1990), and a Newton step on the
 // approximate reciprocal.  Equal to the division: the first for all 2^24 d of two binades
@@ -340,13 +318,13 @@ __device__ __forceinline__ float reciprocal(float s) {
 // for all that both say .rn, and a fused product with a zero that it can see is a product
 // to it: `zeros`, a pair of -0, comes from where it cannot.  Without `clamp` the codes are
 // known to be in 0 .. 15.
-__device__ __forceinline__ uint32_t codes8(const unsigned long long x[4], float low, float inv, unsigned long long zeros,
+__device__ __forceinline__ uint32_t codes8(const float_pair x[4], float low, float inv, float_pair zeros,
                                            bool clamp) {
-    const unsigned long long minus = pair(-low, -low), by = pair(inv, inv), magic = pair(12582912.f, 12582912.f);
+    const float_pair minus = pair(-low, -low), by = pair(inv, inv), magic = pair(12582912.f, 12582912.f);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
-        unsigned long long y = fma2(add2(x[i], minus), by, zeros);
+        float_pair y = fma2(add2(x[i], minus), by, zeros);
         if (clamp) {
             const float2 v = unpair(y);
             y = pair(fminf(fmaxf(v.x, 0.f), 15.f), fminf(fmaxf(v.y, 0.f), 15.f));
@@ -360,7 +338,7 @@ __device__ __forceinline__ uint32_t codes8(const unsigned long long x[4], float 
 // Sixteen codes of a lane, their group's step and minimum.  The group's least and greatest
 // value say whether any of it needs the clamps, which are a path of their own.
 template <int GROUPS, bool FP8>
-__device__ __forceinline__ uint2 quantise16(const Raw<FP8> &raw, float scale, unsigned long long zeros, __half *step,
+__device__ __forceinline__ uint2 quantise16(const Raw<FP8> &raw, float scale, float_pair zeros, __half *step,
                                             __half *low) {
     float mn, mx;
     if (FP8) {
@@ -416,7 +394,7 @@ __device__ __forceinline__ uint2 quantise16(const Raw<FP8> &raw, float scale, un
         unpack16<FP8>(raw, scale, x);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            unsigned long long y[4];
+            float_pair y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 y[i] = pair(fminf(fmaxf(x[8 * h + 2 * i], -65504.f), 65504.f),
@@ -428,7 +406,7 @@ __device__ __forceinline__ uint2 quantise16(const Raw<FP8> &raw, float scale, un
         unpack16<FP8>(raw, scale, x);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            unsigned long long y[4];
+            float_pair y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = pair(x[8 * h + 2 * i], x[8 * h + 2 * i + 1]);
             code[h] = codes8(y, mf, inv, zeros, false);
@@ -459,7 +437,7 @@ __device__ __forceinline__ void write_half(const QCache &c, const QRows &r, int 
     const int lane = threadIdx.x & 31, sub = lane / 8, part = lane % 8;      // row of four, 16 dims of the row
     const void *src = V ? r.v : r.k;
     const float zero = r.rows > 0 ? -0.f : 1.f;
-    const unsigned long long zeros = pair(zero, zero);
+    const float_pair zeros = pair(zero, zero);
     const float scale = FP8 ? (V ? r.v_scale : r.k_scale)[head] : 1.f;
     for_owned(c, r, w, head, [&](int row0, int n, int mine, unsigned char *chunk) {
         const auto load = [&](int i) {
@@ -525,7 +503,7 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
     // a scale whose quotients and remainders could leave the normal numbers is divided by plainly
     const bool plain = !(fabsf(scale) >= 0x1p-60f && fabsf(scale) <= 0x1p60f);
     const float inverse = 1.f / scale, zero = r.rows > 0 ? -0.f : 1.f;
-    const unsigned long long by = pair(inverse, inverse), minus = pair(-scale, -scale), zeros = pair(zero, zero);
+    const float_pair by = pair(inverse, inverse), minus = pair(-scale, -scale), zeros = pair(zero, zero);
     for_owned(c, r, w, head, [&](int row0, int n, int mine, unsigned char *chunk) {
         // target of row row0 + (lane & 15), -1 where nothing is to be written
         int to = -1;
@@ -567,9 +545,9 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
             const float s = __half2float(q[0]), m = __half2float(q[16 * GROUPS]);
             // Two codes at a time: a code 4 k bits up in the mantissa of 2^23 stands for 16^k
             // times itself, which the step's 16^-k takes back without a rounding.
-            const unsigned long long steps[2] = {pair(s, s * 0x1p-4f), pair(s * 0x1p-8f, s * 0x1p-12f)};
-            const unsigned long long less = pair(-8388608.f, -8388608.f), low = pair(m, m);
-            unsigned long long x[8];
+            const float_pair steps[2] = {pair(s, s * 0x1p-4f), pair(s * 0x1p-8f, s * 0x1p-12f)};
+            const float_pair less = pair(-8388608.f, -8388608.f), low = pair(m, m);
+            float_pair x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t c4 = code[e / 4] >> (e & 2 ? 16 : 0), k = 8 * (e & 1);
@@ -588,7 +566,7 @@ __device__ __forceinline__ void read_half(const QCache &c, const QRows &r, int w
                 } else {                         // the same quotients by the rounded reciprocal (Markstein 1990)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const unsigned long long f = fma2(x[e], by, zeros);
+                        const float_pair f = fma2(x[e], by, zeros);
                         x[e] = fma2(fma2(f, minus, x[e]), by, f);
                     }
                 }
