@@ -36,13 +36,13 @@
 // end.  An item cut by a range's end leaves partial results, which a second kernel joins, in
 // a fixed order: the same call gives the same bits.
 //
-// Bounds.  One octet of columns: memory, with about 270 instructions a chunk (88 of them
+// Bounds.  One octet of columns: memory, with about 295 instructions a chunk (88 of them
 // take codes apart) that leave little slack: 64 requests of up to 16384 tokens (32/4 heads,
-// groups of 32) 62 us, one of 262144 (32/8) 61 us, 5.4 TB/s each, 0.8 of the measured copy
+// groups of 32) 63 us, one of 262144 (32/8) 62 us, 5.3 TB/s each, 0.78 of the measured copy
 // rate; 4 us of it pass before the first chunk and 4 in the join.  More octets: each adds
-// about 85 instructions a chunk, and a warp's instructions follow each other at 5 to 8 cycles
+// about 100 instructions a chunk, and a warp's instructions follow each other at 4 to 8 cycles
 // whatever the occupancy that the registers leave.  16 columns (4 tokens of 4 heads) over 32
-// requests of 4096 on average: 55 us, 32 columns: 93 us, where the products alone need 33.
+// requests of 4096 on average: 55 us, 32 columns: 94 us, where the products alone need 33.
 #include <limits.h>
 
 #include <type_traits>
@@ -65,14 +65,14 @@ template <int NT>
 __device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 2 + octets; }
 // Longest cache, by the width of its table, that is not cut (one launch instead of two).
 // Microseconds whole / cut, 32/8 heads, with 8, 16, 32 columns, tables filled:
-//   up to 1024, 1 request    10.8 /  8.4   15.5 / 10.3   22.6 / 15.7
-//               16           11.0 / 13.1   15.9 / 17.4   23.0 / 26.8
-//               64           22.5 / 24.1   34.2 / 36.2   54.4 / 60.5
-//   up to 2048, 1            16.8 /  8.6   24.4 / 11.2   35.3 / 15.3
-//               16           17.1 / 15.9   24.9 / 21.3   36.5 / 34.7
+//   up to 1024, 1 request    10.9 /  8.2   16.3 / 10.6   23.2 / 16.2
+//               16           11.0 / 13.2   16.7 / 17.7   23.0 / 26.9
+//               64           22.7 / 24.2   35.9 / 37.6   55.0 / 62.9
+//   up to 2048, 1            17.1 /  9.0   26.0 / 11.3   35.4 / 15.5
+//               16           17.2 / 16.1   26.3 / 21.9   36.2 / 35.2
 // and filled to 0.3:
-//   up to 1024, 1             6.8 /  8.2    9.4 /  9.9   13.5 / 14.9
-//   up to 2048, 1             8.7 /  7.9   12.2 / 10.1   17.4 / 14.2
+//   up to 1024, 1             6.9 /  8.0    9.8 /  9.9   13.4 / 15.6
+//   up to 2048, 1             8.8 /  8.3   12.8 / 10.4   17.2 / 14.5
 constexpr int kWholeChunks = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 10.f, kSlack = 4.f;   // log2 of the largest weight, where its maximum is set and where it follows
@@ -94,9 +94,9 @@ struct Scratch {
 };
 
 // Blocks per SM, by their registers (168 a thread for 3, 255 for 2), and copies ahead.  8
-// columns, 64 requests up to 16384 tokens / one of 262144 / 256 up to 2048: 62 / 61 / 75 us;
-// with 4 blocks 66 / 66 / 73, with 2 66 / 61 / 103, with 3 and 6 copies 65 / 65 / 78.  16
-// columns, 32 requests up to 8192: 53 us; with 4 blocks, which spill, 59, with 2 55.
+// columns, 64 requests up to 16384 tokens / one of 262144 / 256 up to 2048: 62 / 61 / 77 us;
+// with 4 blocks 66 / 66 / 77, with 2 68 / 63 / 107, with 3 and 6 copies 65 / 64 / 79.  16
+// columns, 32 requests up to 8192: 55 us; with 4 blocks, which spill, 61, with 2 58.
 template <int NT>
 constexpr int blocks_per_sm() { return NT == 1 ? 3 : NT == 2 ? 3 : 2; }
 template <int NT>
@@ -959,14 +959,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(QAttn a, Scratch 
     }
 }
 
-// The narrowest tile that holds a kv head's (query, head) pairs, or the widest.
 // Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32.
 // Where the rows differ, what most of them fill, by the mean that the host knows: 32
 // requests up to 8192 of 4 heads a kv head, with 1 to n tokens each, take with tiles of 8, 16
-// and 32 columns 37, 41, 49 us (n = 2), 44, 46, 53 (3), 51, 48, 57 (4), 76, 65, 71 (8),
-// 123, 98, 100 (16); all with 6 tokens 83 with 16 and 73 with 32, with 8 92 and 92.  64 up to
-// 4096, most of which have one token: 63 and one of 128 90, 84, 96 us, 60 and four of 64
-// 115, 102, 112, 56 and eight of 16 73, 70, 82, one token each 42, 45, 54.
+// and 32 columns 38, 42, 50 us (n = 2), 45, 47, 54 (3), 52, 50, 59 (4), 78, 67, 76 (8),
+// 125, 103, 107 (16); all with 6 tokens 86 with 16 and 73 with 32, with 8 97 and 94.  64 up to
+// 4096, most of which have one token: 63 and one of 128 92, 87, 98 us, 60 and four of 64
+// 118, 107, 115, 56 and eight of 16 75, 73, 84, one token each 42, 46, 55.
 int tile_columns(const QAttn &a) {
     const long long cols = (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
     const bool ragged = a.cu && a.total_q != (long long)a.batch * a.max_q;

@@ -3,11 +3,12 @@
 //
 // Both are bound by memory where there are many rows: per (token, head) 512 bytes of bf16
 // on one side and 128 + 1024 / G bytes of cache on the other.  65536 tokens of 8 heads
-// (groups of 32) are written in 64 us, 5.5 TB/s, 0.81 of the measured copy rate (three
-// quarters of the issue slots go to the quantisation), and 131072 of 4 heads read in 63 us,
-// 5.6 TB/s, 0.83.  Few rows are bound by the latency of one dependent chain (slot, row, extremes,
-// store), 2 us, and take a warp per (row, kv head): four dims per lane, so that a group of G
-// dims is G / 4 neighbouring lanes and its extremes take log2(G / 4) shuffles.
+// (groups of 32) are written in 66 us, 5.3 TB/s, 0.78 of the measured copy rate (three
+// quarters of the issue slots go to the quantisation; from e4m3 in 71), and 131072 of 4 heads
+// read in 62 us, 5.7 TB/s, 0.84 (65536 of 8 heads to e4m3 in 62, which is arithmetic).  Few
+// rows are bound by the latency of one dependent chain (slot, row, extremes, store), 2 us, and
+// take a warp per (row, kv head): four dims per lane, so that a group of G dims is G / 4
+// neighbouring lanes and its extremes take log2(G / 4) shuffles.
 #include <type_traits>
 
 #include "qcache.cuh"

@@ -1197,7 +1197,8 @@ def test_sums_of_a_long_request_in_one_block(fp, rows, h_q):
     2^-11, and the logit's error d (tolerances), which is 2 d of a weight: independent of token to
     token, they add as their roots do, and six times that is taken.  Of the sums of codes and of
     minima, 2^-17: 4096 roundings of at most 2^-24 in each of four warps, of sums that grow, are 2^-20.6
-    of them in the spread, six times that 2^-18, and a product's own sum of 16 drops 2^-21."""
+    of them in the spread, six times that 2^-18, and a product's own sum of 16, which is cut towards
+    zero below the last bit of its largest term and whose codes are subnormal, as much again."""
     import torch
     n, page, group, batch = 262144, 64, 32, 456
     gen = torch.Generator("cuda").manual_seed(rows)
