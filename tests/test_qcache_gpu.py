@@ -1230,3 +1230,40 @@ def test_sums_of_a_long_request_in_one_block(fp, rows, h_q):
             assert ((got[r, i] - ref).abs() <= tol).all(), float(((got[r, i] - ref).abs() / tol).max())
             assert ((got_lse[:, r, i] - want_lse).abs() <= d + 2.0 ** -22 * want_lse.abs()).all()
     assert c.device_status() == 0
+
+
+def test_tensors_handed_over_between_streams(fp):
+    """Rows made on one stream, behind a wait, and written, attended and read on another that an
+    event holds back: the launches' early start is for the kernel before them in their own stream."""
+    import torch
+    lens, h, page, group = [500, 70], 2, 64, 32
+    data, table, q, q32, _ = attn_case(41, lens, [1, 1], 8, h, page, group)
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    bt, ln = i32(np.concatenate([table, np.full((2, 20), 10 ** 6)], 1)), i32(lens)
+    slot = i32([table[0, 499 // page] * page + 499 % page, table[1, 1] * page + 5])
+    rows = [source(50 + i, 2, h, "bf16")[0] for i in range(6)]
+    kept = c.data.clone()
+    want = []
+    for r in rows:
+        c.write(r, r, slot)
+        want.append((c.attn(q, bt, ln)[0].clone(), c.read(slot)[0].clone()))
+    assert not torch.equal(want[0][0], want[1][0])
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    k = torch.zeros_like(rows[0])
+    for _ in range(5):
+        c.data.copy_(kept)
+        torch.cuda.synchronize()
+        got = []
+        for r in rows:
+            with torch.cuda.stream(one):
+                one.wait_stream(two)
+                torch.cuda._sleep(200000)
+                k.copy_(r)
+            with torch.cuda.stream(two):
+                c.attn(q, bt, ln)                        # something of its own before
+                two.wait_stream(one)
+                c.write(k, k, slot)
+                got.append((c.attn(q, bt, ln)[0], c.read(slot)[0]))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert c.device_status() == 0
