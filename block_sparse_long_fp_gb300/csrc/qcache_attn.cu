@@ -23,7 +23,8 @@
 // it by 4 (a warp vote), so that the largest weight so far is between 2^10 and 2^14.  V
 // steps meet them times a power of two of their group, which sums take back at the item's
 // end and which only falls: where a step times it would reach 2, it is set anew, to bring
-// the group's largest of that chunk to 2^-2 .. 2^-1, and the group's sums with it.  Weight
+// the group's largest of that chunk to 2^-2 .. 2^-1 (steps of 2 and more to 1 .. 2, as they
+// are few and the others' lose bits below 2^-14), and the group's sums with it.  Weight
 // times step stays below 2^15, and fp16 flushes weights below 2^-35 of the largest, and
 // products below 2^-33 of the largest weight times its group's largest step, whatever the
 // steps of the other groups are.
@@ -699,8 +700,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                         const int e = (int)(__reduce_max_sync(~0u, most) >> 10) - 15;    // of the largest
                         const int old = exponent_of(up[g]);
                         if (e + old >= 1) {
-                            const float less = pow2f(-2 - e - old);
-                            up[g] = power_pair(-2 - e);
+                            const int now = e >= 1 ? -e : -2 - e;
+                            const float less = pow2f(now - old);
+                            up[g] = power_pair(now);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) vs[g][h] = mul_half2(raw[h], up[g]);
 #pragma unroll

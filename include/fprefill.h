@@ -484,7 +484,8 @@ fp_status fp_qcache_read(const fp_qcache *c, const fp_qcache_rows *r, void *ws, 
  *   Logits, weights' sums and outputs are summed in fp32.  Weights enter the sum of
  *   values in fp16 (2^-11 of each; nothing below 2^-35 of the row's largest), and so do
  *   their products with a value's step (nothing below 2^-33 of the largest weight times
- *   the largest step of that group of dims).
+ *   the largest step of that group of dims, and a step to 2^-23 of that largest, among
+ *   the tokens of the request up to its last row's).
  *   scratch: fp_qcache_attn_scratch_bytes() bytes (partial results of requests
  *   that several thread blocks share); it holds nothing between calls.  A call
  *   enqueues two kernels that hand these over: calls that may run at once, or

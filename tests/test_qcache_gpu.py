@@ -1267,3 +1267,37 @@ def test_tensors_handed_over_between_streams(fp):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("rows,h_q", [(2, 2), (4, 6), (8, 6)])
+@pytest.mark.parametrize("length", [12, 300])
+def test_an_infinite_value_of_a_later_row(fp, length, rows, h_q):
+    """An infinity (65504 in the cache, in steps of up to 8734) in the last token's values, which only
+    the last row attends.  The rows before it lose what fp16 loses of their own steps beside that one:
+    2^-25 of it a step, 15 steps a code, 0.004 of an output's unit at most, and their other roundings."""
+    import torch
+    lens, lq, h, page, group = [length], [rows], 2, 16, 32
+    data, table, q, q32, _ = attn_case(61 + rows, lens, lq, h_q, h, page, group)
+    clean = data.copy()
+    c = fp.QCache(torch.from_numpy(data).cuda(), page, group)
+    slot = i32([table[0, (length - 1) // page] * page + (length - 1) % page])
+    k, v = (t.clone() for t in c.read(slot))
+    v[0, :, 40], v[0, :, 41], v[0, 1, 100] = float("inf"), -float("inf"), float("inf")
+    c.write(k, v, slot)
+    data = c.data.cpu().numpy()
+    ref_o, ref_lse = oq.attention(q32, data, page, group, table, lens, lq)
+    ref_clean, _ = oq.attention(q32, clean, page, group, table, lens, lq)
+    assert np.allclose(ref_o[:-1], ref_clean[:-1]) and np.abs(ref_o[-1]).max() > 2
+    half = np.ascontiguousarray(clean[..., 2048:]).view(np.float16).astype(np.float64)
+    bounds = [np.nan_to_num(np.abs(half[..., i * 64:(i + 1) * 64])).max() for i in range(4)]
+    wide = np.full((1, table.shape[1] + 100), 10 ** 6)
+    wide[:, :table.shape[1]] = table
+    for bt in (table, wide):
+        out, lse = c.attn(q, i32(bt), i32(lens), max_q=rows)
+        got = out.float().cpu().numpy()
+        tol, tol_lse = tolerances(q32, clean, group, ref_o, ref_lse, 128 ** -0.5, bounds)
+        assert np.all(np.abs(got - ref_o)[:-1] <= tol[:-1] + 15 * 2.0 ** -25 * 8736)
+        tol = tolerances(q32, data, group, ref_o, ref_lse, 128 ** -0.5)[0]
+        assert np.all(np.abs(got - ref_o)[-1] <= tol[-1])
+        assert np.all(np.abs(lse.cpu().numpy() - ref_lse) <= tol_lse)
+    assert c.device_status() == 0
