@@ -24,6 +24,7 @@ FP_MAX_BATCH = 128
 FP_SELECT_THRESHOLD, FP_SELECT_TOPK, FP_SELECT_TOPP = 0, 1, 2
 FP_SCORE_PACKED, FP_SCORE_HEAD_UNION = 0, 1
 FP_V_TOKEN_MAJOR, FP_V_DIM_MAJOR = 0, 1
+FP_ROPE_HALF, FP_ROPE_INTERLEAVED = 0, 1
 FP_WS_HEADER_BYTES = 256
 FP_TABLES_MAX_BATCH = 4096
 
@@ -70,13 +71,39 @@ class FpQCacheQuery(Structure):
                 ("max_pages_per_seq", c_int), ("softmax_scale", c_float)]
 
 
+class FpRopeTable(Structure):
+    _fields_ = [("rot", c_int), ("layout", c_int), ("scale", c_float), ("turns", c_void_p)]
+
+
+class FpRopeRows(Structure):
+    _fields_ = [("rows", c_int), ("heads", c_int), ("x", c_void_p), ("x_stride_tok", c_longlong),
+                ("x_stride_head", c_longlong), ("out", c_void_p), ("out_stride_tok", c_longlong),
+                ("out_stride_head", c_longlong), ("out_dtype", c_int), ("out_scale", c_void_p), ("positions", c_void_p),
+                ("inverse", c_int)]
+
+
+class FpCache(Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("num_pages", c_int), ("page_size", c_int), ("h_kv", c_int),
+                ("d", c_int), ("dtype", c_int), ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class FpCacheRows(Structure):
+    _fields_ = [("rows", c_int), ("h_q", c_int), ("k", c_void_p), ("v", c_void_p), ("q", c_void_p),
+                ("k_stride_tok", c_longlong), ("k_stride_head", c_longlong), ("v_stride_tok", c_longlong),
+                ("v_stride_head", c_longlong), ("q_stride_tok", c_longlong), ("q_stride_head", c_longlong),
+                ("q_out", c_void_p), ("q_out_stride_tok", c_longlong), ("q_out_stride_head", c_longlong),
+                ("q_dtype", c_int), ("q_scale", c_void_p), ("slots", c_void_p), ("positions", c_void_p)]
+
+
 # The same structures as bytes: packing them takes a fifth of the time of filling
 # a ctypes one, which counts in calls of a few microseconds.
 _PACK_TABLES = struct.Struct("@6i10P")
 _PACK_ROWS = struct.Struct("@2i2P2q2Pi2P0P")
 _PACK_QUERY = struct.Struct("@5iP2q4Pif0P")
-assert (_PACK_TABLES.size, _PACK_ROWS.size, _PACK_QUERY.size) == tuple(
-    ctypes.sizeof(t) for t in (FpTables, FpQCacheRows, FpQCacheQuery))
+_PACK_ROPE = struct.Struct("@2iP2qP2qi2Pi0P")
+_PACK_APPEND = struct.Struct("@2i3P6qP2qi3P")
+assert (_PACK_TABLES.size, _PACK_ROWS.size, _PACK_QUERY.size, _PACK_ROPE.size, _PACK_APPEND.size) == tuple(
+    ctypes.sizeof(t) for t in (FpTables, FpQCacheRows, FpQCacheQuery, FpRopeRows, FpCacheRows))
 
 
 class FprefillError(RuntimeError):
@@ -127,6 +154,10 @@ def lib():
             "fp_qcache_read": ([PC, PR, c_void_p, c_size_t, c_void_p], c_int),
             "fp_qcache_attn_scratch_bytes": ([PC, PQ], c_size_t),
             "fp_qcache_attn": ([PC, PQ, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_size_t, c_void_p], c_int),
+            "fp_rope_turns": ([c_void_p, c_int, c_void_p], c_int),
+            "fp_rope": ([POINTER(FpRopeTable), POINTER(FpRopeRows), c_void_p], c_int),
+            "fp_cache_append": ([POINTER(FpCache), POINTER(FpRopeTable), POINTER(FpCacheRows), c_void_p, c_size_t,
+                                 c_void_p], c_int),
             "fp_reset_status": ([c_void_p, c_void_p], c_int),
             "fp_device_status": ([c_void_p, c_void_p, POINTER(c_int)], c_int),
             "fp_status_string": ([c_int], ctypes.c_char_p),
@@ -355,7 +386,7 @@ def _need(t, name: str, dtypes, device: int, ndim: int, contiguous: bool = True)
 
 
 class _OnDevice:
-    """What PageTables and QCache share: the status header, and calls on their
+    """What PageTables, QCache, Rope and KVCache share: the status header, and calls on their
     device's current stream whatever device is current."""
 
     def __init__(self, device):
@@ -406,6 +437,18 @@ class _OnDevice:
             return t.data_ptr()
         _need(t, name, (self._fp32,), self._index, 1)
         raise FprefillError(FP_ERR_INVALID, f"{name}: {n} entries wanted, got {t.shape[0]}")
+
+    def _heads(self, t, name: str, heads, fp8: bool = False):
+        """Address and strides of rows [rows, heads, 128] with contiguous dims (any number of heads when None)."""
+        shape, strides = t.shape, t.stride()
+        if not (len(shape) == 3 and t.dtype in (self._fp8 if fp8 else self._bf16) and t.get_device() == self._index and
+                strides[2] == 1 and shape[2] == 128 and shape[1] and (heads is None or shape[1] == heads)):
+            _need(t, name, self._fp8 if fp8 else self._bf16, self._index, 3, False)
+            raise FprefillError(FP_ERR_INVALID, f"{name}: [rows, {'heads' if heads is None else heads}, 128] with contiguous "
+                                f"dims wanted, got {tuple(shape)} {strides}")
+        # a single row (or head) may carry any stride: the packed one stands for it
+        stride_head = strides[1] if shape[1] > 1 else 128
+        return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1] * stride_head, stride_head
 
     def device_status(self) -> int:
         """Waits for the current stream; what its kernels found wrong in device data (FP_OK: nothing)."""
@@ -630,6 +673,153 @@ class QCache(_OnDevice):
             s = self._f[2](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
         if s != FP_OK:
             raise FprefillError(s, "fp_qcache_attn")
+
+
+def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 4096, low: float = 1.0, high: float = 4.0) -> np.ndarray:
+    """Radians a position for the rot / 2 pairs of a rotary embedding, float64:
+    base^(-2 i / rot), scaled for contexts `factor` times the trained ones by
+
+    None       nothing;
+    "linear"   1 / factor for every pair (positions squeezed);
+    "base"     the base raised to base * factor^(rot / (rot - 2)), so that the
+               longest wave is `factor` times as long and the shortest stays;
+    "smooth"   by the waves that a pair makes in `original` positions: 1 / factor
+               up to `low` waves, 1 from `high` on, and linear in them between;
+    "ramp"     the same, but linear in the pair's index between those indices
+               (rounded outwards) where a pair makes `high` and `low` waves."""
+    if rot < 2 or rot > 128 or rot % 2 or not base > 1 or not factor > 0:
+        raise FprefillError(FP_ERR_INVALID, f"rope_frequencies: rot {rot}, base {base}, factor {factor}")
+    i = np.arange(rot // 2, dtype=np.float64)
+    if scaling == "base":
+        if rot == 2:
+            raise FprefillError(FP_ERR_INVALID, "rope_frequencies: one pair has no base to raise")
+        return (base * factor ** (rot / (rot - 2))) ** (-2 * i / rot)
+    f = base ** (-2 * i / rot)
+    if scaling is None:
+        return f
+    if scaling == "linear":
+        return f / factor
+    if scaling not in ("smooth", "ramp") or not original > 0 or not high > low > 0:
+        raise FprefillError(FP_ERR_INVALID, f"rope_frequencies: scaling {scaling!r}, original {original}, low {low}, high {high}")
+    if scaling == "smooth":
+        keep = np.clip((original * f / (2 * np.pi) - low) / (high - low), 0, 1)
+    else:
+        first, last = (rot * np.log(original / (w * 2 * np.pi)) / (2 * np.log(base)) for w in (high, low))
+        first, last = max(0, np.floor(first)), min(rot - 1, np.ceil(last))
+        keep = 1 - np.clip((i - first) / max(last - first, 0.001), 0, 1)
+    return f * keep + f / factor * (1 - keep)
+
+
+class Rope(_OnDevice):
+    """Rotary positions: fp_rope, and the rotation that KVCache.append applies.
+
+    inv_freq: rot / 2 frequencies in radians a position (rope_frequencies, or a
+    model's own), for the first rot dims of a head; layout: "half" (pairs i, i +
+    rot / 2) or "interleaved" (2 i, 2 i + 1); scale multiplies cos and sin.
+    """
+
+    def __init__(self, inv_freq, layout: str = "half", scale: float = 1.0, device="cuda"):
+        import torch
+        freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if freq.ndim != 1 or not 1 <= freq.size <= 64 or layout not in ("half", "interleaved") or not np.isfinite(scale):
+            raise FprefillError(FP_ERR_INVALID, f"Rope: 1 to 64 frequencies, layout half or interleaved, a finite scale "
+                                f"wanted, got {freq.shape}, {layout!r}, {scale}")
+        turns = np.zeros(freq.size, dtype=np.uint64)
+        _check(lib().fp_rope_turns(freq.ctypes.data, freq.size, turns.ctypes.data), "fp_rope_turns")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        super().__init__(self.turns.device)
+        self.rot, self.layout, self.scale = 2 * freq.size, layout, float(scale)
+        self._t = FpRopeTable(self.rot, FP_ROPE_INTERLEAVED if layout == "interleaved" else FP_ROPE_HALF, self.scale,
+                              _ptr(self.turns))
+        self._bytes = bytes(self._t)
+        self._f = self._entry("fp_rope", 3)
+
+    def apply(self, x, positions, out=None, out_scale=None, inverse: bool = False):
+        """x (bf16 [rows, heads, 128]) rotated by positions (int32 [rows]); with
+        inverse, back (the gradient's rotation too).  Into out -- bf16, x itself
+        if wanted, or with out_scale [heads] e4m3 -- or into new rows."""
+        x_at = self._heads(x, "x", None)
+        rows, heads = x.shape[0], x.shape[1]
+        fp8 = out_scale is not None
+        if out is None:
+            out = self._torch.empty((rows, heads, 128), dtype=self._torch.uint8 if fp8 else self._torch.bfloat16,
+                                    device=self.device)
+        out_at = self._heads(out, "out", heads, fp8)
+        if out.shape[0] != rows:
+            raise FprefillError(FP_ERR_INVALID, f"out: {rows} rows wanted, got {out.shape[0]}")
+        R = _PACK_ROPE.pack(rows, heads, *x_at, *out_at, FP_E4M3 if fp8 else FP_BF16,
+                            self._scales(out_scale, "out_scale", heads) if fp8 else 0,
+                            self._vector(positions, "positions", rows), 1 if inverse else 0)
+        self._call(self._f, "fp_rope", self._bytes, R)
+        return out
+
+
+class KVCache(_OnDevice):
+    """The bf16 or e4m3 paged K/V cache that Layer reads, at any position:
+    fp_cache_append on it.
+
+    k_cache, v_cache: [num_pages, page_size, h_kv, 128], bf16, or e4m3 (uint8
+    codes or torch.float8_e4m3fn) with k_scale and v_scale (fp32 [h_kv]).
+    """
+
+    def __init__(self, k_cache, v_cache, k_scale=None, v_scale=None):
+        super().__init__(k_cache.device)
+        fp8 = k_scale is not None or v_scale is not None
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, name, self._fp8 if fp8 else self._bf16, self._index, 4)
+        if v_cache.shape != k_cache.shape or k_cache.shape[3] != 128:
+            raise FprefillError(FP_ERR_INVALID, f"k_cache, v_cache: [num_pages, page_size, h_kv, 128] wanted, got "
+                                f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+        c = self._c = FpCache()
+        c.k, c.v, c.d, c.dtype = _ptr(k_cache), _ptr(v_cache), 128, FP_E4M3 if fp8 else FP_BF16
+        c.num_pages, c.page_size, c.h_kv = (int(n) for n in k_cache.shape[:3])
+        if c.page_size < 16 or (128 % c.page_size and c.page_size % 128):
+            raise FprefillError(FP_ERR_UNSUPPORTED, f"pages of {c.page_size} tokens")
+        if fp8:
+            c.k_scale, c.v_scale = (self._scales(t, n, c.h_kv) for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+        self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
+        self.h_kv, self.page_size = c.h_kv, c.page_size
+        self._bytes = bytes(c)
+        self._f = self._entry("fp_cache_append", 6)
+
+    def append(self, k, v, slots, rope: Rope | None = None, positions=None, q=None, q_out=None, q_scale=None):
+        """Rows of k and v (bf16 [rows, h_kv, 128]) into `slots` (int32 [rows]; -1:
+        none; none twice).  With a Rope, k and q rotated by positions (int32
+        [rows]).  Returns q (bf16 [rows, h_q, 128]) so rotated, in q_out -- bf16,
+        q itself if wanted, or with q_scale [h_q] e4m3 -- or in new rows; None
+        without q."""
+        k_at, v_at = self._heads(k, "k", self.h_kv), self._heads(v, "v", self.h_kv)
+        rows = k.shape[0]
+        if v.shape[0] != rows:
+            raise FprefillError(FP_ERR_INVALID, f"v: {rows} rows wanted, got {v.shape[0]}")
+        slots_at = self._vector(slots, "slots", rows)
+        if (rope is None) != (positions is None):
+            raise FprefillError(FP_ERR_INVALID, "rope and positions come together")
+        if rope is not None and rope._index != self._index:
+            raise FprefillError(FP_ERR_INVALID, f"rope: on cuda:{self._index} wanted, got {rope.device}")
+        q_at, out_at, h_q, scale_at = (0, 0, 0), (0, 0, 0), 0, 0
+        if q is not None:
+            q_at = self._heads(q, "q", None)
+            h_q = q.shape[1]
+            fp8 = q_scale is not None
+            if q_out is None:
+                q_out = self._torch.empty((rows, h_q, 128), dtype=self._torch.uint8 if fp8 else self._torch.bfloat16,
+                                          device=self.device)
+            out_at = self._heads(q_out, "q_out", h_q, fp8)
+            if q.shape[0] != rows or q_out.shape[0] != rows:
+                raise FprefillError(FP_ERR_INVALID, f"q, q_out: {rows} rows wanted, got {q.shape[0]}, {q_out.shape[0]}")
+            if fp8:
+                scale_at = self._scales(q_scale, "q_scale", h_q)
+        elif q_out is not None or q_scale is not None:
+            raise FprefillError(FP_ERR_INVALID, "q_out and q_scale want q")
+        # an empty batch may have no memory: a q of no rows is no q
+        R = _PACK_APPEND.pack(rows, h_q if q_at[0] else 0, k_at[0], v_at[0], q_at[0], *k_at[1:], *v_at[1:], *q_at[1:],
+                              *out_at, FP_E4M3 if scale_at else FP_BF16, scale_at, slots_at,
+                              0 if rope is None else self._vector(positions, "positions", rows))
+        self._call(self._f, "fp_cache_append", self._bytes, 0 if rope is None else rope._bytes, R, self._ws_ptr,
+                   FP_WS_HEADER_BYTES)
+        return q_out
 
 
 def layer_from_case(case, device="cuda", params: FpParams | None = None, v_layout: int = 0):

@@ -514,6 +514,89 @@ size_t fp_qcache_attn_scratch_bytes(const fp_qcache *c, const fp_qcache_query *q
 fp_status fp_qcache_attn(const fp_qcache *c, const fp_qcache_query *q, void *out, float *lse_opt, void *scratch,
                          size_t scratch_bytes, void *ws, size_t ws_bytes, void *stream);
 
+/* ===========================================================================
+ * The bf16 / e4m3 paged cache at any position: rotary positions, and keys and values
+ * appended to the pages that the prefill entry points read.  Lengths, positions, slots and
+ * tables are DEVICE arrays, as for the 4-bit cache above.
+ * ========================================================================= */
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions
+ *
+ * The first `rot` dims of a head form pairs (a, b) of dims: (i, i + rot / 2) in the half
+ * layout, (2 i, 2 i + 1) in the interleaved one, i < rot / 2.  With the angle
+ * t = position * inv_freq[i],
+ *   a' = scale * (a cos t - b sin t),   b' = scale * (b cos t + a sin t),
+ * t negated for the inverse: with scale 1 the inverse undoes the rotation, and with any
+ * scale it is the gradient.  Dims from `rot` on stay as they are (and are not scaled).
+ * Angles are exact to 2^-32 of a turn at any int32 position (negative ones too); products
+ * and sums are fp32, rounded once to the output's type.
+ * ------------------------------------------------------------------------- */
+typedef enum { FP_ROPE_HALF = 0, FP_ROPE_INTERLEAVED = 1 } fp_rope_layout;
+typedef struct {
+    int rot;                          /* even, 2 .. 128 */
+    fp_rope_layout layout;
+    float scale;                      /* multiplies cos and sin (1, or a long context's factor) */
+    const unsigned long long *turns;  /* DEVICE [rot / 2], of fp_rope_turns */
+} fp_rope_table;
+/* turns[i] = the fraction of a turn that one position makes, inv_freq[i] / 2 pi modulo 1, in
+ * units of 2^-64, for n frequencies in radians a position.  Host-only, host arrays.
+ * FP_ERR_INVALID: a frequency that is not finite, or above 2^20 in magnitude. */
+fp_status fp_rope_turns(const double *inv_freq, int n, unsigned long long *turns);
+
+/* fp_rope -- rotate rows
+ *
+ *   x (device bf16): row i, head h at  i * stride_tok + h * stride_head  elements (pointer
+ *     and strides multiples of 16 bytes, stride_head >= 128, stride_tok >= stride_head *
+ *     (heads - 1) + 128); out the same with its own strides, bf16, or e4m3 codes of
+ *     value / out_scale[head] (times the scale's rounded reciprocal; saturated at 448).
+ *   out may be x itself, with like strides and type; otherwise they do not overlap. */
+typedef struct {
+    int rows;                         /* >= 0 */
+    int heads;                        /* >= 1 */
+    const void *x;                    /* DEVICE */
+    long long x_stride_tok, x_stride_head;
+    void *out;                        /* DEVICE */
+    long long out_stride_tok, out_stride_head;
+    fp_dtype out_dtype;
+    const float *out_scale;           /* DEVICE [heads], FP_E4M3 only */
+    const int *positions;             /* DEVICE [rows] */
+    int inverse;                      /* 0 or 1 */
+} fp_rope_rows;
+fp_status fp_rope(const fp_rope_table *t, const fp_rope_rows *r, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * fp_cache_append -- new tokens into the paged cache, rotated on the way
+ *
+ *   k and v rows i go to slot slots[i] of their caches; -1 skips the row, another value
+ *   outside the cache skips it and sets the status.  No slot may appear twice in one call.
+ *   Slots that no row names stay as they are.  With `rope`, k (and q) are rotated by
+ *   positions[i].  q (may be NULL): every row i, whatever its slot, to row i of q_out, which
+ *   may be q itself when both are bf16 with like strides.  bf16 in; out in the cache's type
+ *   (q: q_dtype), rounded and scaled as fp_rope's. */
+typedef struct {
+    void *k, *v;                      /* DEVICE [num_pages, page_size, h_kv, d], 16-byte aligned */
+    int num_pages, page_size;         /* page_size as above; num_pages * page_size <= 2^31 - 1 */
+    int h_kv;
+    int d;                            /* must be 128 */
+    fp_dtype dtype;
+    const float *k_scale, *v_scale;   /* DEVICE [h_kv], FP_E4M3 only */
+} fp_cache;
+typedef struct {
+    int rows;                         /* >= 0 */
+    int h_q;                          /* heads of q (any number; 0 with q NULL) */
+    const void *k, *v, *q;            /* DEVICE bf16, strides as fp_rope's */
+    long long k_stride_tok, k_stride_head, v_stride_tok, v_stride_head, q_stride_tok, q_stride_head;
+    void *q_out;                      /* DEVICE */
+    long long q_out_stride_tok, q_out_stride_head;
+    fp_dtype q_dtype;                 /* of q_out */
+    const float *q_scale;             /* DEVICE [h_q], q_dtype FP_E4M3 only */
+    const int *slots;                 /* DEVICE [rows] */
+    const int *positions;             /* DEVICE [rows], with rope only */
+} fp_cache_rows;
+fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, const fp_cache_rows *r, void *ws,
+                          size_t ws_bytes, void *stream);
+
 /* Zero the status header of a workspace (enqueued on stream). */
 fp_status fp_reset_status(void *ws, void *stream);
 
