@@ -33,4 +33,29 @@ struct RotateRows {
 };
 cudaError_t launch_rotate_rows(const RotateRows &r, cudaStream_t st);
 
+struct Pages {
+    const unsigned char *k, *v;                // [num_pages, page_size, h_kv, kHeadDim]
+    int num_pages, page_size, h_kv;
+};
+
+struct PAttn {
+    Pages c;
+    const float *k_scale, *v_scale;            // null for bf16
+    int batch, h_q, g, total_q, max_q;
+    const void *q;
+    long long q_stride_tok, q_stride_head;
+    const float *q_scale;                      // null for bf16
+    const int *cu;                             // null: max_q rows each
+    const int *seqlens_k, *block_table;
+    int max_pages;
+    int max_len;                               // what the table holds, short of what an int's arithmetic can
+    float scale;                               // logit scale
+    __nv_bfloat16 *out;
+    float *lse;
+    int *status;
+    bool whole;                                // no item is cut (set by the launch)
+};
+size_t cache_attn_scratch_bytes(const PAttn &a);
+cudaError_t launch_cache_attn(const PAttn &a, void *scratch, cudaStream_t st);
+
 }  // namespace fp

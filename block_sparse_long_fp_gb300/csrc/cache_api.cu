@@ -36,11 +36,17 @@ fp_status check_rope(const fp_rope_table *t, bool inverse, Rotation *rot) {
     return FP_OK;
 }
 
-fp_status check_cache(const fp_cache *c) {
-    if (!c || c->h_kv < 1 || c->num_pages < 1 || !dtype_ok(c->dtype)) return FP_ERR_INVALID;
+// What this build supports of a cache's shape.
+fp_status check_shape(const fp_cache *c) {
     if (c->d != kHeadDim) return FP_ERR_UNSUPPORTED;
     if (c->page_size < 16 || !(kBlock % c->page_size == 0 || c->page_size % kBlock == 0)) return FP_ERR_UNSUPPORTED;
-    if ((long long)c->num_pages * c->page_size > (1ll << 31) - 1) return FP_ERR_UNSUPPORTED;
+    return (long long)c->num_pages * c->page_size > (1ll << 31) - 1 ? FP_ERR_UNSUPPORTED : FP_OK;
+}
+
+fp_status check_cache(const fp_cache *c) {
+    if (!c || c->h_kv < 1 || c->num_pages < 1 || !dtype_ok(c->dtype)) return FP_ERR_INVALID;
+    const fp_status s = check_shape(c);
+    if (s != FP_OK) return s;
     const long long tok = (long long)c->h_kv * kHeadDim;
     if (!rows_ok(c->k, tok, kHeadDim, c->h_kv, c->dtype, c->k_scale) ||
         !rows_ok(c->v, tok, kHeadDim, c->h_kv, c->dtype, c->v_scale))
@@ -55,6 +61,40 @@ RowsPart part(const void *in, long long in_tok, long long in_head, void *out, lo
               int heads, fp_dtype t, const float *scale) {
     return RowsPart{static_cast<const __nv_bfloat16 *>(in), out, in_tok, in_head, out_tok, out_head,
                     t == FP_E4M3 ? scale : nullptr, heads};
+}
+
+// Everything of an attention call but its buffers.
+fp_status check_query(const fp_cache *c, const fp_qcache_query *q, PAttn *a) {
+    if (!c || c->h_kv < 1 || c->num_pages < 1 || !dtype_ok(c->dtype)) return FP_ERR_INVALID;
+    const fp_status s = check_shape(c);
+    if (s != FP_OK) return s;
+    if (!q || q->batch < 1 || q->total_q < 0 || q->max_q < 1 || q->max_pages_per_seq < 1) return FP_ERR_INVALID;
+    if (q->batch > FP_TABLES_MAX_BATCH) return FP_ERR_UNSUPPORTED;
+    if (q->h_q < 1 || q->h_q % c->h_kv || !dtype_ok(q->dtype)) return FP_ERR_INVALID;
+    if ((long long)q->total_q * q->h_q > (1ll << 30)) return FP_ERR_UNSUPPORTED;
+    if (!q->cu_seqlens_q && (long long)q->batch * q->max_q > q->total_q) return FP_ERR_INVALID;
+    memset(a, 0, sizeof(*a));
+    a->c = Pages{static_cast<const unsigned char *>(c->k), static_cast<const unsigned char *>(c->v), c->num_pages,
+                 c->page_size, c->h_kv};
+    a->k_scale = c->dtype == FP_E4M3 ? c->k_scale : nullptr;
+    a->v_scale = c->dtype == FP_E4M3 ? c->v_scale : nullptr;
+    a->batch = q->batch;
+    a->h_q = q->h_q;
+    a->g = q->h_q / c->h_kv;
+    a->total_q = q->total_q;
+    a->max_q = q->max_q;
+    a->q = q->q;
+    a->q_stride_tok = q->q_stride_tok;
+    a->q_stride_head = q->q_stride_head;
+    a->q_scale = q->dtype == FP_E4M3 ? q->q_scale : nullptr;
+    a->cu = q->cu_seqlens_q;
+    a->seqlens_k = q->seqlens_k;
+    a->block_table = q->block_table;
+    a->max_pages = q->max_pages_per_seq;
+    const long long held = (long long)q->max_pages_per_seq * c->page_size, most = (1ll << 31) - 64;
+    a->max_len = (int)(held < most ? held : most);
+    a->scale = q->softmax_scale > 0.f ? q->softmax_scale : 1.f / sqrtf((float)kHeadDim);
+    return FP_OK;
 }
 
 }  // namespace
@@ -133,6 +173,34 @@ fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, cons
     a.num_slots = (long long)c->num_pages * c->page_size;
     a.status = static_cast<int *>(ws);
     return launch_rotate_rows(a, (cudaStream_t)stream) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
+}
+
+size_t fp_cache_attn_scratch_bytes(const fp_cache *c, const fp_qcache_query *q) {
+    PAttn a;
+    if (check_query(c, q, &a) != FP_OK) return 0;
+    a.k_scale = c->dtype == FP_E4M3 ? reinterpret_cast<const float *>(16) : nullptr;     // the type alone counts
+    return cache_attn_scratch_bytes(a);
+}
+
+fp_status fp_cache_attn(const fp_cache *c, const fp_qcache_query *q, void *out, float *lse_opt, void *scratch,
+                        size_t scratch_bytes, void *ws, size_t ws_bytes, void *stream) {
+    PAttn a;
+    fp_status s = check_query(c, q, &a);
+    if (s != FP_OK || (s = check_cache(c)) != FP_OK) return s;
+    if (!q->seqlens_k || !q->block_table || !aligned(q->seqlens_k, 4) || !aligned(q->block_table, 4) ||
+        !aligned(q->cu_seqlens_q, 4))
+        return FP_ERR_INVALID;
+    if (q->total_q > 0) {
+        if (!out || !aligned(out, 16) || !aligned(lse_opt, 4)) return FP_ERR_INVALID;
+        if (!rows_ok(q->q, q->q_stride_tok, q->q_stride_head, q->h_q, q->dtype, q->q_scale)) return FP_ERR_INVALID;
+    }
+    if ((s = check_ws(ws, ws_bytes)) != FP_OK) return s;
+    if (!scratch || !aligned(scratch, 16) || scratch_bytes < cache_attn_scratch_bytes(a)) return FP_ERR_WORKSPACE;
+    if (q->total_q == 0) return FP_OK;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse_opt;
+    a.status = static_cast<int *>(ws);
+    return launch_cache_attn(a, scratch, (cudaStream_t)stream) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
 }
 
 }  // extern "C"

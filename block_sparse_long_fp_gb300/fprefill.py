@@ -158,6 +158,9 @@ def lib():
             "fp_rope": ([POINTER(FpRopeTable), POINTER(FpRopeRows), c_void_p], c_int),
             "fp_cache_append": ([POINTER(FpCache), POINTER(FpRopeTable), POINTER(FpCacheRows), c_void_p, c_size_t,
                                  c_void_p], c_int),
+            "fp_cache_attn_scratch_bytes": ([POINTER(FpCache), PQ], c_size_t),
+            "fp_cache_attn": ([POINTER(FpCache), PQ, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_size_t, c_void_p],
+                              c_int),
             "fp_reset_status": ([c_void_p, c_void_p], c_int),
             "fp_device_status": ([c_void_p, c_void_p, POINTER(c_int)], c_int),
             "fp_status_string": ([c_int], ctypes.c_char_p),
@@ -507,7 +510,99 @@ class PageTables(_OnDevice):
         return self
 
 
-class QCache(_OnDevice):
+class _Cache(_OnDevice):
+    """What QCache and KVCache share: attention over their pages, and its scratch."""
+
+    def _entries(self, attn: str, *others):
+        """Sets up the entry points: `others`, pairs of names and argument counts, and last the attention's."""
+        self._scratch, self._scratch_bytes, self._lock = {}, {}, threading.Lock()
+        self._f = tuple(self._entry(*f) for f in others) + (self._entry(attn, 9),)
+        self._attn_name, self._scratch_query = attn, getattr(self._lib, attn + "_scratch_bytes")
+
+    def attn(self, q, block_table, seqlens_k, cu_seqlens_q=None, max_q=None, out=None, lse=None, want_lse=True,
+             q_scale=None, softmax_scale: float = 0.0):
+        """Attention of q (bf16 [total_q, h_q, 128], or e4m3 with q_scale [h_q])
+        over the cached tokens: (out bf16 [total_q, h_q, 128], lse fp32 [h_q,
+        total_q] or None).
+
+        block_table int32 [batch, max_pages], seqlens_k int32 [batch] (the
+        queries' own tokens included).  Request r owns rows cu_seqlens_q[r] ..
+        cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
+        cu_seqlens_q, max_q rows each (by default total_q / batch, which has to
+        be a whole number).  Rows behind the last request's are not written:
+        in an `out` of this call's own they are what the memory held."""
+        torch, dev, h_kv = self._torch, self._index, self.h_kv
+        shape, strides = q.shape, q.stride()
+        kinds = self._bf16 if q_scale is None else self._fp8
+        if not (len(shape) == 3 and q.dtype in kinds and q.get_device() == dev and strides[2] == 1 and shape[2] == 128 and
+                shape[1] % h_kv == 0):
+            _need(q, "q", kinds, dev, 3, False)
+            raise FprefillError(FP_ERR_INVALID, f"q: [rows, a multiple of {h_kv}, 128] with contiguous dims wanted, "
+                                f"got {tuple(shape)} {strides}")
+        total_q, h_q, _ = shape
+        batch = seqlens_k.shape[0]
+        seqlens_at = self._vector(seqlens_k, "seqlens_k", batch)
+        if not (block_table.dtype is self._int32 and block_table.dim() == 2 and block_table.shape[0] == batch and
+                block_table.get_device() == dev and block_table.is_contiguous()):
+            _need(block_table, "block_table", (self._int32,), dev, 2)
+            raise FprefillError(FP_ERR_INVALID, f"block_table: {batch} rows wanted, one for each length")
+        width = block_table.shape[1]
+        cu_at = 0 if cu_seqlens_q is None else self._vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
+        if max_q is None:
+            if cu_seqlens_q is None and batch and total_q % batch:
+                raise FprefillError(FP_ERR_INVALID, f"{total_q} rows are no equal share of {batch} requests: cu_seqlens_q or "
+                                    "max_q wanted")
+            max_q = max(1, total_q // batch if batch and cu_seqlens_q is None else total_q)
+        stride_head = strides[1] if h_q > 1 else 128
+        Q = _PACK_QUERY.pack(batch, h_q, total_q, max_q, FP_BF16 if q_scale is None else FP_E4M3, q.data_ptr(),
+                             strides[0] if total_q > 1 else h_q * stride_head, stride_head,
+                             0 if q_scale is None else self._scales(q_scale, "q_scale", h_q), cu_at, seqlens_at,
+                             block_table.data_ptr(), width, softmax_scale)
+        if out is None:
+            out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=self.device)
+        elif out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
+            _need(out, "out", self._bf16, dev, 3)
+            raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
+        if lse is not None:
+            _need(lse, "lse", (self._fp32,), dev, 2)
+            if lse.shape != (h_q, total_q):
+                raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
+        elif want_lse:
+            lse = torch.empty((h_q, total_q), dtype=self._fp32, device=self.device)
+        key = (batch, h_q, total_q, max_q, cu_at == 0, width)
+        n = self._scratch_bytes.get(key)
+        if n is None:
+            if len(self._scratch_bytes) >= 512:        # a server's rows may take any number of shapes
+                self._scratch_bytes.clear()
+            n = self._scratch_bytes[key] = int(
+                self._scratch_query(self._c, FpQCacheQuery.from_buffer_copy(Q)))
+        args = (self._bytes, Q, out.data_ptr(), 0 if lse is None else lse.data_ptr())
+        if torch.cuda.current_device() == dev:
+            self._attn(args, n)
+        else:
+            with torch.cuda.device(dev):
+                self._attn(args, n)
+        return out, lse
+
+    def _attn(self, args, n: int):
+        """fp_qcache_attn with n bytes of scratch of the current stream: calls on
+        two streams share none, and a captured call has its own, out of the
+        graph's memory.  The library enqueues two kernels that hand partial
+        results over in it: of threads on one stream, one enqueues at a time."""
+        torch, stream = self._torch, self._stream(self._index)
+        capturing = torch.cuda.is_current_stream_capturing()
+        with self._lock:
+            scratch = None if capturing else self._scratch.get(stream)
+            if scratch is None or scratch.numel() < n:
+                scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
+                if not capturing:
+                    self._scratch[stream] = scratch
+            s = self._f[-1](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
+        if s != FP_OK:
+            raise FprefillError(s, self._attn_name)
+
+
+class QCache(_Cache):
     """A paged K/V cache held in 4 bits: fp_qcache_write, fp_qcache_read and
     fp_qcache_attn on it.
 
@@ -529,9 +624,8 @@ class QCache(_OnDevice):
             raise FprefillError(FP_ERR_INVALID, f"data: [pages, heads, {c.page_size // 16}, {self.chunk_bytes(group)}] "
                                 f"wanted, got {tuple(data.shape)}")
         self.data, self.h_kv, self.page_size, self.group = data, c.h_kv, c.page_size, c.group
-        self._scratch, self._scratch_bytes, self._lock = {}, {}, threading.Lock()
         self._bytes = bytes(c)
-        self._f = self._entry("fp_qcache_write", 5), self._entry("fp_qcache_read", 5), self._entry("fp_qcache_attn", 9)
+        self._entries("fp_qcache_attn", ("fp_qcache_write", 5), ("fp_qcache_read", 5))
 
     @staticmethod
     def chunk_bytes(group: int = 32) -> int:
@@ -591,88 +685,6 @@ class QCache(_OnDevice):
         self._call(self._f[1], "fp_qcache_read", self._bytes, self._rows(k_out, v_out, slots, k_scale, v_scale, out_slots),
                    self._ws_ptr, FP_WS_HEADER_BYTES)
         return k_out, v_out
-
-    def attn(self, q, block_table, seqlens_k, cu_seqlens_q=None, max_q=None, out=None, lse=None, want_lse=True,
-             q_scale=None, softmax_scale: float = 0.0):
-        """Attention of q (bf16 [total_q, h_q, 128], or e4m3 with q_scale [h_q])
-        over the cached tokens: (out bf16 [total_q, h_q, 128], lse fp32 [h_q,
-        total_q] or None).
-
-        block_table int32 [batch, max_pages], seqlens_k int32 [batch] (the
-        queries' own tokens included).  Request r owns rows cu_seqlens_q[r] ..
-        cu_seqlens_q[r+1]-1 (int32 [batch+1]), at most max_q; without
-        cu_seqlens_q, max_q rows each (by default total_q / batch, which has to
-        be a whole number).  Rows behind the last request's are not written:
-        in an `out` of this call's own they are what the memory held."""
-        torch, dev, h_kv = self._torch, self._index, self.h_kv
-        shape, strides = q.shape, q.stride()
-        kinds = self._bf16 if q_scale is None else self._fp8
-        if not (len(shape) == 3 and q.dtype in kinds and q.get_device() == dev and strides[2] == 1 and shape[2] == 128 and
-                shape[1] % h_kv == 0):
-            _need(q, "q", kinds, dev, 3, False)
-            raise FprefillError(FP_ERR_INVALID, f"q: [rows, a multiple of {h_kv}, 128] with contiguous dims wanted, "
-                                f"got {tuple(shape)} {strides}")
-        total_q, h_q, _ = shape
-        batch = seqlens_k.shape[0]
-        seqlens_at = self._vector(seqlens_k, "seqlens_k", batch)
-        if not (block_table.dtype is self._int32 and block_table.dim() == 2 and block_table.shape[0] == batch and
-                block_table.get_device() == dev and block_table.is_contiguous()):
-            _need(block_table, "block_table", (self._int32,), dev, 2)
-            raise FprefillError(FP_ERR_INVALID, f"block_table: {batch} rows wanted, one for each length")
-        width = block_table.shape[1]
-        cu_at = 0 if cu_seqlens_q is None else self._vector(cu_seqlens_q, "cu_seqlens_q", batch + 1)
-        if max_q is None:
-            if cu_seqlens_q is None and batch and total_q % batch:
-                raise FprefillError(FP_ERR_INVALID, f"{total_q} rows are no equal share of {batch} requests: cu_seqlens_q or "
-                                    "max_q wanted")
-            max_q = max(1, total_q // batch if batch and cu_seqlens_q is None else total_q)
-        stride_head = strides[1] if h_q > 1 else 128
-        Q = _PACK_QUERY.pack(batch, h_q, total_q, max_q, FP_BF16 if q_scale is None else FP_E4M3, q.data_ptr(),
-                             strides[0] if total_q > 1 else h_q * stride_head, stride_head,
-                             0 if q_scale is None else self._scales(q_scale, "q_scale", h_q), cu_at, seqlens_at,
-                             block_table.data_ptr(), width, softmax_scale)
-        if out is None:
-            out = torch.empty((total_q, h_q, 128), dtype=torch.bfloat16, device=self.device)
-        elif out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
-            _need(out, "out", self._bf16, dev, 3)
-            raise FprefillError(FP_ERR_INVALID, "out: the shape of q wanted")
-        if lse is not None:
-            _need(lse, "lse", (self._fp32,), dev, 2)
-            if lse.shape != (h_q, total_q):
-                raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
-        elif want_lse:
-            lse = torch.empty((h_q, total_q), dtype=self._fp32, device=self.device)
-        key = (batch, h_q, total_q, max_q, cu_at == 0, width)
-        n = self._scratch_bytes.get(key)
-        if n is None:
-            if len(self._scratch_bytes) >= 512:        # a server's rows may take any number of shapes
-                self._scratch_bytes.clear()
-            n = self._scratch_bytes[key] = int(
-                self._lib.fp_qcache_attn_scratch_bytes(self._c, FpQCacheQuery.from_buffer_copy(Q)))
-        args = (self._bytes, Q, out.data_ptr(), 0 if lse is None else lse.data_ptr())
-        if torch.cuda.current_device() == dev:
-            self._attn(args, n)
-        else:
-            with torch.cuda.device(dev):
-                self._attn(args, n)
-        return out, lse
-
-    def _attn(self, args, n: int):
-        """fp_qcache_attn with n bytes of scratch of the current stream: calls on
-        two streams share none, and a captured call has its own, out of the
-        graph's memory.  The library enqueues two kernels that hand partial
-        results over in it: of threads on one stream, one enqueues at a time."""
-        torch, stream = self._torch, self._stream(self._index)
-        capturing = torch.cuda.is_current_stream_capturing()
-        with self._lock:
-            scratch = None if capturing else self._scratch.get(stream)
-            if scratch is None or scratch.numel() < n:
-                scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
-                if not capturing:
-                    self._scratch[stream] = scratch
-            s = self._f[2](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
-        if s != FP_OK:
-            raise FprefillError(s, "fp_qcache_attn")
 
 
 def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -755,9 +767,9 @@ class Rope(_OnDevice):
         return out
 
 
-class KVCache(_OnDevice):
+class KVCache(_Cache):
     """The bf16 or e4m3 paged K/V cache that Layer reads, at any position:
-    fp_cache_append on it.
+    fp_cache_append and fp_cache_attn on it.
 
     k_cache, v_cache: [num_pages, page_size, h_kv, 128], bf16, or e4m3 (uint8
     codes or torch.float8_e4m3fn) with k_scale and v_scale (fp32 [h_kv]).
@@ -781,7 +793,7 @@ class KVCache(_OnDevice):
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
         self.h_kv, self.page_size = c.h_kv, c.page_size
         self._bytes = bytes(c)
-        self._f = self._entry("fp_cache_append", 6)
+        self._entries("fp_cache_attn", ("fp_cache_append", 6))
 
     def append(self, k, v, slots, rope: Rope | None = None, positions=None, q=None, q_out=None, q_scale=None):
         """Rows of k and v (bf16 [rows, h_kv, 128]) into `slots` (int32 [rows]; -1:
@@ -817,7 +829,7 @@ class KVCache(_OnDevice):
         R = _PACK_APPEND.pack(rows, h_q if q_at[0] else 0, k_at[0], v_at[0], q_at[0], *k_at[1:], *v_at[1:], *q_at[1:],
                               *out_at, FP_E4M3 if scale_at else FP_BF16, scale_at, slots_at,
                               0 if rope is None else self._vector(positions, "positions", rows))
-        self._call(self._f, "fp_cache_append", self._bytes, 0 if rope is None else rope._bytes, R, self._ws_ptr,
+        self._call(self._f[0], "fp_cache_append", self._bytes, 0 if rope is None else rope._bytes, R, self._ws_ptr,
                    FP_WS_HEADER_BYTES)
         return q_out
 

@@ -597,6 +597,23 @@ typedef struct {
 fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, const fp_cache_rows *r, void *ws,
                           size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * fp_cache_attn -- attention over the paged cache at any position
+ *
+ *   As fp_qcache_attn, over the bf16 values, or the e4m3 codes times their head's scales, of
+ *   `c`: the same query structure, results, refusals, status and scratch rules (with
+ *   fp_cache_attn_scratch_bytes()).  Queries are bf16 or e4m3, whatever the cache's type.
+ *   Keys and values that a row does not attend may be anything.  In a value that a row
+ *   attends, a NaN or an infinity makes that dim of the row one that is not finite; in a key,
+ *   a NaN makes the row NaN.
+ *   Logits and sums are fp32.  Weights enter the sum of values in bf16 for a bf16 cache (half
+ *   a step, 2^-9 of each), in fp16 for an e4m3 one (2^-12; nothing below 2^-34 of the row's
+ *   largest), where bf16 queries enter as fp16 under a power of two of the row (nothing
+ *   below 2^-39 of its largest). */
+size_t fp_cache_attn_scratch_bytes(const fp_cache *c, const fp_qcache_query *q);
+fp_status fp_cache_attn(const fp_cache *c, const fp_qcache_query *q, void *out, float *lse_opt, void *scratch,
+                        size_t scratch_bytes, void *ws, size_t ws_bytes, void *stream);
+
 /* Zero the status header of a workspace (enqueued on stream). */
 fp_status fp_reset_status(void *ws, void *stream);
 

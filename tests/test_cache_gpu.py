@@ -344,3 +344,310 @@ def test_append_captured_and_replayed(fp):
         got = r.apply(k, pos)
     s.synchronize()
     assert torch.equal(got, r.apply(k, pos))
+
+
+# -- attention --------------------------------------------------------------------
+
+def attn_case(fp, reqs, h_q, h, page, dtype, q_dtype, seed=0, spare=3, k_scale=1.0, q_scale=1.5, pad_rows=0):
+    """Requests (length, queries) over a shuffled cache; what lies behind a request's last token is poison."""
+    import torch
+    rng = np.random.default_rng(seed)
+    lens, lq = [n for n, _ in reqs], [m for _, m in reqs]
+    count = [-(-n // page) for n in lens]
+    pool = sum(count) + spare
+    order = rng.permutation(pool)
+    table = np.full((len(reqs), max(1, max(count)) + 1), -9, np.int64)
+    at = 0
+    for r, c in enumerate(count):
+        table[r, :c] = order[at:at + c]
+        at += c
+    g = torch.Generator().manual_seed(seed)
+    shape = (pool, page, h, 128)
+    bias = torch.randn((h, 128), generator=g)
+    k = torch.randn(shape, generator=g) * k_scale + bias * bias.abs() * k_scale
+    v = torch.randn(shape, generator=g)
+    used = torch.zeros((pool, page), dtype=torch.bool)
+    for r, (n, c) in enumerate(zip(lens, count)):
+        for j in range(c):
+            used[table[r, j], :min(page, n - j * page)] = True
+    total = sum(lq) + pad_rows
+    q = torch.randn((total, h_q, 128), generator=g) * q_scale
+    ks = vs = qs = None
+    if dtype == "e4m3":
+        ks, vs = (0.01 + 0.02 * torch.rand(h, generator=g) for _ in range(2))
+        k, v = ((x / s.view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) for x, s in ((k, ks), (v, vs)))
+        k[~used], v[~used] = 0x7f, 0xff                                   # NaN
+    else:
+        k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+        k[~used], v[~used] = math.nan, math.inf
+    if q_dtype == "e4m3":
+        qs = 0.01 + 0.02 * torch.rand(h_q, generator=g)
+        q = (q / qs.view(-1, 1)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        q = q.to(torch.bfloat16)
+    up = [None if x is None else x.cuda() for x in (ks, vs, qs)]
+    c = fp.KVCache(k.cuda(), v.cuda(), up[0], up[1])
+
+    def values(x, s):
+        return host(x) if s is None else host(x) * s.double().numpy()[:, None]
+    cu = np.concatenate([[0], np.cumsum(lq)])
+    return dict(c=c, q=q.cuda(), q_scale=up[2], table=table, lens=lens, lq=lq, cu=cu, qv=values(q, qs),
+                kv=values(k, ks), vv=values(v, vs))
+
+
+def reference(s, scale=None):
+    """(out, lse, bound of out, bound of lse).
+
+    A logit: 128 exact products summed in fp32, cut at 2^-23 of the partial sums a step: 2^-16 of the sum of
+    their magnitudes at most; scaling and subtracting the maximum round at 2^-24 of the logit, the exponential
+    is within 2^-22: d.  A weight is off by d, and by its rounding to bf16 (2^-8) or fp16 (2^-11): an output by
+    that much of the weighted magnitudes of the values, then by fp32 sums of up to n terms cut at 2^-23 (a step
+    sums 16, in 4 warps and several blocks), and by its own rounding (2^-8).  The LSE: d, a sum of n positive
+    weights over 64 lanes and warps, and the rounding of itself."""
+    out, lse = oc.attention(s["qv"], s["kv"], s["vv"], s["table"], s["lens"], s["lq"], scale)
+    scale = 1 / math.sqrt(128) if scale is None else scale
+    with np.errstate(invalid="ignore"):
+        reach, _ = oc.attention(s["qv"], s["kv"], np.abs(s["vv"]), s["table"], s["lens"], s["lq"], scale)
+    n = max(1, max(s["lens"]))
+    kmax = np.abs(np.nan_to_num(s["kv"], nan=0.0, posinf=0.0)).max((0, 1))               # [h, 128]
+    g = s["qv"].shape[1] // kmax.shape[0]
+    size = scale * (np.abs(s["qv"]) * np.repeat(kmax, g, 0)).sum(-1)                      # [rows, h_q]
+    d = 2.0 ** -16 * size + 2.0 ** -20
+    w = 2.0 ** -11 if s["c"].k_scale is not None else 2.0 ** -8
+    tol = 2.0 ** -8 * np.abs(out) + reach * (w + 2 * d[..., None] + 2.0 ** -23 * (n / 16 + 64)) + 1e-30
+    lse_tol = d.T + 2.0 ** -24 * (n / 64 + 64) + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
+    return out, lse, tol, lse_tol
+
+
+def check_attn(s, got, lse, scale=None, rows=None):
+    want, want_lse, tol, lse_tol = reference(s, scale)
+    n = sum(s["lq"]) if rows is None else rows
+    got, lse = host(got)[:n], host(lse)[:, :n]
+    bad = ~(np.abs(got - want[:n]) <= tol[:n])
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], got[bad][:3], want[:n][bad][:3], tol[:n][bad][:3])
+    none = np.isneginf(want_lse[:, :n])
+    assert np.array_equal(np.isneginf(lse), none)
+    assert not got[none.T].any()
+    assert np.all(np.abs(lse - want_lse[:, :n])[~none] <= lse_tol[:, :n][~none])
+
+
+def run_attn(s, max_q=None, **kw):
+    cu = i32(s["cu"])
+    return s["c"].attn(s["q"], i32(s["table"]), i32(s["lens"]), cu_seqlens_q=cu, max_q=max_q or max(1, max(s["lq"])),
+                       q_scale=s["q_scale"], **kw)
+
+
+TYPES = [("bf16", "bf16"), ("e4m3", "e4m3"), ("e4m3", "bf16"), ("bf16", "e4m3")]
+
+
+@pytest.mark.parametrize("dtype,q_dtype", TYPES)
+@pytest.mark.parametrize("reqs,h_q,h,page", [
+    ([(1, 1)], 1, 1, 16), ([(700, 1)], 32, 8, 16), ([(15, 1), (16, 1), (17, 1), (0, 1), (129, 1)], 8, 1, 128),
+    ([(5001, 1), (64, 1), (0, 1), (1999, 1), (3, 1)], 15, 5, 256), ([(40000, 1)], 16, 2, 64),
+    ([(300, 3), (2, 2), (1, 4), (0, 2), (90, 1)], 6, 2, 32), ([(1000, 8), (3000, 5), (8, 8)], 32, 8, 64),
+    ([(2100, 4), (77, 1), (450, 2)], 48, 3, 16), ([(9000, 2), (33, 33), (500, 20)], 12, 3, 384),
+    ([(130, 130), (1, 1)], 4, 4, 64), ([(100 + 37 * i, 1) for i in range(70)], 16, 4, 32)])
+def test_attn(fp, reqs, h_q, h, page, dtype, q_dtype):
+    s = attn_case(fp, reqs, h_q, h, page, dtype, q_dtype, seed=len(reqs) + h_q)
+    out, lse = run_attn(s)
+    check_attn(s, out, lse)
+    assert s["c"].device_status() == 0
+    again, lse2 = run_attn(s)                          # the same call gives the same bits
+    assert bool((again == out).all()) and bool((lse2 == lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq", [1, 3, 7])
+def test_attn_without_offsets_and_with_wider_bounds(fp, lq, dtype):
+    """Equal rows need no offsets; a bound above the rows there are changes nothing beyond rounding."""
+    import torch
+    s = attn_case(fp, [(900, lq), (31, lq), (lq, lq)], 8, 2, 32, dtype, "bf16", seed=4)
+    table, lens = i32(s["table"]), i32(s["lens"])
+    out, lse = s["c"].attn(s["q"], table, lens)
+    check_attn(s, out, lse)
+    for bound in (lq, lq + 1, 20, 300):
+        check_attn(s, *run_attn(s, max_q=bound))
+    out, none = run_attn(s, want_lse=False)
+    assert none is None
+    given = torch.empty_like(out), torch.empty((8, 3 * lq), device="cuda")
+    got = run_attn(s, out=given[0], lse=given[1])
+    assert got[0] is given[0] and got[1] is given[1]
+    check_attn(s, *got)
+    scaled = run_attn(s, softmax_scale=0.2)
+    check_attn(s, *scaled, scale=0.2)
+
+
+def test_attn_strided_queries_and_rows_behind(fp):
+    """Queries inside a fused projection; rows behind the last request's are left as they were."""
+    import torch
+    s = attn_case(fp, [(400, 2), (90, 1)], 8, 2, 64, "bf16", "bf16", seed=6, pad_rows=5)
+    wide = torch.full((8, 14, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:11] = s["q"]
+    s["q"] = wide[:, 3:11]
+    out = torch.full((8, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, 8), 5.0, device="cuda")
+    run_attn(s, out=out, lse=lse)
+    check_attn(s, out, lse, rows=3)
+    assert bool((out[3:] == 3).all()) and bool((lse[:, 3:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype,bad", [("bf16", math.nan), ("bf16", math.inf), ("e4m3", math.nan)])
+@pytest.mark.parametrize("lq,h_q", [(2, 4), (9, 8), (40, 4)])
+def test_attn_not_finite_reaches_only_rows_that_attend(fp, dtype, bad, lq, h_q):
+    """A value that is not finite: its dim of the rows that attend it, no other.  In a key: the whole rows."""
+    n, page, h = 230, 32, 2
+    for at in (n - 1, n - lq + 1, n - lq, 17):         # the last token's, the second row's own, the first row's, a common one
+        for side in ("v", "k"):
+            s = attn_case(fp, [(n, lq), (50, 1)], h_q, h, page, dtype, "bf16", seed=at)
+            c, name = s["c"], {"v": "vv", "k": "kv"}[side]
+            cache = c.v_cache if side == "v" else c.k_cache
+            pg = int(s["table"][0, at // page])
+            cache[pg, at % page, 1, 77] = (0x7f if dtype == "e4m3" else bad)
+            s[name][pg, at % page, 1, 77] = math.nan
+            out, lse = run_attn(s)
+            got = host(out)
+            want, _ = oc.attention(s["qv"], s["kv"], s["vv"], s["table"], s["lens"], s["lq"])
+            rows = np.arange(lq) + n - lq >= at                                  # that attend it
+            hit = np.zeros(got.shape, bool)
+            heads = slice(h_q // 2, h_q)
+            if side == "v":
+                hit[:lq, heads, 77] = rows[:, None]
+            else:
+                hit[:lq, heads] = rows[:, None, None]
+            if side == "k" and math.isinf(bad):        # an infinite logit: the row is NaN, or the key counts for nothing
+                assert np.isfinite(got[~hit]).all()
+                continue
+            assert np.array_equal(~np.isfinite(got), hit), (at, side)
+            s2 = dict(s, vv=np.nan_to_num(s["vv"]), kv=np.nan_to_num(s["kv"]))
+            ref, _, tol, _ = reference(s2)
+            ok = ~hit
+            assert np.all(np.abs(got - ref)[ok] <= tol[ok])
+
+
+def test_attn_sharp_and_flat_rows(fp):
+    """Logits of a thousand and of nothing, a maximum that rises token by token, values of large mean."""
+    import torch
+    for dtype in ("bf16", "e4m3"):
+        s = attn_case(fp, [(3000, 1), (600, 4)], 8, 2, 64, dtype, "bf16", seed=9, k_scale=1.0, q_scale=30.0)
+        check_attn(s, *run_attn(s))
+        s = attn_case(fp, [(3000, 1), (600, 4)], 8, 2, 64, dtype, "bf16", seed=9, q_scale=0.0)
+        check_attn(s, *run_attn(s))
+    s = attn_case(fp, [(2000, 1)], 4, 1, 64, "bf16", "bf16", seed=3)
+    t = torch.arange(2000)
+    pages = torch.as_tensor(s["table"][0])[t // 64]
+    ramp = (t.float() / 8).to(torch.bfloat16)
+    s["c"].k_cache[pages.cuda(), (t % 64).cuda(), 0] = ramp[:, None].cuda() / 8
+    s["c"].v_cache += 5
+    s["kv"], s["vv"] = host(s["c"].k_cache), host(s["c"].v_cache)
+    s["q"].fill_(0.25)
+    s["qv"] = host(s["q"])
+    check_attn(s, *run_attn(s))
+
+
+def test_attn_bad_device_data(fp):
+    """Pages out of range read as zeros, lengths out of range as an empty cache, rows outside q are left out."""
+    s = attn_case(fp, [(200, 2), (90, 1)], 4, 2, 32, "bf16", "bf16", seed=5)
+    c = s["c"]
+    for bad in (-1, c.k_cache.shape[0], 2 ** 31 - 1):
+        t = dict(s, table=s["table"].copy())
+        t["table"][0, 2] = bad
+        check_attn(t, *run_attn(t))
+        assert c.device_status() == 5
+        c.reset_status()
+    for bad in (-1, s["table"].shape[1] * 32 + 1, 2 ** 31 - 1):
+        t = dict(s, lens=[bad, 90])
+        out, lse = run_attn(t)
+        t["lens"] = [0, 90]
+        check_attn(t, out, lse)
+        assert c.device_status() == 5
+        c.reset_status()
+    for cu in ([0, 2, 9], [-3, 2, 3], [0, 2, 1], [5, 7, 9], [0, 2 ** 31 - 1, 3]):
+        c.attn(s["q"], i32(s["table"]), i32(s["lens"]), cu_seqlens_q=i32(cu), max_q=2)
+        c.device_status()
+        c.reset_status()
+    check_attn(s, *run_attn(s))
+    assert c.device_status() == 0
+
+
+def test_attn_refusals(fp):
+    import torch
+    s = attn_case(fp, [(200, 1), (90, 1)], 4, 2, 32, "bf16", "bf16", seed=5)
+    c, table, lens = s["c"], i32(s["table"]), i32(s["lens"])
+    good = dict(q=s["q"], block_table=table, seqlens_k=lens)
+    q8 = s["q"].to(torch.float8_e4m3fn)
+    for bad in (dict(q=s["q"][:, :3]), dict(q=s["q"].float()), dict(q=q8), dict(q_scale=f32([1] * 4)), dict(q=s["q"].cpu()),
+                dict(block_table=table[:1]), dict(block_table=table.long()), dict(seqlens_k=lens[:1]),
+                dict(cu_seqlens_q=i32([0, 1])), dict(max_q=0), dict(out=s["q"][:1]), dict(lse=f32(np.zeros((2, 4)))),
+                dict(q=s["q"][:1]), dict(max_q=2), dict(q=q8, q_scale=f32([1] * 3))):
+        with pytest.raises(fp.FprefillError):
+            c.attn(**dict(good, **bad))
+    out, lse = c.attn(s["q"][:0], table, lens, cu_seqlens_q=i32([0, 0, 0]))
+    assert out.shape == (0, 4, 128) and lse.shape == (4, 0)
+
+
+def test_attn_past_4_gb(fp):
+    """A request whose last pages lie past 2^32 bytes of the cache."""
+    import torch
+    page, h, pages = 128, 8, 20000
+    k = torch.zeros((pages, page, h, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    c = fp.KVCache(k, v)
+    ids = [pages - 1, 3, pages - 2]
+    for j, p in enumerate(ids):
+        k[p], v[p] = bf16(j, page, h, 128), bf16(10 + j, page, h, 128)
+    s = dict(c=c, q=bf16(30, 2, 16, 128), q_scale=None, table=np.array([ids]), lens=[300], lq=[2], cu=np.array([0, 2]))
+    small = np.array([[0, 1, 2]])
+    s["qv"] = host(s["q"])
+    out, lse = run_attn(s)
+    at = torch.as_tensor(ids).cuda()
+    check_attn(dict(s, table=small, kv=host(k[at]), vv=host(v[at])), out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_captured_two_graphs_and_streams(fp, dtype):
+    """Graphs read the lengths and tables of the moment; two graphs, two streams and threads share nothing."""
+    import threading
+    import torch
+    a = attn_case(fp, [(6000, 1), (90, 1), (0, 1)], 32, 8, 64, dtype, "bf16", seed=1)
+    b = attn_case(fp, [(50, 1), (3000, 1), (777, 1)], 32, 8, 64, dtype, "bf16", seed=2)
+    width = max(a["table"].shape[1], b["table"].shape[1])
+    for s in (a, b):
+        s["table"] = np.pad(s["table"], ((0, 0), (0, width - s["table"].shape[1])), constant_values=-1)
+        run_attn(s)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in (a, b):
+        table, lens, cu = i32(s["table"]), i32(s["lens"]), i32(s["cu"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = s["c"].attn(s["q"], table, lens, cu_seqlens_q=cu, max_q=1)
+        graphs.append((g, out, lens, table, cu))       # the graph reads them: they stay
+    for _ in range(3):
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for st in streams:
+            st.wait_stream(torch.cuda.current_stream())
+        for (g, *_), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for s, (_, out, *_) in zip((a, b), graphs):
+            check_attn(s, *out)
+    graphs[0][2].copy_(i32([5000, 64, 0]))
+    graphs[0][0].replay()
+    check_attn(dict(a, lens=[5000, 64, 0]), *graphs[0][1])
+    results = [[], []]
+
+    def work(s, got):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got.append(run_attn(s))
+            torch.cuda.current_stream().synchronize()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=x) for x in zip((a, a), results)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for got in results:
+        for out in got:
+            check_attn(a, *out)

@@ -192,3 +192,37 @@ def test_oracle_attention_is_softmax_attention():
             assert np.allclose(o[i, a], p @ vr[:33 + i, a // 2] / p.sum()) and np.isclose(lse[a, i], np.log(p.sum()))
     o, lse = oc.attention(q, k, v, table, [2], [3])              # the first row has no key
     assert not o[0].any() and np.all(lse[:, 0] == -np.inf) and np.all(np.isfinite(lse[:, 1:]))
+
+
+# -- the attention's refusals -------------------------------------------------------
+
+def query(fp, **over):
+    return filled(fp.FpQCacheQuery(3, 16, 3, 1, fp.FP_BF16, P, 2048, 128, 0, 0, P, P, 8, 0.0), over)
+
+
+def attn(fp, c=None, q=None, out=P, lse=P, scratch=P, scratch_bytes=1 << 40, ws=P, ws_bytes=256):
+    return fp.lib().fp_cache_attn(c or cache(fp), q or query(fp), out, lse, scratch, scratch_bytes, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(batch=0), 1), (dict(batch=4097, total_q=5000), 2), (dict(h_q=6), 1), (dict(h_q=0), 1), (dict(total_q=-1), 1),
+    (dict(max_q=0), 1), (dict(max_q=2), 1), (dict(dtype=5), 1), (dict(q=None), 1), (dict(q=P + 8), 1),
+    (dict(q_stride_tok=2040), 1), (dict(q_stride_head=64), 1), (dict(dtype=1), 1), (dict(dtype=1, q_scale=P + 1), 1),
+    (dict(seqlens_k=None), 1), (dict(block_table=None), 1), (dict(block_table=P + 2), 1), (dict(cu_seqlens_q=P + 2), 1),
+    (dict(max_pages_per_seq=0), 1), (dict(total_q=(1 << 26) + 1, cu_seqlens_q=P), 2),
+])
+def test_attn_refusals(fp, over, code):
+    assert attn(fp, q=query(fp, **over)) == code
+
+
+def test_attn_refuses_caches_and_buffers(fp):
+    assert attn(fp, out=None) == 1 and attn(fp, out=P + 2) == 1 and attn(fp, lse=P + 2) == 1
+    assert attn(fp, scratch=None) == 3 and attn(fp, scratch=P + 8) == 3 and attn(fp, scratch_bytes=0) == 3
+    assert attn(fp, ws=None) == 3 and attn(fp, ws_bytes=8) == 3
+    assert attn(fp, c=cache(fp, k=None)) == 1 and attn(fp, c=cache(fp, page_size=24)) == 2
+    assert attn(fp, c=cache(fp, dtype=1)) == 1 and attn(fp, c=cache(fp, d=64)) == 2
+    assert attn(fp, q=query(fp, total_q=0, cu_seqlens_q=P, q=None), out=None) == 0
+    L = fp.lib()
+    assert L.fp_cache_attn_scratch_bytes(cache(fp), query(fp)) >= 16
+    assert L.fp_cache_attn_scratch_bytes(cache(fp), query(fp, max_q=2)) == 0
+    assert L.fp_cache_attn_scratch_bytes(cache(fp, page_size=24), query(fp)) == 0
