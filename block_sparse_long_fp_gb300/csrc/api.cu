@@ -13,6 +13,14 @@ namespace {
 
 unsigned long long g_wait_ns = 200000000ull;    // bounded-wait limit inside kernels (200 ms)
 
+}  // namespace
+
+namespace fp {
+unsigned long long wait_limit_ns() { return g_wait_ns; }
+}  // namespace fp
+
+namespace {
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

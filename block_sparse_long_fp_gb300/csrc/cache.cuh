@@ -54,8 +54,15 @@ struct PAttn {
     float *lse;
     int *status;
     bool whole;                                // no item is cut (set by the launch)
+    int most_columns;                          // rows times g up to which a request is the columns' (set by the launch)
 };
+// cache_attn.cu: by columns, and which of the two takes what
 size_t cache_attn_scratch_bytes(const PAttn &a);
-cudaError_t launch_cache_attn(const PAttn &a, void *scratch, cudaStream_t st);
+cudaError_t launch_cache_attn(const PAttn &a, void *scratch, unsigned long long limit_ns, cudaStream_t st);
+// cache_tiles.cu: the requests of more columns, by tiles
+size_t cache_tiles_scratch_bytes(const PAttn &a);
+cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long limit_ns, cudaStream_t st);
+// the limit of bounded waits (fp_set_wait_limit_ns)
+unsigned long long wait_limit_ns();
 
 }  // namespace fp

@@ -200,7 +200,7 @@ fp_status fp_cache_attn(const fp_cache *c, const fp_qcache_query *q, void *out, 
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse_opt;
     a.status = static_cast<int *>(ws);
-    return launch_cache_attn(a, scratch, (cudaStream_t)stream) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
+    return launch_cache_attn(a, scratch, wait_limit_ns(), (cudaStream_t)stream) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
 }
 
 }  // extern "C"

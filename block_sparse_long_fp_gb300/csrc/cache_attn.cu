@@ -211,9 +211,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
 
     // this block's range of units, and the request it starts in: an item is its start and
     // end, then its chunks
+    const auto tiles_of_columns = [&](const Request &q) {
+        return (long long)q.rows * a.g > a.most_columns ? 0 : tiles_of(a, q, kCols);
+    };
     const auto octets_of = [&](const Request &q, int tile) { return (min(kCols, q.rows * a.g - tile * kCols) + 7) / 8; };
     const auto units = [&](const Request &q) {
-        const int tiles = tiles_of(a, q, kCols);
+        const int tiles = tiles_of_columns(q);
         if (tiles == 0 || a.whole) return (long long)a.c.h_kv * tiles;
         return (long long)a.c.h_kv * (kItem + chunks_of(q)) *
                ((tiles - 1) * chunk_units<NT>(NT) + chunk_units<NT>(octets_of(q, tiles - 1)));
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
     int r = s_r;
     long long item0 = s_at;                       // first unit of the current item
     q = s_q;
-    int tiles = tiles_of(a, q, kCols), chunks = chunks_of(q);
+    int tiles = tiles_of_columns(q), chunks = chunks_of(q);
     int kv, tile;                                 // of the current item
     {
         const long long full = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<NT>(NT);
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
         while (kv >= a.c.h_kv || tiles == 0) {    // the next request that has rows
             if (++r >= a.batch) return;           // lengths that changed under the kernel
             q = request_of(a, r);
-            tiles = tiles_of(a, q, kCols);
+            tiles = tiles_of_columns(q);
             chunks = chunks_of(q);
             kv = tile = 0;
         }
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
             const long long last = next - 1;                 // and the block that has it
             const long long ends = longer * (share + 1);       // of the longer blocks
             const int b = (int)(last < ends ? quotient(last, share + 1) : longer + quotient(last - ends, share));
-            sc.open[blockIdx.x] = Open{b - (int)blockIdx.x + 1, q.row0, q.rows, kv, tile};
+            sc.open[blockIdx.x] = Open{min(b, blocks - 1) - (int)blockIdx.x + 1, q.row0, q.rows, kv, tile};
         }
         __syncthreads();
         at = item0 = next;
@@ -617,11 +620,17 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
     }
 }
 
+// Requests of more columns go to the tiles of 256 rows.
+constexpr int kMostColumns = 64;
+bool with_tiles(const PAttn &a) { return a.g <= 256 && (long long)a.max_q * a.g > kMostColumns; }
+bool with_columns(const PAttn &a) { return a.cu || !with_tiles(a); }
+
 // Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32;
-// where the rows differ, what most of them fill, by the mean that the host knows.
+// where the rows differ, what most of them fill, by the mean that the host knows; beside
+// tiles of rows, what a decoding request fills.
 int tile_columns(const PAttn &a) {
-    const long long cols = (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
-    const bool ragged = a.cu && a.total_q != (long long)a.batch * a.max_q;
+    const long long cols = with_tiles(a) ? a.g : (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
+    const bool ragged = a.cu && !with_tiles(a) && a.total_q != (long long)a.batch * a.max_q;
     if (cols <= 8 || (ragged && all <= 8ll * a.batch)) return 8;
     return cols <= 16 || (ragged && all <= 16ll * a.batch) ? 16 : 32;
 }
@@ -674,22 +683,30 @@ size_t cache_attn_scratch_bytes(const PAttn &args) {
     PAttn a = args;
     a.whole = whole_items(a);
     const size_t n = blocks_of(a), cols = tile_columns(a);
-    return align256(n * sizeof(Open)) + align256(n * 2 * cols * sizeof(float2)) + n * 2 * cols * kHeadDim * sizeof(float);
+    const size_t columns =
+        align256(n * sizeof(Open)) + align256(n * 2 * cols * sizeof(float2)) + n * 2 * cols * kHeadDim * sizeof(float);
+    const size_t tiles = with_tiles(a) ? cache_tiles_scratch_bytes(a) : 0;       // one after the other in the same memory
+    return with_columns(a) && columns > tiles ? columns : tiles;
 }
 
-cudaError_t launch_cache_attn(const PAttn &args, void *scratch, cudaStream_t st) {
+cudaError_t launch_cache_attn(const PAttn &args, void *scratch, unsigned long long limit_ns, cudaStream_t st) {
     PAttn a = args;
     a.whole = whole_items(a);
-    const size_t n = blocks_of(a), cols = tile_columns(a);
-    char *p = static_cast<char *>(scratch);
-    Scratch sc;
-    sc.open = reinterpret_cast<Open *>(p);
-    p += align256(n * sizeof(Open));
-    sc.ml = reinterpret_cast<float2 *>(p);
-    p += align256(n * 2 * cols * sizeof(float2));
-    sc.o = reinterpret_cast<float *>(p);
-    return a.k_scale ? launch_columns<true>(a, sc, (int)cols, (int)n, st)
-                     : launch_columns<false>(a, sc, (int)cols, (int)n, st);
+    a.most_columns = with_tiles(a) ? (a.cu ? kMostColumns : 0) : INT_MAX;
+    if (with_columns(a)) {
+        const size_t n = blocks_of(a), cols = tile_columns(a);
+        char *p = static_cast<char *>(scratch);
+        Scratch sc;
+        sc.open = reinterpret_cast<Open *>(p);
+        p += align256(n * sizeof(Open));
+        sc.ml = reinterpret_cast<float2 *>(p);
+        p += align256(n * 2 * cols * sizeof(float2));
+        sc.o = reinterpret_cast<float *>(p);
+        const cudaError_t e = a.k_scale ? launch_columns<true>(a, sc, (int)cols, (int)n, st)
+                                        : launch_columns<false>(a, sc, (int)cols, (int)n, st);
+        if (e != cudaSuccess) return e;
+    }
+    return with_tiles(a) ? launch_cache_tiles(a, scratch, limit_ns, st) : cudaSuccess;
 }
 
 }  // namespace fp

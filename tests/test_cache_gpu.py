@@ -651,3 +651,110 @@ def test_attn_captured_two_graphs_and_streams(fp, dtype):
     for got in results:
         for out in got:
             check_attn(a, *out)
+
+
+# -- requests of many rows --------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,q_dtype", TYPES)
+@pytest.mark.parametrize("reqs,h_q,h,page", [
+    ([(128, 128)], 1, 1, 128), ([(65, 65)], 1, 1, 16), ([(700, 300)], 8, 1, 64), ([(129, 129), (1, 1), (0, 70), (40, 90)], 4, 2, 32),
+    ([(5000, 17)], 16, 2, 256), ([(1000, 1000)], 6, 3, 16), ([(2111, 129), (64, 64), (3000, 1), (333, 100)], 14, 2, 384),
+    ([(1500, 33), (900, 700)], 64, 2, 64), ([(20000, 130)], 4, 1, 32), ([(150 + 11 * i, 90 + i) for i in range(40)], 8, 4, 64)])
+def test_attn_of_many_rows(fp, reqs, h_q, h, page, dtype, q_dtype):
+    s = attn_case(fp, reqs, h_q, h, page, dtype, q_dtype, seed=len(reqs) + h_q)
+    out, lse = run_attn(s)
+    assert s["c"].device_status() == 0
+    check_attn(s, out, lse)
+    again, lse2 = run_attn(s)
+    assert bool((again == out).all()) and bool((lse2 == lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_of_equal_rows_without_offsets(fp, dtype):
+    s = attn_case(fp, [(900, 40), (331, 40), (40, 40)], 8, 2, 32, dtype, "bf16", seed=4)
+    out, lse = s["c"].attn(s["q"], i32(s["table"]), i32(s["lens"]))
+    check_attn(s, out, lse)
+    for bound in (8, 16, 17, 400):                     # a bound that is too low changes nothing either
+        check_attn(s, *run_attn(s, max_q=bound))
+    assert s["c"].device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_of_many_rows_strided_and_rows_behind(fp, dtype):
+    import torch
+    s = attn_case(fp, [(400, 100), (90, 1)], 8, 2, 64, dtype, "bf16", seed=6, pad_rows=5)
+    wide = torch.full((106, 14, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:11] = s["q"]
+    s["q"] = wide[:, 3:11]
+    out = torch.full((106, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, 106), 5.0, device="cuda")
+    run_attn(s, out=out, lse=lse)
+    check_attn(s, out, lse, rows=101)
+    assert bool((out[101:] == 3).all()) and bool((lse[:, 101:] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq,h_q", [(300, 2), (200, 16)])
+def test_attn_of_many_rows_not_finite(fp, dtype, lq, h_q):
+    """Values that are not finite at the diagonal, before it, and in several dims and blocks at once."""
+    n, page, h = 1500, 64, 2
+    s = attn_case(fp, [(n, lq)], h_q, h, page, dtype, "bf16", seed=3)
+    hit = np.zeros((lq, h_q, 128), bool)
+    for at, d in ((n - 1, 5), (n - lq, 6), (n - lq + 1, 7), (n - 150, 8), (n - 150, 127), (n - 100, 8), (100, 0), (n - lq - 1, 64)):
+        pg = int(s["table"][0, at // page])
+        s["c"].v_cache[pg, at % page, 1, d] = 0xff if dtype == "e4m3" else math.nan
+        s["vv"][pg, at % page, 1, d] = math.nan
+        hit[np.arange(lq) + n - lq >= at, h_q // 2:, d] = True
+    out, _ = run_attn(s)
+    got = host(out)
+    assert np.array_equal(np.isnan(got), hit)
+    ref, _, tol, _ = reference(dict(s, vv=np.nan_to_num(s["vv"])))
+    assert np.all(np.abs(got - ref)[~hit] <= tol[~hit])
+
+
+def test_attn_of_many_rows_sharp_and_flat(fp):
+    for dtype in ("bf16", "e4m3"):
+        for scale in (30.0, 0.0):
+            s = attn_case(fp, [(700, 90), (600, 4)], 8, 2, 64, dtype, "bf16", seed=9, q_scale=scale)
+            check_attn(s, *run_attn(s))
+
+
+def test_attn_of_many_rows_bad_device_data(fp):
+    s = attn_case(fp, [(300, 80), (90, 1)], 4, 2, 32, "bf16", "bf16", seed=5)
+    c = s["c"]
+    for bad in (-1, c.k_cache.shape[0], 2 ** 31 - 1):
+        t = dict(s, table=s["table"].copy())
+        t["table"][0, 2] = bad
+        check_attn(t, *run_attn(t))
+        assert c.device_status() == 5
+        c.reset_status()
+    for bad in (-1, s["table"].shape[1] * 32 + 1, 2 ** 31 - 1):
+        t = dict(s, lens=[bad, 90])
+        out, lse = run_attn(t)
+        t["lens"] = [0, 90]
+        check_attn(t, out, lse)
+        assert c.device_status() == 5
+        c.reset_status()
+    for cu in ([0, 80, 90], [-3, 77, 81], [0, 81, 1], [5, 85, 81], [0, 2 ** 31 - 1, 3]):
+        c.attn(s["q"], i32(s["table"]), i32(s["lens"]), cu_seqlens_q=i32(cu), max_q=80)
+        assert c.device_status() in (0, 5)
+        c.reset_status()
+    check_attn(s, *run_attn(s))
+    assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_of_many_rows_captured(fp, dtype):
+    import torch
+    s = attn_case(fp, [(2000, 300), (90, 1), (500, 70)], 16, 4, 64, dtype, "bf16", seed=1)
+    table, lens, cu = i32(s["table"]), i32(s["lens"]), i32(s["cu"])
+    run_attn(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = s["c"].attn(s["q"], table, lens, cu_seqlens_q=cu, max_q=300)
+    for new in ([2000, 90, 500], [301, 64, 70], [1999, 0, 420]):
+        lens.copy_(i32(new))
+        g.replay()
+        check_attn(dict(s, lens=new), *out)
+    assert s["c"].device_status() == 0
