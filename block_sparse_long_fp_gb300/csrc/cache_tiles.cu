@@ -5,10 +5,11 @@
 //   S_t = Q_t K^T,   O_t += P_t V,   t = 0, 1,
 // with S, P (over S, as packed 16-bit pairs) and O in TMEM (2 x (128 + 128) of its 512
 // columns).  The halves alternate, so that one half's softmax runs beside the other's products.
-// bf16 caches take bf16 operands (e4m3 queries exactly, weights rounded to bf16); e4m3 caches
-// fp16 ones, into which codes go exactly on their way through shared memory (queries of bf16
-// under a power of two per row, weights in fp16).  Weights are 2^(logit - m + 10), m following
-// when the logits pass it by 4; sums, maxima and outputs are fp32.
+// A bf16 cache takes bf16 operands (e4m3 queries exactly, weights rounded to bf16).  Of an
+// e4m3 one keys are taken as they are, against e4m3 queries, or two e4m3 terms of bf16 ones;
+// values become fp16, exactly, on their way through shared memory, against weights in fp16.
+// Weights are 2^(logit - m + 10), m following when the logits pass it by 4; sums, maxima and
+// outputs are fp32.
 //
 // Work: the (request, kv head, tile) items laid end to end, each as long as its start and end
 // cost plus the keys that its rows attend, are cut into equal ranges, one for each SM: the
@@ -17,10 +18,11 @@
 // tile's weight linear in its number, and sums and searches closed.  An item that a range's
 // end cuts leaves partial results to the join.
 //
-// Roles (16 warps): the product issuer, the walk over the items (both in the first warpgroup),
-// loaders, and a softmax warpgroup for each half, a thread a row.  bf16 tiles come by TMA
-// through the block table, 64 dims a box, into rings of two; e4m3 tiles by TMA into two
-// staging tiles, which the loaders convert.  Every wait is bounded.
+// Roles (16 warps): the issuer of products, the walk over the items, queries (a warp a half,
+// which brings the next item's while this one ends), loaders, and a softmax warpgroup for each
+// half, a thread a row.  Tiles come by TMA through the block table: K into a ring of 2 (bf16)
+// or 4, V into a ring of 2, of e4m3 through two staging tiles that the loaders convert from.
+// Every wait is bounded.
 //
 // What a row does not attend may be anything, and a weight of zero does not keep a NaN out of
 // a product: the loaders clear values behind a request's last token, and take values that are
@@ -48,9 +50,9 @@ constexpr int kMinBlocks = 4;                    // least blocks of keys worth a
 constexpr int kTile = kBlock * kHeadDim * 2, kHalf = kTile / 2;      // bytes; a half: 64 dims
 constexpr int kSmemQ = 0, kSmemK = 2 * kTile, kSmemV = 4 * kTile, kSmemStage = 6 * kTile;
 
-enum { QF = 0, KF = 2, KE = 4, VF = 6, VE = 8, SF = 10, PF = 12, OF = 14, MF = 16, ME = 18, SG = 20, SE = 22, VX = 24, DR = 26,
-       kBars = 27 };
-constexpr int kItemReaders = 1 + 8 + 4;          // the issuer, the softmax warps, the loaders' warps
+enum { QF = 0, QE = 2, KF = 4, KE = 8, VF = 12, VE = 14, SF = 16, PF = 18, OF = 20, MF = 22, ME = 24, SG = 26, SE = 28, VX = 30,
+       DR = 32, kBars = 33 };
+constexpr int kItemReaders = 1 + 2 + 8 + 4;      // the issuer, the queries' warps, the softmax warps, the loaders' warps
 
 // A piece of an item, as the roles read it.
 struct Item {
@@ -64,13 +66,17 @@ struct Item {
     int not_finite;                              // any of:
     int pad;
     int from[kHeadDim];                          // first key of a value that was taken out, INT_MAX: none
+    signed char exponent[kRows];                 // of the power of two that a query row was multiplied by
 };
 struct Control {
     unsigned long long bars[kBars];
     uint32_t tmem, abort;
-    long long sums[kTilesWarps], at;
-    int r, pad[3];
-    Item item[2];
+    long long at;
+    int r, pad;
+    union {
+        Item item[2];
+        long long sums[kTilesWarps];             // of the scan, before the roles part
+    };
 };
 constexpr int kSmemBf16 = kSmemStage + (int)sizeof(Control) + 1024, kSmemFp8 = kSmemBf16 + kTile;
 static_assert(kSmemFp8 <= 227 * 1024, "shared memory");
@@ -149,72 +155,114 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t tile, int row, int piece) 
     return tile + (piece >> 3) * kHalf + row * 128 + (((piece ^ row) & 7) << 4);
 }
 
-// The warp's 32 rows of a half's queries into shared memory; returns what the row of this
-// lane was scaled by, undone.
-template <bool kFp8>
-__device__ __forceinline__ float load_queries(const PAttn &a, const void *mine, uint32_t tile, int row0) {
+// 16 bytes into shared memory, or zeros.
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A half's 128 rows of queries into shared memory, by a warp: `mine(row)` is the address of a
+// row, 0 for one that is not there.  A bf16 cache takes bf16 tiles.  An e4m3 one takes e4m3
+// codes as they are; bf16 rows under a power of two, as two e4m3 terms of 4 bits each, which
+// hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it.
+template <bool kFp8, typename F>
+__device__ __forceinline__ void load_queries(const PAttn &a, const F &mine, uint32_t tile, signed char *exponent) {
     const int lane = threadIdx.x & 31;
-    float undo = 1.f;
-    if (a.q_scale) {                             // 8 lanes a row of codes
+    const bool codes = a.q_scale != nullptr;
 #pragma unroll 1
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-            uint4 w[4];
+    for (int set = 0; set < 4; ++set) {
+        const unsigned long long own = mine(32 * set + lane);
+        if (codes) {                             // 8 lanes a row, 4 rows at once
+            if (kFp8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const unsigned long long p = __shfl_sync(~0u, (unsigned long long)mine, 4 * (i0 + i) + (lane >> 3));
-                w[i] = p ? *reinterpret_cast<const uint4 *>(p + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
-            }
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned long long p = __shfl_sync(~0u, own, 4 * i + (lane >> 3));
+                    const int row = 32 * set + 4 * i + (lane >> 3), c = lane & 7;
+                    copy16_or_zero(tile + row * 128 + (((c ^ row) & 7) << 4),
+                                   p ? reinterpret_cast<const unsigned char *>(p) + c * 16 : static_cast<const unsigned char *>(a.q), p != 0);
+                }
+            } else {
+                uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 4 * (i0 + i) + (lane >> 3), c = lane & 7;
-                const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t h[8];
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned long long p = __shfl_sync(~0u, own, 4 * i + (lane >> 3));
+                    w[i] = p ? *reinterpret_cast<const uint4 *>(p + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[e] = codes_to_f16(v[e >> 1] >> (16 * (e & 1)));
-                    if (!kFp8) {
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 32 * set + 4 * i + (lane >> 3), c = lane & 7;
+                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        h[e] = codes_to_f16(v[e >> 1] >> (16 * (e & 1)));
                         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
                         h[e] = pack16<false>(f.x, f.y);
                     }
+                    st_shared_v4(piece_at(tile, row, 2 * c), make_uint4(h[0], h[1], h[2], h[3]));
+                    st_shared_v4(piece_at(tile, row, 2 * c + 1), make_uint4(h[4], h[5], h[6], h[7]));
                 }
-                st_shared_v4(piece_at(tile, row, 2 * c), make_uint4(h[0], h[1], h[2], h[3]));
-                st_shared_v4(piece_at(tile, row, 2 * c + 1), make_uint4(h[4], h[5], h[6], h[7]));
             }
-        }
-    } else {                                     // 16 lanes a row
-#pragma unroll 1
-        for (int i0 = 0; i0 < 16; i0 += 8) {
-            uint4 w[8];
+        } else {                                 // 16 lanes a row, 2 rows at once
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const unsigned long long p = __shfl_sync(~0u, (unsigned long long)mine, 2 * (i0 + i) + (lane >> 4));
-                w[i] = p ? *reinterpret_cast<const uint4 *>(p + (lane & 15) * 16) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = row0 + 2 * (i0 + i) + (lane >> 4);
-                if (kFp8) {
-                    uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    float top = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
-#pragma unroll
-                    for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                    const int ex = fp16_scale_exp(__float_as_uint(top));
-                    const float up = pow2f(ex);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = pack16<true>(__uint_as_float(v[e] << 16) * up, __uint_as_float(v[e] & 0xffff0000u) * up);
-                    w[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                    const int its = __shfl_sync(~0u, ex, (lane & 1) * 16);
-                    if (lane >> 1 == i0 + i) undo = pow2f(-its);
-                }
-                st_shared_v4(piece_at(tile, row, lane & 15), w[i]);
+            for (int i = 0; i < 16; ++i) {
+                const unsigned long long p = __shfl_sync(~0u, own, 2 * i + (lane >> 4));
+                const int row = 32 * set + 2 * i + (lane >> 4), c = lane & 15;
+                copy16_or_zero(piece_at(tile, row, c),
+                               p ? reinterpret_cast<const unsigned char *>(p) + c * 16 : static_cast<const unsigned char *>(a.q), p != 0);
             }
         }
     }
-    return undo;
+    copies_commit();
+    copies_wait<0>();
+    __syncwarp();
+    if (kFp8 && !codes) {
+        // in place: a row's 64 and 64 dims of bf16 make room for its two terms of 128 bytes
+#pragma unroll 1
+        for (int i0 = 0; i0 < 64; i0 += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = ld_shared_v4(piece_at(tile, 2 * (i0 + i) + (lane >> 4), lane & 15));
+            uint2 hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                float x[8], top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(v[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+                    top = max3f(top, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
+                }
+#pragma unroll
+                for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
+                if ((lane & 15) == 0) exponent[2 * (i0 + i) + (lane >> 4)] = (signed char)ex;
+                const float up = pow2f(ex);
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[2 * e] * up, y = x[2 * e + 1] * up;
+                    h[e] = e4m3_pair(u, y);
+                    const uint32_t back = codes_to_f16(h[e]);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                    l[e] = e4m3_pair(u - f.x, y - f.y);
+                }
+                hi[i] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                lo[i] = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * (i0 + i) + (lane >> 4), c = lane & 15;
+                const uint32_t at = tile + row * 128 + ((((c >> 1) ^ row) & 7) << 4) + (c & 1) * 8;
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[i].x), "r"(hi[i].y) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kHalf), "r"(lo[i].x), "r"(lo[i].y) : "memory");
+            }
+        }
+    }
 }
 
 template <bool kFp8>
@@ -227,6 +275,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     Control &ctl = *reinterpret_cast<Control *>(smem + (kFp8 ? kSmemStage + kTile : kSmemStage));
     const uint32_t base = smem_u32(smem), bars = smem_u32(ctl.bars);
     const auto bar = [&](int k) { return bars + 8u * (uint32_t)k; };
+    constexpr int kRing = kFp8 ? 4 : 2, kSlot = kTile / (kFp8 ? 2 : 1);        // tiles of K, as they come
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     after_previous();
 
@@ -257,9 +306,9 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     if (tid == 0) {
         for (int k = 0; k < kBars; ++k) {
             uint32_t count = 1;
-            if (k == QF || k == QF + 1 || k == PF || k == PF + 1 || k == SE || k == SE + 1 || k == VX || k == VX + 1) count = 128;
-            if (kFp8 && (k == KF || k == KF + 1 || k == VF || k == VF + 1)) count = 128;
-            if (k == MF || k == MF + 1) count = 32;
+            if (k == PF || k == PF + 1 || k == SE || k == SE + 1 || k == VX || k == VX + 1) count = 128;
+            if (kFp8 && (k == VF || k == VF + 1)) count = 128;
+            if (k == MF || k == MF + 1 || k == QF || k == QF + 1) count = 32;
             if (k == ME || k == ME + 1) count = kItemReaders;
             mbar_init(bar(k), count);
         }
@@ -368,15 +417,25 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             }
         } else if (warp == 0 && lane == 0) {
             // ================= the products' issuer =================
-            constexpr uint32_t kIdS = kFp8 ? idesc_f16(128, 128, false) : idesc_bf16(128, 128, false);
+            constexpr uint32_t kIdS = kFp8 ? idesc_e4m3(128, 128, false) : idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = kFp8 ? idesc_f16(128, 128, true) : idesc_bf16(128, 128, true);
             const uint64_t dq = smem_desc_sw128(base + kSmemQ, 16, 1024), dk = smem_desc_sw128(base + kSmemK, 16, 1024);
             const uint64_t dv = smem_desc_sw128(base + kSmemV, kHalf, 1024);
+            // e4m3: one term of the queries, or two
             const auto issue_s = [&](int t, int s) {
+                const uint64_t qt = dq + ((t * kTile) >> 4), ks = dk + ((s * kSlot) >> 4);
+                if (kFp8) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + t * 256, dq + ((t * kTile) >> 4) + off, dk + ((s * kTile) >> 4) + off, kIdS, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + kk * 2, ks + kk * 2, kIdS, kk > 0);
+                    if (!a.q_scale)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + (kHalf >> 4) + kk * 2, ks + kk * 2, kIdS, true);
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + t * 256, qt + off, ks + off, kIdS, kk > 0);
+                    }
                 }
                 tc_commit(bar(SF + t));
             };
@@ -394,24 +453,30 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 const bool two = item.rows - item.tile * kRows > kBlock;
                 mbar_arrive(bar(ME + b));
                 if (!live) break;
-                if (!wait(bar(QF), items[0]++) || (two && !wait(bar(QF + 1), items[1]++)) || !wait(bar(KF + (it & 1)), it >> 1)) break;
+                const auto keys_there = [&](uint32_t i) { return wait(bar(KF + i % kRing), i / kRing); };
+                if (!wait(bar(QF), items[0]++) || (two && !wait(bar(QF + 1), items[1]++)) || !keys_there(it)) break;
                 tc_fence_after();
-                issue_s(0, it & 1);
-                if (two) issue_s(1, it & 1);
-                tc_commit(bar(KE + (it & 1)));
+                issue_s(0, it % kRing);
+                if (count == 1) tc_commit(bar(QE));
+                if (two) {
+                    issue_s(1, it % kRing);
+                    if (count == 1) tc_commit(bar(QE + 1));
+                }
+                tc_commit(bar(KE + it % kRing));
                 bool good = true;
                 for (int j = 0; j < count; ++j, ++it) {
-                    const int s = it & 1, s1 = (it + 1) & 1;
-                    const bool more = j + 1 < count;
+                    const uint32_t s = it & 1, s1 = (it + 1) % kRing;
+                    const bool more = j + 1 < count, last = j + 2 == count;
                     good = j < edge ? wait(bar(VF + s), it >> 1) : wait(bar(VX + (edges & 1)), edges >> 1);
                     if (j >= edge) ++edges;
                     if (!good || !(good = wait(bar(PF), phase[0]++))) break;
                     tc_fence_after();
                     issue_o(0, s, j > 0);
                     if (more) {
-                        if (!(good = wait(bar(KF + s1), (it + 1) >> 1))) break;
+                        if (!(good = keys_there(it + 1))) break;
                         tc_fence_after();
                         issue_s(0, s1);
+                        if (last) tc_commit(bar(QE));
                     } else {
                         tc_commit(bar(OF));
                     }
@@ -422,7 +487,10 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     }
                     tc_commit(bar(VE + s));
                     if (more) {
-                        if (two) issue_s(1, s1);
+                        if (two) {
+                            issue_s(1, s1);
+                            if (last) tc_commit(bar(QE + 1));
+                        }
                         tc_commit(bar(KE + s1));
                     } else if (two) {
                         tc_commit(bar(OF + 1));
@@ -434,6 +502,33 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 tc_commit(bar(DR));
                 mbar_wait_drain(bar(DR), 0);
             }
+        } else if (warp >= 2) {
+            // ================= queries, a warp a half =================
+            const int t = warp - 2;
+            uint32_t items = 0;
+            for (int k = 0;; ++k) {
+                const int b = k & 1;
+                if (!__all_sync(~0u, wait(bar(MF + b), k >> 1))) break;
+                Item &item = ctl.item[b];
+                if (!item.live) break;
+                const int row0 = item.tile * kRows + t * kBlock;
+                if (item.rows > row0) {
+                    // the products of the item before are done with their queries
+                    if (items && !__all_sync(~0u, wait(bar(QE + t), items - 1))) break;
+                    const auto mine = [&](int row) -> unsigned long long {
+                        const int packed = row0 + row, i = packed / a.g, head = item.kv * a.g + packed % a.g;
+                        if (packed >= item.rows) return 0;
+                        const long long at = (item.row0 + i) * a.q_stride_tok + head * a.q_stride_head;
+                        return (unsigned long long)(static_cast<const unsigned char *>(a.q) + (a.q_scale ? at : 2 * at));
+                    };
+                    load_queries<kFp8>(a, mine, base + kSmemQ + t * kTile, item.exponent + t * kBlock);
+                    fence_proxy_async();
+                    mbar_arrive(bar(QF + t));
+                    ++items;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ME + b));
+            }
         }
     } else if (warp < 8) {
         setmaxnreg_dec<kRegsLoad>();
@@ -441,8 +536,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         const int lw = warp - 4, lt = tid - 128;
         const int box = a.c.page_size < kBlock ? a.c.page_size : kBlock, boxes = kBlock / box;     // rows of one; boxes of a block
         const int outside = a.c.num_pages * a.c.page_size;               // reads zeros
-        uint32_t nk = 0, nv = 0, nx = 0, edges = 0;      // tiles of K, of V, staged ones; edge blocks
-        uint32_t armed_k = 0, armed_v = 0;
+        uint32_t nk = 0, nv = 0, nx = 0, edges = 0;      // tiles of K and V, staged ones of V, edge blocks
         for (int k = 0; !dead; ++k) {
             const int b = k & 1;
             const bool got = wait(bar(MF + b), k >> 1);
@@ -454,7 +548,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             // the row of the caches where this lane's box of a block starts
             const auto look = [&](int j) {
                 const int tok = (c0 + j) * kBlock + (lane % boxes) * box;
-                if (lw != 0 || j >= count || tok >= len) return outside;
+                if (lw > 1 || j >= count || tok >= len) return outside;
                 const int page = table[tok / a.c.page_size];
                 if (page < 0 || page >= a.c.num_pages) {
                     set_status(a.status, FP_ERR_DEVICE_BOUNDS);
@@ -462,104 +556,97 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 }
                 return page * a.c.page_size + tok % a.c.page_size;
             };
-            const auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int z) {       // warp 0
-                if (lane == 0) mbar_expect_tx(full, kFp8 ? kHalf : kTile);
+            const auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int z) {       // a warp
+                if (lane == 0) mbar_expect_tx(full, kSlot);
                 __syncwarp();
                 if (lane < (kFp8 ? 1 : 2) * boxes)
                     tma_load_3d(dst + (lane / boxes) * kHalf + (lane % boxes) * box * 128, map, full, (lane / boxes) * 64, kv, z);
                 __syncwarp();
             };
             bool good = true;
-            if (!kFp8) {
-                const auto keys = [&](int z) {
-                    if (lw == 0) {
-                        good = nk < 2 || __all_sync(~0u, wait(bar(KE + (nk & 1)), (nk >> 1) ^ 1));
-                        if (good) {
-                            copy(&map_k, base + kSmemK + (nk & 1) * kTile, bar(KF + (nk & 1)), z);
-                            armed_k = nk + 1;
-                        }
-                    }
+            // K by warp 1, as far ahead as its ring goes
+            const auto keys = [&](int z) {
+                good = nk < kRing || __all_sync(~0u, wait(bar(KE + nk % kRing), (nk / kRing) ^ 1));
+                if (good) {
+                    copy(&map_k, base + kSmemK + (nk % kRing) * kSlot, bar(KF + nk % kRing), z);
                     ++nk;
-                };
-                int z0 = look(0), z1 = look(1);
-                keys(z0);
-                for (int j = 0; j < count && good; ++j) {
-                    const int z2 = look(j + 2);
-                    if (j + 1 < count) keys(z1);
-                    const uint32_t s = nv & 1, tile = base + kSmemV + s * kTile;
-                    // every loader follows the ring phase by phase: a parity alone does not tell a tile from
-                    // the one before it
-                    good = good && (nv < 2 || __all_sync(~0u, wait(bar(VE + s), (nv >> 1) ^ 1)));
-                    if (lw == 0 && good) {
-                        copy(&map_v, tile, bar(VF + s), z0);
-                        armed_v = nv + 1;
-                    }
-                    if (!good) break;
-                    if (c0 + j >= edge) {                // a thread a row
-                        if (!(good = __all_sync(~0u, wait(bar(VF + s), nv >> 1)))) break;
-                        const int key = (c0 + j) * kBlock + lt;         // can pass 2^31 behind the last token
-                        if ((uint32_t)key >= (uint32_t)len) {
+                }
+            };
+            const auto stage = [&](int z) {              // e4m3 V, by warp 0
+                good = nx < 2 || __all_sync(~0u, wait(bar(SE + (nx & 1)), (nx >> 1) ^ 1));
+                if (good) {
+                    copy(&map_v, base + kSmemStage + (nx & 1) * kHalf, bar(SG + (nx & 1)), z);
+                    ++nx;
+                }
+            };
+            constexpr int kAhead = kRing - 1;
+            int z1 = 0;                                  // of the next tile that this warp copies
+            if (lw == 1) {
+                int z[kAhead];
 #pragma unroll
-                            for (int p = 0; p < 16; ++p) st_shared_v4(piece_at(tile, lt, p), make_uint4(0, 0, 0, 0));
-                        } else if (key >= min_keys) {
+                for (int i = 0; i < kAhead; ++i) z[i] = look(i);
+                z1 = look(kAhead);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (i < count && good) keys(z[i]);
+            } else if (lw == 0) {
+                const int z0 = look(0);
+                z1 = look(1);
+                if (kFp8) {
+                    stage(z0);
+                    if (count > 1 && good) stage(z1);
+                    z1 = look(2);
+                } else {
+                    z1 = z0;
+                }
+            }
+            for (int j = 0; j < count && good; ++j, ++nv) {
+                const uint32_t s = nv & 1, tile = base + kSmemV + s * kTile;
+                const int z = z1;
+                if (lw < 2) z1 = look(j + 1 + (lw == 1 ? kAhead : kFp8 ? 2 : 0));
+                if (lw == 1 && j + kAhead < count) keys(z);
+                // every loader follows the ring phase by phase: a parity alone does not tell a tile from
+                // the one before it
+                if (!good || !(good = nv < 2 || __all_sync(~0u, wait(bar(VE + s), (nv >> 1) ^ 1)))) break;
+                if (!kFp8) {
+                    if (lw == 0) copy(&map_v, tile, bar(VF + s), z);
+                    if (c0 + j < edge) continue;
+                    // a thread a row
+                    if (!(good = __all_sync(~0u, wait(bar(VF + s), nv >> 1)))) break;
+                    const int key = (c0 + j) * kBlock + lt;         // can pass 2^31 behind the last token
+                    if ((uint32_t)key >= (uint32_t)len) {
+#pragma unroll
+                        for (int p = 0; p < 16; ++p) st_shared_v4(piece_at(tile, lt, p), make_uint4(0, 0, 0, 0));
+                    } else if (key >= min_keys) {
 #pragma unroll 4
-                            for (int p = 0; p < 16; ++p) {
-                                uint4 w = ld_shared_v4(piece_at(tile, lt, p));
-                                const auto bad = [](uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; };
-                                if (bad(w.x) | bad(w.y) | bad(w.z) | bad(w.w)) {
-                                    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+                        for (int p = 0; p < 16; ++p) {
+                            uint4 w = ld_shared_v4(piece_at(tile, lt, p));
+                            const auto bad = [](uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; };
+                            if (bad(w.x) | bad(w.y) | bad(w.z) | bad(w.w)) {
+                                uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const uint32_t x = bad(v[e]);
-                                        if (x & 0x8000u) atomicMin(&item.from[8 * p + 2 * e], key);
-                                        if (x >> 31) atomicMin(&item.from[8 * p + 2 * e + 1], key);
-                                        v[e] &= ~((x >> 15) * 0xffffu);
-                                    }
-                                    st_shared_v4(piece_at(tile, lt, p), make_uint4(v[0], v[1], v[2], v[3]));
-                                    item.not_finite = 1;
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t x = bad(v[e]);
+                                    if (x & 0x8000u) atomicMin(&item.from[8 * p + 2 * e], key);
+                                    if (x >> 31) atomicMin(&item.from[8 * p + 2 * e + 1], key);
+                                    v[e] &= ~((x >> 15) * 0xffffu);
                                 }
+                                st_shared_v4(piece_at(tile, lt, p), make_uint4(v[0], v[1], v[2], v[3]));
+                                item.not_finite = 1;
                             }
                         }
-                        fence_proxy_async();
-                        mbar_arrive(bar(VX + (edges & 1)));
-                        ++edges;
                     }
-                    ++nv;
-                    z0 = z1;
-                    z1 = z2;
-                }
-            } else {
-                // staged tiles in the order K0, K1, V0, K2, V1, ... : of tile x its block, and whether it is V
-                const auto block_at = [&](int x) { return x == 0 ? 0 : x & 1 ? min((x + 1) / 2, count - 1) : x / 2 - 1; };
-                const auto is_v = [&](int x) { return x > 0 && (!(x & 1) || (x + 1) / 2 >= count); };
-                const auto stage = [&](int x, int z) {       // warp 0
-                    const uint32_t i = nx + x;
-                    good = i < 2 || __all_sync(~0u, wait(bar(SE + (i & 1)), (i >> 1) ^ 1));
-                    if (good) {
-                        copy(is_v(x) ? &map_v : &map_k, base + kSmemStage + (i & 1) * kHalf, bar(SG + (i & 1)), z);
-                        armed_k = i + 1;
-                    }
-                };
-                if (lw == 0) {
-                    const int z0 = look(0), z1 = look(block_at(1));
-                    stage(0, z0);
-                    if (good) stage(1, z1);
-                }
-                for (int x = 0; x < 2 * count && good; ++x) {
-                    const int z = x + 2 < 2 * count ? look(block_at(x + 2)) : outside;
-                    const uint32_t i = nx + x;
-                    const bool v = is_v(x);
-                    const uint32_t tiles = v ? nv : nk, s = tiles & 1;
-                    if (!(good = __all_sync(~0u, wait(bar(SG + (i & 1)), i >> 1)))) break;
-                    if (tiles >= 2 && !(good = __all_sync(~0u, wait(bar((v ? VE : KE) + s), (tiles >> 1) ^ 1)))) break;
-                    const uint32_t from = base + kSmemStage + (i & 1) * kHalf + lt * 16;
-                    const uint32_t tile = base + (v ? kSmemV : kSmemK) + s * kTile;
+                    fence_proxy_async();
+                    mbar_arrive(bar(VX + (edges & 1)));
+                    ++edges;
+                } else {
+                    if (!(good = __all_sync(~0u, wait(bar(SG + s), nv >> 1)))) break;      // the staging ring goes as V's does
+                    const uint32_t from = base + kSmemStage + s * kHalf + lt * 16;
                     uint4 w[8];
 #pragma unroll
                     for (int p = 0; p < 8; ++p) w[p] = ld_shared_v4(from + p * 2048);
-                    mbar_arrive(bar(SE + (i & 1)));
-                    const int key0 = (c0 + block_at(x)) * kBlock + lt / 8, c = lt & 7;
-                    const bool edged = v && c0 + block_at(x) >= edge;
+                    const int key0 = (c0 + j) * kBlock + lt / 8, c = lt & 7;
+                    const bool edged = c0 + j >= edge;
 #pragma unroll
                     for (int p = 0; p < 8; ++p) {            // row 16 p + lt / 8, dims 16 c ..
                         const uint32_t u[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
@@ -591,22 +678,26 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                         st_shared_v4(piece_at(tile, row, 2 * c + 1 - o), o ? lo : hi);
                     }
                     fence_proxy_async();
-                    mbar_arrive(bar((v ? VF : KF) + s));
-                    nv += v;
-                    nk += !v;
-                    if (lw == 0 && x + 2 < 2 * count) stage(x + 2, z);
+                    mbar_arrive(bar(VF + s));
+                    // not before the codes were used: an arrival waits for no load that is on its way, and the
+                    // next tile may land first
+                    mbar_arrive(bar(SE + s));
+                    if (lw == 0 && j + 2 < count) stage(z);
                 }
-                nx += 2 * count;
             }
             if (!__all_sync(~0u, good)) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ME + b));
         }
         // after an abort, the copies armed last land before the block leaves
-        if (lw == 0 && lane == 0 && ld_shared_volatile(wait.abort)) {
-            for (uint32_t i = armed_k < 2 ? 0 : armed_k - 2; i < armed_k; ++i)
-                mbar_wait_drain(bar((kFp8 ? SG : KF) + (i & 1)), (i >> 1) & 1);
-            for (uint32_t i = armed_v < 2 ? 0 : armed_v - 2; i < armed_v; ++i) mbar_wait_drain(bar(VF + (i & 1)), (i >> 1) & 1);
+        if (lw < 2 && lane == 0 && ld_shared_volatile(wait.abort)) {
+            if (lw == 1) {
+                for (uint32_t i = nk < kRing ? 0 : nk - kRing; i < nk; ++i) mbar_wait_drain(bar(KF + i % kRing), (i / kRing) & 1);
+            } else {
+                // of bf16, the one that the last wait was for may not have been armed: waiting for it runs out
+                const uint32_t n = kFp8 ? nx : nv + 1;
+                for (uint32_t i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_wait_drain(bar((kFp8 ? SG : VF) + (i & 1)), (i >> 1) & 1);
+            }
         }
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
@@ -631,15 +722,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             const int keys = valid ? max(0, min(item.len, item.len - item.lq + i + 1)) : 0;
             float cs = a.scale * kLog2e;                             // base-2 logits
             if (kFp8) cs *= __ldg(a.k_scale + item.kv);
-            const void *mine = nullptr;
-            if (valid) {
-                const long long at = (item.row0 + i) * a.q_stride_tok + head * a.q_stride_head;
-                if (a.q_scale) cs *= __ldg(a.q_scale + head);
-                mine = static_cast<const unsigned char *>(a.q) + (a.q_scale ? at : 2 * at);
-            }
-            cs *= load_queries<kFp8>(a, mine, base + kSmemQ + t * kTile, quarter * 32);
-            fence_proxy_async();
-            mbar_arrive(bar(QF + t));
+            if (a.q_scale && valid) cs *= __ldg(a.q_scale + head);
             const int count = item.c1 - item.c0, key0 = item.c0 * kBlock;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
@@ -650,6 +733,8 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     break;
                 }
                 tc_fence_after();
+                if (kFp8 && !a.q_scale && j == 0)
+                    cs *= pow2f(-*reinterpret_cast<const volatile signed char *>(&item.exponent[t * kBlock + row]));
                 float x[128];
                 {
                     uint32_t v[4][32];
@@ -786,9 +871,9 @@ EncodeFn encode() {
     }();
     return fn;
 }
-// A cache as [tokens][h_kv][128]: boxes of `rows` tokens of one head, 64 dims of bf16 (swizzled,
-// as the products take them) or 128 of e4m3 (plain); a token past the last one reads zeros.
-bool map_pages(CUtensorMap *m, const void *base, const Pages &c, bool fp8) {
+// A cache as [tokens][h_kv][128]: boxes of tokens of one head, 64 dims of bf16 or 128 of e4m3,
+// swizzled as the products take them or plain; a token past the last one reads zeros.
+bool map_pages(CUtensorMap *m, const void *base, const Pages &c, bool fp8, bool swizzled) {
     const EncodeFn fn = encode();
     if (!fn) return false;
     const cuuint64_t esz = fp8 ? 1 : 2;
@@ -797,7 +882,7 @@ bool map_pages(CUtensorMap *m, const void *base, const Pages &c, bool fp8) {
     const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), 1, (cuuint32_t)(c.page_size < kBlock ? c.page_size : kBlock)};
     const cuuint32_t one[3] = {1, 1, 1};
     return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -827,13 +912,13 @@ cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long
     sc.o = reinterpret_cast<float *>(p);
     const bool fp8 = a.k_scale != nullptr;
     CUtensorMap map_k, map_v;
-    if (!map_pages(&map_k, a.c.k, a.c, fp8) || !map_pages(&map_v, a.c.v, a.c, fp8)) return cudaErrorInvalidValue;
+    if (!map_pages(&map_k, a.c.k, a.c, fp8, true) || !map_pages(&map_v, a.c.v, a.c, fp8, !fp8)) return cudaErrorInvalidValue;
     const auto kernel = fp8 ? tiles_kernel<true> : tiles_kernel<false>;
     const int smem = fp8 ? kSmemFp8 : kSmemBf16;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if ((e = launch_chained(kernel, (unsigned)n, kTilesThreads, smem, st, a, sc, map_k, map_v, limit_ns)) != cudaSuccess) return e;
-    return launch_chained(join_kernel<kRows / 8, kSm, PAttn>, n < 2 * kSm ? (unsigned)n * 2 : 2 * kSm, kJoinWarps * 32, 0, st, a, sc,
+    return launch_chained(join_kernel<kRows / 8, kSm, PAttn>, (unsigned)n * 8, kJoinWarps * 32, 0, st, a, sc,
                           (int)n);
 }
 

@@ -400,7 +400,8 @@ def reference(s, scale=None):
 
     A logit: 128 exact products summed in fp32, cut at 2^-23 of the partial sums a step: 2^-16 of the sum of
     their magnitudes at most; scaling and subtracting the maximum round at 2^-24 of the logit, the exponential
-    is within 2^-22: d.  A weight is off by d, and by its rounding to bf16 (2^-8) or fp16 (2^-11): an output by
+    is within 2^-22: d.  (bf16 queries of an e4m3 cache enter as two e4m3 terms, the largest in 2^7 .. 2^8: each
+    element is exact, or off by half of e4m3's least step, 2^-10, so by 2^-17 of the row's largest.)  A weight is off by d, and by its rounding to bf16 (2^-8) or fp16 (2^-11): an output by
     that much of the weighted magnitudes of the values, then by fp32 sums of up to n terms cut at 2^-23 (a step
     sums 16, in 4 warps and several blocks), and by its own rounding (2^-8).  The LSE: d, a sum of n positive
     weights over 64 lanes and warps, and the rounding of itself."""
@@ -413,6 +414,8 @@ def reference(s, scale=None):
     g = s["qv"].shape[1] // kmax.shape[0]
     size = scale * (np.abs(s["qv"]) * np.repeat(kmax, g, 0)).sum(-1)                      # [rows, h_q]
     d = 2.0 ** -16 * size + 2.0 ** -20
+    if s["c"].k_scale is not None and s["q_scale"] is None:
+        d = d + 2.0 ** -17 * scale * np.abs(s["qv"]).max(-1) * np.repeat(kmax.sum(-1), g)
     w = 2.0 ** -11 if s["c"].k_scale is not None else 2.0 ** -8
     tol = 2.0 ** -8 * np.abs(out) + reach * (w + 2 * d[..., None] + 2.0 ** -23 * (n / 16 + 64)) + 1e-30
     lse_tol = d.T + 2.0 ** -24 * (n / 64 + 64) + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
