@@ -444,7 +444,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, dv + ((s * kTile + kk * 16 * 128) >> 4), kIdO, more || kk > 0);
             };
-            uint32_t it = 0, edges = 0, phase[2] = {0, 0}, items[2] = {0, 0};
+            uint32_t it = 0, edges = 0, phase0 = 0, phase1 = 0, items0 = 0, items1 = 0;
             for (int k = 0;; ++k) {
                 const int b = k & 1;
                 if (!wait(bar(MF + b), k >> 1)) break;
@@ -454,7 +454,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 mbar_arrive(bar(ME + b));
                 if (!live) break;
                 const auto keys_there = [&](uint32_t i) { return wait(bar(KF + i % kRing), i / kRing); };
-                if (!wait(bar(QF), items[0]++) || (two && !wait(bar(QF + 1), items[1]++)) || !keys_there(it)) break;
+                if (!wait(bar(QF), items0++) || (two && !wait(bar(QF + 1), items1++)) || !keys_there(it)) break;
                 tc_fence_after();
                 issue_s(0, it % kRing);
                 if (count == 1) tc_commit(bar(QE));
@@ -463,13 +463,14 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     if (count == 1) tc_commit(bar(QE + 1));
                 }
                 tc_commit(bar(KE + it % kRing));
+                // written out for both halves: as a loop over them it cost 8 %
                 bool good = true;
                 for (int j = 0; j < count; ++j, ++it) {
                     const uint32_t s = it & 1, s1 = (it + 1) % kRing;
                     const bool more = j + 1 < count, last = j + 2 == count;
                     good = j < edge ? wait(bar(VF + s), it >> 1) : wait(bar(VX + (edges & 1)), edges >> 1);
                     if (j >= edge) ++edges;
-                    if (!good || !(good = wait(bar(PF), phase[0]++))) break;
+                    if (!good || !(good = wait(bar(PF), phase0++))) break;
                     tc_fence_after();
                     issue_o(0, s, j > 0);
                     if (more) {
@@ -481,7 +482,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                         tc_commit(bar(OF));
                     }
                     if (two) {
-                        if (!(good = wait(bar(PF + 1), phase[1]++))) break;
+                        if (!(good = wait(bar(PF + 1), phase1++))) break;
                         tc_fence_after();
                         issue_o(1, s, j > 0);
                     }
@@ -641,41 +642,59 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     ++edges;
                 } else {
                     if (!(good = __all_sync(~0u, wait(bar(SG + s), nv >> 1)))) break;      // the staging ring goes as V's does
+                    // rows 16 p + lt / 8, dims 16 c ..  The loops stay short: what the softmax and this
+                    // run at once has to fit the instruction caches
                     const uint32_t from = base + kSmemStage + s * kHalf + lt * 16;
-                    uint4 w[8];
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) w[p] = ld_shared_v4(from + p * 2048);
-                    const int key0 = (c0 + j) * kBlock + lt / 8, c = lt & 7;
-                    const bool edged = c0 + j >= edge;
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {            // row 16 p + lt / 8, dims 16 c ..
-                        const uint32_t u[4] = {w[p].x, w[p].y, w[p].z, w[p].w};
-                        uint32_t h[8];
+                    const int row0 = lt >> 3, c = lt & 7, o = c >> 2;
+                    const auto convert = [&](uint4 w, uint32_t (&h)[8]) {
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int e = 0; e < 8; ++e) h[e] = codes_to_f16(u[e >> 1] >> (16 * (e & 1)));
-                        if (edged) {
-                            const int key = key0 + 16 * p;
-                            if ((uint32_t)key >= (uint32_t)len) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) h[e] = 0;
-                            } else if (key >= min_keys) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const uint32_t y = ((h[e] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;
-                                    if (y) {
-                                        if (y & 0x8000u) atomicMin(&item.from[16 * c + 2 * e], key);
-                                        if (y >> 31) atomicMin(&item.from[16 * c + 2 * e + 1], key);
-                                        h[e] &= ~((y >> 15) * 0xffffu);
-                                        item.not_finite = 1;
-                                    }
-                                }
-                            }
-                        }
-                        // lanes 4 .. 7 of a row write their two pieces the other way round: all banks, once
-                        const int row = 16 * p + lt / 8, o = c >> 2;
+                    };
+                    // lanes 4 .. 7 of a row write their two pieces the other way round: all banks, once
+                    const auto put = [&](int row, const uint32_t (&h)[8]) {
                         const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
                         st_shared_v4(piece_at(tile, row, 2 * c + o), o ? hi : lo);
                         st_shared_v4(piece_at(tile, row, 2 * c + 1 - o), o ? lo : hi);
+                    };
+                    if (c0 + j < edge) {
+#pragma unroll 1
+                        for (int p = 0; p < 8; p += 4) {
+                            uint4 w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = ld_shared_v4(from + (p + i) * 2048);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t h[8];
+                                convert(w[i], h);
+                                put(row0 + 16 * (p + i), h);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int p = 0; p < 8; ++p) {
+                            uint32_t h[8];
+                            convert(ld_shared_v4(from + p * 2048), h);
+                            const int key = (c0 + j) * kBlock + row0 + 16 * p;
+                            const bool behind = (uint32_t)key >= (uint32_t)len;
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                if (behind) h[e] = 0;
+                                any |= ((h[e] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;
+                            }
+                            if (any && key >= min_keys) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint32_t y = ((h[e] & 0x7fff7fffu) + 0x04000400u) & 0x80008000u;
+                                    if (y & 0x8000u) atomicMin(&item.from[16 * c + 2 * e], key);
+                                    if (y >> 31) atomicMin(&item.from[16 * c + 2 * e + 1], key);
+                                    h[e] &= ~((y >> 15) * 0xffffu);
+                                }
+                                item.not_finite = 1;
+                            }
+                            put(row0 + 16 * p, h);
+                        }
                     }
                     fence_proxy_async();
                     mbar_arrive(bar(VF + s));
