@@ -54,6 +54,9 @@ struct PAttn {
     float *lse;
     int *status;
     bool whole;                                // no item is cut (set by the launch)
+    bool q_codes;                              // e4m3 queries
+    int half;                                  // queries of half a tile (set by the launch)
+    const signed char *q_exponent;             // of the power of two of converted bf16 queries (set by the launch)
     int most_columns;                          // rows times g up to which a request is the columns' (set by the launch)
 };
 // cache_attn.cu: by columns, and which of the two takes what

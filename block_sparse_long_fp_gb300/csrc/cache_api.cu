@@ -22,7 +22,7 @@ bool dtype_ok(fp_dtype t) { return t == FP_BF16 || t == FP_E4M3; }
 // row has a scale a head.
 bool rows_ok(const void *p, long long tok, long long head, int heads, fp_dtype t, const float *scale) {
     const int esz = t == FP_E4M3 ? 1 : 2;
-    const long long most = 1ll << 40;          // products with a row number stay in 64 bits
+    const long long most = 1ll << 38;          // what the copies' descriptors take
     return p && aligned(p, 16) && head >= kHeadDim && head <= most && tok <= most &&
            tok >= head * (heads - 1) + kHeadDim && (tok * esz) % 16 == 0 && (head * esz) % 16 == 0 &&
            (t == FP_BF16 || (scale && aligned(scale, 4)));
@@ -87,6 +87,7 @@ fp_status check_query(const fp_cache *c, const fp_qcache_query *q, PAttn *a) {
     a->q_stride_tok = q->q_stride_tok;
     a->q_stride_head = q->q_stride_head;
     a->q_scale = q->dtype == FP_E4M3 ? q->q_scale : nullptr;
+    a->q_codes = q->dtype == FP_E4M3;
     a->cu = q->cu_seqlens_q;
     a->seqlens_k = q->seqlens_k;
     a->block_table = q->block_table;

@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
 
 // Requests of more columns go to the tiles of 256 rows.
 constexpr int kMostColumns = 64;
-bool with_tiles(const PAttn &a) { return a.g <= 256 && (long long)a.max_q * a.g > kMostColumns; }
+bool with_tiles(const PAttn &a) { return a.g <= kBlock && (long long)a.max_q * a.g > kMostColumns; }
 bool with_columns(const PAttn &a) { return a.cu || !with_tiles(a); }
 
 // Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32;
@@ -664,7 +664,7 @@ cudaError_t launch(const PAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     if (e != cudaSuccess) return e;
     if ((e = launch_chained(columns_kernel<kFp8, NT>, blocks, kThreads, smem, st, a, sc)) != cudaSuccess) return e;
     if (a.whole) return cudaSuccess;
-    return launch_chained(join_kernel<NT, most_blocks<kFp8>(), PAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0,
+    return launch_chained(join_kernel<InOrder<8 * NT>, 8 * NT, most_blocks<kFp8>(), PAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0,
                           st, a, sc, blocks);
 }
 

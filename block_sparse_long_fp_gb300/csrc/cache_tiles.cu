@@ -1,7 +1,8 @@
 // fp_cache_attn for requests of many rows: tiles of 256 (query, head) rows on tcgen05.
 //
 // A kv head's rows of a request -- query by query, the g heads of a query together -- are cut
-// into tiles of 2 x 128; every 128 keys and values are loaded once for both halves:
+// into tiles of two halves of at most 128, whole queries each; every 128 keys and values are
+// loaded once for both halves:
 //   S_t = Q_t K^T,   O_t += P_t V,   t = 0, 1,
 // with S, P (over S, as packed 16-bit pairs) and O in TMEM (2 x (128 + 128) of its 512
 // columns).  The halves alternate, so that one half's softmax runs beside the other's products.
@@ -12,17 +13,17 @@
 // outputs are fp32.
 //
 // Work: the (request, kv head, tile) items laid end to end, each as long as its start and end
-// cost plus the keys that its rows attend, are cut into equal ranges, one for each SM: the
-// lengths are the GPU's, the triangle below a prompt's diagonal is weighed in, and few rows
-// over a long cache spread over all SMs.  Lengths are counted in keys times g, which makes a
-// tile's weight linear in its number, and sums and searches closed.  An item that a range's
-// end cuts leaves partial results to the join.
+// cost plus the keys that its last row may attend, are cut into equal ranges, one for each SM:
+// the lengths are the GPU's, the triangle below a prompt's diagonal is weighed in, and few rows
+// over a long cache spread over all SMs.  A tile's weight is linear in its number, which makes
+// sums and searches closed.  An item that a range's end cuts leaves partial results to the join.
 //
-// Roles (16 warps): the issuer of products, the walk over the items, queries (a warp a half,
-// which brings the next item's while this one ends), loaders, and a softmax warpgroup for each
-// half, a thread a row.  Tiles come by TMA through the block table: K into a ring of 2 (bf16)
-// or 4, V into a ring of 2, of e4m3 through two staging tiles that the loaders convert from.
-// Every wait is bounded.
+// Roles (16 warps): the issuer of products, the walk over the items, the copies of queries and
+// those of keys and values (TMA, through the block table), loaders that convert or clean, and a
+// softmax warpgroup for each half, a thread a row.  bf16 tiles of K and V share a ring of 5;
+// e4m3 keys have one of 4, values one of 2 that the loaders fill from two staged tiles.  Every
+// wait is bounded.  The roles' code is kept short: together it has to fit the instruction
+// caches (with the conversion written out eight times a step took 5100 clocks and not 3700).
 //
 // What a row does not attend may be anything, and a weight of zero does not keep a NaN out of
 // a product: the loaders clear values behind a request's last token, and take values that are
@@ -44,29 +45,37 @@ constexpr int kTilesThreads = 512, kTilesWarps = kTilesThreads / 32;
 // Registers: 128 a thread at launch, dealt anew among the warpgroups.
 constexpr int kRegsControl = 80, kRegsLoad = 80, kRegsSoftmax = 176;
 static_assert(kRegsControl + kRegsLoad + 2 * kRegsSoftmax <= 4 * 128, "register split");
-constexpr int kRows = 256;                       // packed rows of a tile
+constexpr int kRows = 2 * kBlock;                // places of a tile's rows
 constexpr int kItemKeys = 384;                   // what an item's start and end cost, in keys
 constexpr int kMinBlocks = 4;                    // least blocks of keys worth an SM
 constexpr int kTile = kBlock * kHeadDim * 2, kHalf = kTile / 2;      // bytes; a half: 64 dims
-constexpr int kSmemQ = 0, kSmemK = 2 * kTile, kSmemV = 4 * kTile, kSmemStage = 6 * kTile;
+constexpr int kSmemQ = 0, kSmemK = 2 * kTile;
+constexpr int kRingBf16 = 5;                     // K0 V0 K1 V1 ...
+constexpr int kRingK = 4, kSmemV = kSmemK + kRingK * kHalf, kSmemStage = kSmemV + 2 * kTile;      // e4m3
+constexpr int kSmemEnd = 7 * kTile;
+static_assert(kSmemK + kRingBf16 * kTile == kSmemEnd && kSmemStage + 2 * kHalf == kSmemEnd, "shared memory");
 
-enum { QF = 0, QE = 2, KF = 4, KE = 8, VF = 12, VE = 14, SF = 16, PF = 18, OF = 20, MF = 22, ME = 24, SG = 26, SE = 28, VX = 30,
-       DR = 32, kBars = 33 };
-constexpr int kItemReaders = 1 + 2 + 8 + 4;      // the issuer, the queries' warps, the softmax warps, the loaders' warps
+// Barriers: queries, tiles full and empty (bf16: of the ring; e4m3: of K, then V), S ready, P
+// ready, O ready, items, staged tiles (bf16: tiles to be cleaned, of which the ring may hold
+// three) full and empty (cleaned).
+enum { QF = 0, QE = 2, TF = 4, TE = 10, SF = 16, PF = 18, OF = 20, MF = 22, ME = 24, GF = 26, GE = 29, DR = 32, kBars = 33 };
+constexpr int kUnclean = (kRingBf16 + 1) / 2;
+static_assert(kUnclean == GE - GF, "barriers of tiles to be cleaned");
+constexpr int VF = TF + kRingK, VE = TE + kRingK;
+constexpr int kItemReaders = 1 + 1 + 1 + 8 + 4;  // issuer, queries, copies, softmax warps, loaders' warps
 
 // A piece of an item, as the roles read it.
 struct Item {
     int live;                                    // 0: no more
     int r, row0, lq, len, kv;
-    int rows, tile;                              // packed rows of the request; tile of them
-    int c0, c1;                                  // blocks of keys
+    int rows, tile;                              // queries of the request; tile of them
+    int c0, c1;                                  // blocks of keys (none: rows without a key)
     int edge;                                    // first block that not every row attends whole
     int min_keys;                                // keys of the tile's first row
     int opens, closes;
     int not_finite;                              // any of:
     int pad;
     int from[kHeadDim];                          // first key of a value that was taken out, INT_MAX: none
-    signed char exponent[kRows];                 // of the power of two that a query row was multiplied by
 };
 struct Control {
     unsigned long long bars[kBars];
@@ -78,10 +87,10 @@ struct Control {
         long long sums[kTilesWarps];             // of the scan, before the roles part
     };
 };
-constexpr int kSmemBf16 = kSmemStage + (int)sizeof(Control) + 1024, kSmemFp8 = kSmemBf16 + kTile;
-static_assert(kSmemFp8 <= 227 * 1024, "shared memory");
+constexpr int kSmem = kSmemEnd + (int)sizeof(Control) + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
-// The columns' sum over the whole block of threads.
+// Exclusive scan over all threads; *all is the sum.
 __device__ __forceinline__ long long scan_all(long long n, long long *all, long long *sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     long long x = n;
@@ -104,25 +113,24 @@ __device__ __forceinline__ long long scan_all(long long n, long long *all, long 
     return x;
 }
 
-// A request's tiles, and the units of each: base + 256 (tile + 1), keys times g.
+// A request's tiles, and the units of each, in keys: base + queries up to its end.
 struct Tiles {
     int n, start;
     long long base;
 };
 __device__ __forceinline__ Tiles tiles_in(const PAttn &a, const Request &q) {
     Tiles t;
-    const long long rows = (long long)q.rows * a.g;
-    t.n = rows > a.most_columns ? (int)((rows + kRows - 1) / kRows) : 0;
+    t.n = (long long)q.rows * a.g > a.most_columns ? (q.rows + 2 * a.half - 1) / (2 * a.half) : 0;
     t.start = q.len - q.lq;
     // a start past 2^27 counts as that: sums of weights stay in 64 bits
-    t.base = (long long)a.g * (kItemKeys + min(max(t.start, 0), 1 << 27));
+    t.base = kItemKeys + min(max(t.start, 0), 1 << 27);
     return t;
 }
-__device__ __forceinline__ long long units_before(const Tiles &t, long long tile) {
-    return tile * t.base + 128 * tile * (tile + 1);
+__device__ __forceinline__ long long units_before(const PAttn &a, const Tiles &t, long long tile) {
+    return tile * t.base + a.half * tile * (tile + 1);
 }
 __device__ __forceinline__ long long units_of(const PAttn &a, const Tiles &t) {
-    const long long u = a.c.h_kv * units_before(t, t.n);
+    const long long u = a.c.h_kv * units_before(a, t, t.n);
     return u < (1ll << 50) ? u : 1ll << 50;      // past any lengths that fit together
 }
 
@@ -155,127 +163,16 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t tile, int row, int piece) 
     return tile + (piece >> 3) * kHalf + row * 128 + (((piece ^ row) & 7) << 4);
 }
 
-// 16 bytes into shared memory, or zeros.
-__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-
-// A half's 128 rows of queries into shared memory, by a warp: `mine(row)` is the address of a
-// row, 0 for one that is not there.  A bf16 cache takes bf16 tiles.  An e4m3 one takes e4m3
-// codes as they are; bf16 rows under a power of two, as two e4m3 terms of 4 bits each, which
-// hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it.
-template <bool kFp8, typename F>
-__device__ __forceinline__ void load_queries(const PAttn &a, const F &mine, uint32_t tile, signed char *exponent) {
-    const int lane = threadIdx.x & 31;
-    const bool codes = a.q_scale != nullptr;
-#pragma unroll 1
-    for (int set = 0; set < 4; ++set) {
-        const unsigned long long own = mine(32 * set + lane);
-        if (codes) {                             // 8 lanes a row, 4 rows at once
-            if (kFp8) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const unsigned long long p = __shfl_sync(~0u, own, 4 * i + (lane >> 3));
-                    const int row = 32 * set + 4 * i + (lane >> 3), c = lane & 7;
-                    copy16_or_zero(tile + row * 128 + (((c ^ row) & 7) << 4),
-                                   p ? reinterpret_cast<const unsigned char *>(p) + c * 16 : static_cast<const unsigned char *>(a.q), p != 0);
-                }
-            } else {
-                uint4 w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const unsigned long long p = __shfl_sync(~0u, own, 4 * i + (lane >> 3));
-                    w[i] = p ? *reinterpret_cast<const uint4 *>(p + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = 32 * set + 4 * i + (lane >> 3), c = lane & 7;
-                    const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        h[e] = codes_to_f16(v[e >> 1] >> (16 * (e & 1)));
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-                        h[e] = pack16<false>(f.x, f.y);
-                    }
-                    st_shared_v4(piece_at(tile, row, 2 * c), make_uint4(h[0], h[1], h[2], h[3]));
-                    st_shared_v4(piece_at(tile, row, 2 * c + 1), make_uint4(h[4], h[5], h[6], h[7]));
-                }
-            }
-        } else {                                 // 16 lanes a row, 2 rows at once
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const unsigned long long p = __shfl_sync(~0u, own, 2 * i + (lane >> 4));
-                const int row = 32 * set + 2 * i + (lane >> 4), c = lane & 15;
-                copy16_or_zero(piece_at(tile, row, c),
-                               p ? reinterpret_cast<const unsigned char *>(p) + c * 16 : static_cast<const unsigned char *>(a.q), p != 0);
-            }
-        }
-    }
-    copies_commit();
-    copies_wait<0>();
-    __syncwarp();
-    if (kFp8 && !codes) {
-        // in place: a row's 64 and 64 dims of bf16 make room for its two terms of 128 bytes
-#pragma unroll 1
-        for (int i0 = 0; i0 < 64; i0 += 4) {
-            uint4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ld_shared_v4(piece_at(tile, 2 * (i0 + i) + (lane >> 4), lane & 15));
-            uint2 hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                float x[8], top = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(v[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
-                    top = max3f(top, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
-                }
-#pragma unroll
-                for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
-                if ((lane & 15) == 0) exponent[2 * (i0 + i) + (lane >> 4)] = (signed char)ex;
-                const float up = pow2f(ex);
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u = x[2 * e] * up, y = x[2 * e + 1] * up;
-                    h[e] = e4m3_pair(u, y);
-                    const uint32_t back = codes_to_f16(h[e]);
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-                    l[e] = e4m3_pair(u - f.x, y - f.y);
-                }
-                hi[i] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-                lo[i] = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 2 * (i0 + i) + (lane >> 4), c = lane & 15;
-                const uint32_t at = tile + row * 128 + ((((c >> 1) ^ row) & 7) << 4) + (c & 1) * 8;
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[i].x), "r"(hi[i].y) : "memory");
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + kHalf), "r"(lo[i].x), "r"(lo[i].y) : "memory");
-            }
-        }
-    }
-}
-
 template <bool kFp8>
 __global__ void __launch_bounds__(kTilesThreads, 1)
-tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMap map_k,
+tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v, unsigned long long limit_ns) {
     extern __shared__ unsigned char smem_raw[];
     // 1024-byte aligned, as the swizzle wants; addresses by offsets in the shared window
     unsigned char *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-    Control &ctl = *reinterpret_cast<Control *>(smem + (kFp8 ? kSmemStage + kTile : kSmemStage));
+    Control &ctl = *reinterpret_cast<Control *>(smem + kSmemEnd);
     const uint32_t base = smem_u32(smem), bars = smem_u32(ctl.bars);
     const auto bar = [&](int k) { return bars + 8u * (uint32_t)k; };
-    constexpr int kRing = kFp8 ? 4 : 2, kSlot = kTile / (kFp8 ? 2 : 1);        // tiles of K, as they come
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
     after_previous();
 
@@ -285,7 +182,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     long long n = 0, total;
     for (int r = tid * each; r < min(a.batch, (tid + 1) * each); ++r) n += units_of(a, tiles_in(a, q = request_of(a, r)));
     long long low = scan_all(n, &total, ctl.sums);
-    const long long want = total / ((long long)a.g * kBlock * kMinBlocks) + 1;
+    const long long want = total / (kBlock * kMinBlocks) + 1;
     const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
@@ -306,9 +203,9 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     if (tid == 0) {
         for (int k = 0; k < kBars; ++k) {
             uint32_t count = 1;
-            if (k == PF || k == PF + 1 || k == SE || k == SE + 1 || k == VX || k == VX + 1) count = 128;
+            if (k == PF || k == PF + 1 || (k >= GE && k < GE + kUnclean)) count = 128;
             if (kFp8 && (k == VF || k == VF + 1)) count = 128;
-            if (k == MF || k == MF + 1 || k == QF || k == QF + 1) count = 32;
+            if (k == MF || k == MF + 1) count = 32;
             if (k == ME || k == ME + 1) count = kItemReaders;
             mbar_init(bar(k), count);
         }
@@ -335,21 +232,21 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         } else if (warp == 1) {
             // ================= the walk over the items =================
             int r = ctl.r;
+            long long item0 = ctl.at, at = first;
             q = request_of(a, r);
             Tiles t = tiles_in(a, q);
-            long long item0 = ctl.at, at = first;
             int kv, tile;
             {
-                const long long head = units_before(t, t.n);
+                const long long head = units_before(a, t, t.n);
                 kv = min((int)quotient(first - item0, head), a.c.h_kv - 1);
                 item0 += kv * head;
                 int lo = 0, hi = t.n - 1;        // the last tile that starts at or before `first`
                 while (lo < hi) {
                     const int mid = (lo + hi + 1) >> 1;
-                    if (item0 + units_before(t, mid) <= first) lo = mid; else hi = mid - 1;
+                    if (item0 + units_before(a, t, mid) <= first) lo = mid; else hi = mid - 1;
                 }
                 tile = lo;
-                item0 += units_before(t, tile);
+                item0 += units_before(a, t, tile);
             }
             for (int k = 0;; ++k) {
                 const int b = k & 1;
@@ -371,17 +268,17 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                         kv = tile = 0;
                     }
                     if (r >= a.batch) break;     // lengths that changed under the kernel
-                    const int rows = q.rows * a.g;
-                    const long long units = t.base + 256ll * (tile + 1), next = item0 + units;
-                    // keys of a packed row: up to its query's own
-                    const auto keys_of = [&](int row) { return max(0, min(q.len, t.start + row / a.g + 1)); };
-                    const int count = max(1, (keys_of(min(kRows * (tile + 1), rows) - 1) + kBlock - 1) / kBlock);
+                    const long long units = t.base + 2ll * a.half * (tile + 1), next = item0 + units;
+                    // keys of a query: up to its own
+                    const auto keys_of = [&](int i) { return max(0, min(q.len, t.start + i + 1)); };
+                    const int count = (keys_of(min(2 * a.half * (tile + 1), q.rows) - 1) + kBlock - 1) / kBlock;
                     const auto block_of = [&](long long unit) {
-                        const long long c = (quotient(unit, a.g) - kItemKeys) / kBlock;
+                        const long long c = (unit - kItemKeys) / kBlock;
                         return (int)(c < 0 ? 0 : c < count ? c : count);
                     };
                     const int c0 = at <= item0 ? 0 : block_of(at - item0), c1 = end >= next ? count : block_of(end - item0);
-                    if (c1 > c0) {
+                    // rows without a key are the piece's that has the item's first unit
+                    if (c1 > c0 || (count == 0 && at <= item0)) {
                         live = true;
                         if (lane == 0) {
                             it.r = r;
@@ -389,17 +286,17 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                             it.lq = q.lq;
                             it.len = q.len;
                             it.kv = kv;
-                            it.rows = rows;
+                            it.rows = q.rows;
                             it.tile = tile;
                             it.c0 = c0;
                             it.c1 = c1;
-                            it.min_keys = keys_of(kRows * tile);
+                            it.min_keys = keys_of(2 * a.half * tile);
                             it.edge = it.min_keys / kBlock;
                             it.opens = c0 == 0;
                             it.closes = c1 == count;
                             it.not_finite = 0;
                             if (c0 == 0 && c1 < count) {             // and the block that has its last key
-                                const long long whole = (long long)a.g * (kItemKeys + (long long)kBlock * count);
+                                const long long whole = kItemKeys + (long long)kBlock * count;
                                 const long long last = item0 + (whole < units ? whole : units) - 1, ends = longer * (share + 1);
                                 const long long to = last < ends ? quotient(last, share + 1) : longer + quotient(last - ends, share);
                                 sc.open[blockIdx.x] = Open{(int)(to < blocks ? to : blocks - 1) - (int)blockIdx.x + 1, q.row0, q.rows, kv, tile};
@@ -420,14 +317,14 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             constexpr uint32_t kIdS = kFp8 ? idesc_e4m3(128, 128, false) : idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = kFp8 ? idesc_f16(128, 128, true) : idesc_bf16(128, 128, true);
             const uint64_t dq = smem_desc_sw128(base + kSmemQ, 16, 1024), dk = smem_desc_sw128(base + kSmemK, 16, 1024);
-            const uint64_t dv = smem_desc_sw128(base + kSmemV, kHalf, 1024);
-            // e4m3: one term of the queries, or two
-            const auto issue_s = [&](int t, int s) {
-                const uint64_t qt = dq + ((t * kTile) >> 4), ks = dk + ((s * kSlot) >> 4);
+            const uint64_t dv = smem_desc_sw128(base + (kFp8 ? kSmemV : kSmemK), kHalf, 1024);
+            const bool terms = kFp8 && !a.q_scale;           // two of the queries
+            const auto issue_s = [&](int t, uint32_t slot) {
+                const uint64_t qt = dq + ((t * kTile) >> 4), ks = dk + ((slot * (kFp8 ? kHalf : kTile)) >> 4);
                 if (kFp8) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + kk * 2, ks + kk * 2, kIdS, kk > 0);
-                    if (!a.q_scale)
+                    if (terms)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + (kHalf >> 4) + kk * 2, ks + kk * 2, kIdS, true);
                 } else {
@@ -439,62 +336,63 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 }
                 tc_commit(bar(SF + t));
             };
-            const auto issue_o = [&](int t, int s, bool more) {
+            const auto issue_o = [&](int t, uint32_t slot, bool more) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, dv + ((s * kTile + kk * 16 * 128) >> 4), kIdO, more || kk > 0);
+                    mma_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, dv + ((slot * kTile + kk * 16 * 128) >> 4), kIdO, more || kk > 0);
             };
+            // it: blocks so far.  Their tiles: bf16 K in place 2 it of the ring, V behind it
             uint32_t it = 0, edges = 0, phase0 = 0, phase1 = 0, items0 = 0, items1 = 0;
             for (int k = 0;; ++k) {
                 const int b = k & 1;
                 if (!wait(bar(MF + b), k >> 1)) break;
                 const Item &item = ctl.item[b];
                 const int live = item.live, count = item.c1 - item.c0, edge = kFp8 ? INT_MAX : item.edge - item.c0;
-                const bool two = item.rows - item.tile * kRows > kBlock;
+                const bool two = item.rows - 2 * a.half * item.tile > a.half;
                 mbar_arrive(bar(ME + b));
                 if (!live) break;
-                const auto keys_there = [&](uint32_t i) { return wait(bar(KF + i % kRing), i / kRing); };
-                if (!wait(bar(QF), items0++) || (two && !wait(bar(QF + 1), items1++)) || !keys_there(it)) break;
-                tc_fence_after();
-                issue_s(0, it % kRing);
-                if (count == 1) tc_commit(bar(QE));
-                if (two) {
-                    issue_s(1, it % kRing);
-                    if (count == 1) tc_commit(bar(QE + 1));
-                }
-                tc_commit(bar(KE + it % kRing));
-                // written out for both halves: as a loop over them it cost 8 %
+                if (count == 0) continue;
+                if (!wait(bar(QF), items0++) || (two && !wait(bar(QF + 1), items1++))) break;
                 bool good = true;
-                for (int j = 0; j < count; ++j, ++it) {
-                    const uint32_t s = it & 1, s1 = (it + 1) % kRing;
-                    const bool more = j + 1 < count, last = j + 2 == count;
-                    good = j < edge ? wait(bar(VF + s), it >> 1) : wait(bar(VX + (edges & 1)), edges >> 1);
-                    if (j >= edge) ++edges;
-                    if (!good || !(good = wait(bar(PF), phase0++))) break;
-                    tc_fence_after();
-                    issue_o(0, s, j > 0);
-                    if (more) {
-                        if (!(good = keys_there(it + 1))) break;
-                        tc_fence_after();
-                        issue_s(0, s1);
-                        if (last) tc_commit(bar(QE));
-                    } else {
-                        tc_commit(bar(OF));
-                    }
-                    if (two) {
-                        if (!(good = wait(bar(PF + 1), phase1++))) break;
-                        tc_fence_after();
-                        issue_o(1, s, j > 0);
-                    }
-                    tc_commit(bar(VE + s));
-                    if (more) {
-                        if (two) {
-                            issue_s(1, s1);
-                            if (last) tc_commit(bar(QE + 1));
+                // S of block j behind O of block j - 1, half by half; written out for both halves (as a
+                // loop over them it cost 8 %)
+                for (int j = 0; j <= count; ++j) {
+                    const uint32_t x = 2 * (it - 1) + 1;             // V of the block before
+                    const uint32_t vs = kFp8 ? (it - 1) & 1 : x % kRingBf16, ks = kFp8 ? it % kRingK : (2 * it) % kRingBf16;
+                    if (j > 0) {
+                        if (j - 1 >= edge) {
+                            good = wait(bar(GE + edges % kUnclean), edges / kUnclean);
+                            ++edges;
+                        } else {
+                            good = kFp8 ? wait(bar(VF + vs), (it - 1) >> 1) : wait(bar(TF + vs), x / kRingBf16);
                         }
-                        tc_commit(bar(KE + s1));
-                    } else if (two) {
-                        tc_commit(bar(OF + 1));
+                        if (!good || !(good = wait(bar(PF), phase0++))) break;
+                        tc_fence_after();
+                        issue_o(0, vs, j > 1);
+                        if (j == count) tc_commit(bar(OF));
+                    }
+                    if (j < count) {
+                        if (!(good = kFp8 ? wait(bar(TF + ks), it / kRingK) : wait(bar(TF + ks), 2 * it / kRingBf16))) break;
+                        tc_fence_after();
+                        issue_s(0, ks);
+                        if (j + 1 == count) tc_commit(bar(QE));
+                    }
+                    if (j > 0) {
+                        if (two) {
+                            if (!(good = wait(bar(PF + 1), phase1++))) break;
+                            tc_fence_after();
+                            issue_o(1, vs, j > 1);
+                            if (j == count) tc_commit(bar(OF + 1));
+                        }
+                        tc_commit(bar((kFp8 ? VE : TE) + vs));
+                    }
+                    if (j < count) {
+                        if (two) {
+                            issue_s(1, ks);
+                            if (j + 1 == count) tc_commit(bar(QE + 1));
+                        }
+                        tc_commit(bar(TE + ks));
+                        ++it;
                     }
                 }
                 if (!good) break;
@@ -503,123 +401,142 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 tc_commit(bar(DR));
                 mbar_wait_drain(bar(DR), 0);
             }
-        } else if (warp >= 2) {
-            // ================= queries, a warp a half =================
-            const int t = warp - 2;
-            uint32_t items = 0;
+        } else if (warp == 2 && lane == 0) {
+            // ================= queries =================
+            uint32_t items[2] = {0, 0};
+            for (int k = 0;; ++k) {
+                const int b = k & 1;
+                if (!wait(bar(MF + b), k >> 1)) break;
+                const Item &item = ctl.item[b];
+                if (!item.live) break;
+                const int i0 = 2 * a.half * item.tile, count = item.c1 - item.c0;
+                bool good = true;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (count == 0 || item.rows - i0 <= t * a.half) continue;
+                    // the products of the item before are done with their queries
+                    if (good && items[t]) good = wait(bar(QE + t), items[t] - 1);
+                    if (!good) continue;
+                    const int row = item.row0 + i0 + t * a.half;
+                    const int boxes = kFp8 && a.q_scale ? 1 : 2;     // bf16: 64 dims each; e4m3: a term each
+                    mbar_expect_tx(bar(QF + t), boxes * a.half * a.g * 128);
+                    for (int x = 0; x < boxes; ++x)
+                        tma_load_3d(base + kSmemQ + t * kTile + x * kHalf, &map_q, bar(QF + t), kFp8 ? 0 : 64 * x, item.kv * a.g,
+                                    row + (kFp8 ? x * a.total_q : 0));
+                    ++items[t];
+                }
+                mbar_arrive(bar(ME + b));
+                if (!good) break;
+            }
+            if (ld_shared_volatile(wait.abort))
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (items[t]) mbar_wait_drain(bar(QF + t), (items[t] - 1) & 1);
+        } else if (warp == 3) {
+            // ================= keys and values =================
+            const int box = a.c.page_size < kBlock ? a.c.page_size : kBlock, boxes = kBlock / box;     // rows of one; boxes of a block
+            const int outside = a.c.num_pages * a.c.page_size;               // reads zeros
+            uint32_t nt = 0, nk = 0, nx = 0, edges = 0;      // tiles of the ring (e4m3: of K, staged ones of V), edge blocks
             for (int k = 0;; ++k) {
                 const int b = k & 1;
                 if (!__all_sync(~0u, wait(bar(MF + b), k >> 1))) break;
-                Item &item = ctl.item[b];
+                const Item &item = ctl.item[b];
                 if (!item.live) break;
-                const int row0 = item.tile * kRows + t * kBlock;
-                if (item.rows > row0) {
-                    // the products of the item before are done with their queries
-                    if (items && !__all_sync(~0u, wait(bar(QE + t), items - 1))) break;
-                    const auto mine = [&](int row) -> unsigned long long {
-                        const int packed = row0 + row, i = packed / a.g, head = item.kv * a.g + packed % a.g;
-                        if (packed >= item.rows) return 0;
-                        const long long at = (item.row0 + i) * a.q_stride_tok + head * a.q_stride_head;
-                        return (unsigned long long)(static_cast<const unsigned char *>(a.q) + (a.q_scale ? at : 2 * at));
-                    };
-                    load_queries<kFp8>(a, mine, base + kSmemQ + t * kTile, item.exponent + t * kBlock);
-                    fence_proxy_async();
-                    mbar_arrive(bar(QF + t));
-                    ++items;
+                const int c0 = item.c0, count = item.c1 - c0, len = item.len, kv = item.kv, edge = item.edge;
+                const int *table = a.block_table + (long long)item.r * a.max_pages;
+                // the row of the caches where this lane's box of a block starts
+                const auto look = [&](int j) {
+                    const int tok = (c0 + j) * kBlock + (lane % boxes) * box;
+                    if (j >= count || tok >= len) return outside;
+                    const int page = table[tok / a.c.page_size];
+                    if (page < 0 || page >= a.c.num_pages) {
+                        set_status(a.status, FP_ERR_DEVICE_BOUNDS);
+                        return outside;
+                    }
+                    return page * a.c.page_size + tok % a.c.page_size;
+                };
+                const auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int z) {
+                    if (lane == 0) mbar_expect_tx(full, kFp8 ? kHalf : kTile);
+                    __syncwarp();
+                    if (lane < (kFp8 ? 1 : 2) * boxes)
+                        tma_load_3d(dst + (lane / boxes) * kHalf + (lane % boxes) * box * 128, map, full, (lane / boxes) * 64, kv, z);
+                    __syncwarp();
+                };
+                bool good = true;
+                int z0 = look(0), z1 = look(1);
+                if (!kFp8) {
+                    for (int x = 0; x < 2 * count && good; ++x) {
+                        const uint32_t slot = nt % kRingBf16;
+                        if (!(good = nt < kRingBf16 || __all_sync(~0u, wait(bar(TE + slot), (nt / kRingBf16) ^ 1)))) break;
+                        const bool v = x & 1, unclean = v && c0 + x / 2 >= edge;
+                        if (unclean && lane == 0) mbar_arrive(bar(TF + slot));       // the issuer waits for the cleaners instead
+                        copy(v ? &map_v : &map_k, base + kSmemK + slot * kTile, unclean ? bar(GF + edges % kUnclean) : bar(TF + slot), z0);
+                        edges += unclean;
+                        ++nt;
+                        if (v) {
+                            z0 = z1;
+                            z1 = look(x / 2 + 2);
+                        }
+                    }
+                } else {
+                    // K0 K1 K2 V0 K3 V1 ...: V of block j behind K of block j + 2
+                    int zv = z0, zw = z1;                    // of the next two V
+                    for (int j = 0; j < count + 2 && good; ++j) {
+                        const int z2 = look(j + 2);
+                        if (j < count) {
+                            const uint32_t slot = nk % kRingK;
+                            if (!(good = nk < kRingK || __all_sync(~0u, wait(bar(TE + slot), (nk / kRingK) ^ 1)))) break;
+                            copy(&map_k, base + kSmemK + slot * kHalf, bar(TF + slot), z0);
+                            ++nk;
+                        }
+                        if (j >= 2) {
+                            const uint32_t slot = nx & 1;
+                            if (!(good = nx < 2 || __all_sync(~0u, wait(bar(GE + slot), (nx >> 1) ^ 1)))) break;
+                            copy(&map_v, base + kSmemStage + slot * kHalf, bar(GF + slot), zv);
+                            ++nx;
+                            zv = zw;
+                            zw = z0;
+                        }
+                        z0 = z1;
+                        z1 = z2;
+                    }
                 }
+                if (!good) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ME + b));
+            }
+            // after an abort, the copies armed last land before the block leaves
+            if (lane == 0 && ld_shared_volatile(wait.abort)) {
+                constexpr uint32_t kRing = kFp8 ? kRingK : kRingBf16;
+                const uint32_t m = kFp8 ? nk : nt, g = kFp8 ? nx : edges;
+                for (uint32_t i = m < kRing ? 0 : m - kRing; i < m; ++i) mbar_wait_drain(bar(TF + i % kRing), (i / kRing) & 1);
+                constexpr uint32_t kStaged = kFp8 ? 2 : kUnclean;
+                for (uint32_t i = g < kStaged ? 0 : g - kStaged; i < g; ++i) mbar_wait_drain(bar(GF + i % kStaged), (i / kStaged) & 1);
             }
         }
     } else if (warp < 8) {
         setmaxnreg_dec<kRegsLoad>();
-        // ================= loaders =================
-        const int lw = warp - 4, lt = tid - 128;
-        const int box = a.c.page_size < kBlock ? a.c.page_size : kBlock, boxes = kBlock / box;     // rows of one; boxes of a block
-        const int outside = a.c.num_pages * a.c.page_size;               // reads zeros
-        uint32_t nk = 0, nv = 0, nx = 0, edges = 0;      // tiles of K and V, staged ones of V, edge blocks
+        // ================= loaders: e4m3 values become fp16; bf16 ones are cleaned where some rows do not attend them
+        const int lt = tid - 128;
+        uint32_t nv = 0, edges = 0;                      // blocks, edge blocks
         for (int k = 0; !dead; ++k) {
             const int b = k & 1;
             const bool got = wait(bar(MF + b), k >> 1);
             if (!__all_sync(~0u, got)) break;
             Item &item = ctl.item[b];
             if (!item.live) break;
-            const int c0 = item.c0, count = item.c1 - c0, len = item.len, kv = item.kv, edge = item.edge, min_keys = item.min_keys;
-            const int *table = a.block_table + (long long)item.r * a.max_pages;
-            // the row of the caches where this lane's box of a block starts
-            const auto look = [&](int j) {
-                const int tok = (c0 + j) * kBlock + (lane % boxes) * box;
-                if (lw > 1 || j >= count || tok >= len) return outside;
-                const int page = table[tok / a.c.page_size];
-                if (page < 0 || page >= a.c.num_pages) {
-                    set_status(a.status, FP_ERR_DEVICE_BOUNDS);
-                    return outside;
-                }
-                return page * a.c.page_size + tok % a.c.page_size;
-            };
-            const auto copy = [&](const CUtensorMap *map, uint32_t dst, uint32_t full, int z) {       // a warp
-                if (lane == 0) mbar_expect_tx(full, kSlot);
-                __syncwarp();
-                if (lane < (kFp8 ? 1 : 2) * boxes)
-                    tma_load_3d(dst + (lane / boxes) * kHalf + (lane % boxes) * box * 128, map, full, (lane / boxes) * 64, kv, z);
-                __syncwarp();
-            };
+            const int c0 = item.c0, count = item.c1 - c0, len = item.len, edge = item.edge, min_keys = item.min_keys;
             bool good = true;
-            // K by warp 1, as far ahead as its ring goes
-            const auto keys = [&](int z) {
-                good = nk < kRing || __all_sync(~0u, wait(bar(KE + nk % kRing), (nk / kRing) ^ 1));
-                if (good) {
-                    copy(&map_k, base + kSmemK + (nk % kRing) * kSlot, bar(KF + nk % kRing), z);
-                    ++nk;
-                }
-            };
-            const auto stage = [&](int z) {              // e4m3 V, by warp 0
-                good = nx < 2 || __all_sync(~0u, wait(bar(SE + (nx & 1)), (nx >> 1) ^ 1));
-                if (good) {
-                    copy(&map_v, base + kSmemStage + (nx & 1) * kHalf, bar(SG + (nx & 1)), z);
-                    ++nx;
-                }
-            };
-            constexpr int kAhead = kRing - 1;
-            int z1 = 0;                                  // of the next tile that this warp copies
-            if (lw == 1) {
-                int z[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) z[i] = look(i);
-                z1 = look(kAhead);
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    if (i < count && good) keys(z[i]);
-            } else if (lw == 0) {
-                const int z0 = look(0);
-                z1 = look(1);
-                if (kFp8) {
-                    stage(z0);
-                    if (count > 1 && good) stage(z1);
-                    z1 = look(2);
-                } else {
-                    z1 = z0;
-                }
-            }
-            for (int j = 0; j < count && good; ++j, ++nv) {
-                const uint32_t s = nv & 1, tile = base + kSmemV + s * kTile;
-                const int z = z1;
-                if (lw < 2) z1 = look(j + 1 + (lw == 1 ? kAhead : kFp8 ? 2 : 0));
-                if (lw == 1 && j + kAhead < count) keys(z);
-                // every loader follows the ring phase by phase: a parity alone does not tell a tile from
-                // the one before it
-                if (!good || !(good = nv < 2 || __all_sync(~0u, wait(bar(VE + s), (nv >> 1) ^ 1)))) break;
+            for (int j = kFp8 ? 0 : max(0, edge - c0); j < count && good; ++j) {
                 if (!kFp8) {
-                    if (lw == 0) copy(&map_v, tile, bar(VF + s), z);
-                    if (c0 + j < edge) continue;
-                    // a thread a row
-                    if (!(good = __all_sync(~0u, wait(bar(VF + s), nv >> 1)))) break;
-                    const int key = (c0 + j) * kBlock + lt;         // can pass 2^31 behind the last token
+                    const uint32_t tile = base + kSmemK + ((2 * (nv + j) + 1) % kRingBf16) * kTile;
+                    if (!(good = __all_sync(~0u, wait(bar(GF + edges % kUnclean), edges / kUnclean)))) break;
+                    const int key = (c0 + j) * kBlock + lt;         // a thread a row; can pass 2^31 behind the last token
                     if ((uint32_t)key >= (uint32_t)len) {
-#pragma unroll
+#pragma unroll 4
                         for (int p = 0; p < 16; ++p) st_shared_v4(piece_at(tile, lt, p), make_uint4(0, 0, 0, 0));
                     } else if (key >= min_keys) {
-#pragma unroll 4
+#pragma unroll 2
                         for (int p = 0; p < 16; ++p) {
                             uint4 w = ld_shared_v4(piece_at(tile, lt, p));
                             const auto bad = [](uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; };
@@ -638,12 +555,13 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                         }
                     }
                     fence_proxy_async();
-                    mbar_arrive(bar(VX + (edges & 1)));
+                    mbar_arrive(bar(GE + edges % kUnclean));
                     ++edges;
                 } else {
-                    if (!(good = __all_sync(~0u, wait(bar(SG + s), nv >> 1)))) break;      // the staging ring goes as V's does
-                    // rows 16 p + lt / 8, dims 16 c ..  The loops stay short: what the softmax and this
-                    // run at once has to fit the instruction caches
+                    const uint32_t s = nv & 1, tile = base + kSmemV + s * kTile;
+                    if (!(good = nv < 2 || __all_sync(~0u, wait(bar(VE + s), (nv >> 1) ^ 1)))) break;
+                    if (!(good = __all_sync(~0u, wait(bar(GF + s), nv >> 1)))) break;      // the staging ring goes as V's does
+                    // rows 16 p + lt / 8, dims 16 c ..
                     const uint32_t from = base + kSmemStage + s * kHalf + lt * 16;
                     const int row0 = lt >> 3, c = lt & 7, o = c >> 2;
                     const auto convert = [&](uint4 w, uint32_t (&h)[8]) {
@@ -700,29 +618,21 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     mbar_arrive(bar(VF + s));
                     // not before the codes were used: an arrival waits for no load that is on its way, and the
                     // next tile may land first
-                    mbar_arrive(bar(SE + s));
-                    if (lw == 0 && j + 2 < count) stage(z);
+                    mbar_arrive(bar(GE + s));
+                    ++nv;
                 }
             }
+            if (!kFp8) nv += count;
             if (!__all_sync(~0u, good)) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ME + b));
-        }
-        // after an abort, the copies armed last land before the block leaves
-        if (lw < 2 && lane == 0 && ld_shared_volatile(wait.abort)) {
-            if (lw == 1) {
-                for (uint32_t i = nk < kRing ? 0 : nk - kRing; i < nk; ++i) mbar_wait_drain(bar(KF + i % kRing), (i / kRing) & 1);
-            } else {
-                // of bf16, the one that the last wait was for may not have been armed: waiting for it runs out
-                const uint32_t n = kFp8 ? nx : nv + 1;
-                for (uint32_t i = n < 2 ? 0 : n - 2; i < n; ++i) mbar_wait_drain(bar((kFp8 ? SG : VF) + (i & 1)), (i >> 1) & 1);
-            }
         }
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
         // ================= softmax, a warpgroup a half, a thread a row =================
         const int t = (warp - 8) / 4, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t s_at = tmem + ((uint32_t)(quarter * 32) << 16) + t * 256, o_at = s_at + 128;
+        const int own = row / a.g;                       // query of the half
         uint32_t phase = 0, items = 0;
         for (int k = 0; !dead; ++k) {
             const int b = k & 1;
@@ -730,18 +640,21 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             if (!__all_sync(~0u, got)) break;
             const Item &item = ctl.item[b];
             if (!item.live) break;
-            const int rows = item.rows, packed = item.tile * kRows + t * kBlock + row;
-            if (rows - item.tile * kRows <= t * kBlock) {            // no row in this half
+            const int i0 = 2 * a.half * item.tile + t * a.half, i = i0 + own, head = item.kv * a.g + row - own * a.g;
+            const bool valid = own < a.half && i < item.rows;
+            if (item.rows <= i0) {                       // no row in this half
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ME + b));
                 continue;
             }
-            const bool valid = packed < rows;
-            const int i = packed / a.g, head = item.kv * a.g + packed % a.g;
             const int keys = valid ? max(0, min(item.len, item.len - item.lq + i + 1)) : 0;
+            const long long out_row = item.row0 + i;
             float cs = a.scale * kLog2e;                             // base-2 logits
             if (kFp8) cs *= __ldg(a.k_scale + item.kv);
-            if (a.q_scale && valid) cs *= __ldg(a.q_scale + head);
+            if (valid) {
+                if (a.q_scale) cs *= __ldg(a.q_scale + head);
+                else if (kFp8) cs *= pow2f(-a.q_exponent[out_row * a.h_q + head]);
+            }
             const int count = item.c1 - item.c0, key0 = item.c0 * kBlock;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
@@ -752,8 +665,6 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     break;
                 }
                 tc_fence_after();
-                if (kFp8 && !a.q_scale && j == 0)
-                    cs *= pow2f(-*reinterpret_cast<const volatile signed char *>(&item.exponent[t * kBlock + row]));
                 float x[128];
                 {
                     uint32_t v[4][32];
@@ -824,22 +735,30 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 l += (r0 + r1) + (r2 + r3);
             }
             if (!ok) break;
-            const bool done = wait(bar(OF + t), items);
-            if (!__all_sync(~0u, done)) break;
-            tc_fence_after();
+            if (count > 0) {
+                const bool done = wait(bar(OF + t), items);
+                if (!__all_sync(~0u, done)) break;
+                tc_fence_after();
+                ++items;
+            }
             const bool whole = item.opens && item.closes;
             const float v_scale = kFp8 ? __ldg(a.v_scale + item.kv) : 1.f;
             const float by = !whole ? v_scale : l == 0.f ? 0.f : v_scale / l;
             const int not_finite = *reinterpret_cast<const volatile int *>(&item.not_finite);
-            const long long out_row = item.row0 + i, slot = ((long long)blockIdx.x * 2 + (item.opens ? 1 : 0)) * kRows + t * kBlock + row;
+            const long long slot = ((long long)blockIdx.x * 2 + (item.opens ? 1 : 0)) * kRows + t * kBlock + row;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
-                tmem_ld32(o_at + c * 32, o);
-                tmem_ld_wait();
-                reg_fence(o);
+                if (count > 0) {
+                    tmem_ld32(o_at + c * 32, o);
+                    tmem_ld_wait();
+                    reg_fence(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
                 if (not_finite)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -865,7 +784,6 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ME + b));
-            ++items;
         }
     }
     tc_fence_before();
@@ -874,6 +792,57 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// Queries of another type than the tiles take, for the copies to fetch: e4m3 ones as bf16
+// rows; bf16 ones of an e4m3 cache under a power of two, as two e4m3 terms of 4 bits each,
+// which hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it:
+// [2][total_q, h_q, 128] codes, the exponents behind them.  16 lanes a row.
+template <bool kTerms>
+__global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed char *exponent) {
+    after_previous();
+    const long long rows = (long long)a.total_q * a.h_q, row = blockIdx.x * 16ll + threadIdx.x / 16;
+    const int c = threadIdx.x & 15;
+    if (row >= rows) return;                             // 16 lanes together
+    const long long tok = row / a.h_q, at = tok * a.q_stride_tok + (row - tok * a.h_q) * a.q_stride_head + 8 * c;
+    if (!kTerms) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at);
+        uint32_t h[4] = {codes_to_f16(w.x), codes_to_f16(w.x >> 16), codes_to_f16(w.y), codes_to_f16(w.y >> 16)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
+            h[e] = pack16<false>(f.x, f.y);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(to) + row * kHeadDim + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+        return;
+    }
+    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + at);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    float x[8], top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(v[e] << 16);
+        x[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+        top = max3f(top, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
+    }
+    const unsigned lanes = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, d));
+    const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
+    const float up = pow2f(ex);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float u = x[2 * e] * up, y = x[2 * e + 1] * up;
+        hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(u, y), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t back = codes_to_f16(hi[e]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+        lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(u - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
+    }
+    unsigned char *p = static_cast<unsigned char *>(to) + row * kHeadDim + 8 * c;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2 *>(p + rows * kHeadDim) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    if (c == 0) exponent[row] = (signed char)ex;
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -890,15 +859,16 @@ EncodeFn encode() {
     }();
     return fn;
 }
-// A cache as [tokens][h_kv][128]: boxes of tokens of one head, 64 dims of bf16 or 128 of e4m3,
-// swizzled as the products take them or plain; a token past the last one reads zeros.
-bool map_pages(CUtensorMap *m, const void *base, const Pages &c, bool fp8, bool swizzled) {
+// [n2][n1][128] of bf16 or e4m3 at strides s1, s2 (elements): boxes of 128 bytes of a row by b1
+// by b2, swizzled as the products take them or plain; past the end it reads zeros.
+bool make_map(CUtensorMap *m, const void *base, long long n1, long long n2, long long s1, long long s2, int b1, int b2, bool fp8,
+              bool swizzled) {
     const EncodeFn fn = encode();
     if (!fn) return false;
     const cuuint64_t esz = fp8 ? 1 : 2;
-    const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)c.h_kv, (cuuint64_t)c.num_pages * c.page_size};
-    const cuuint64_t strides[2] = {kHeadDim * esz, kHeadDim * esz * c.h_kv};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), 1, (cuuint32_t)(c.page_size < kBlock ? c.page_size : kBlock)};
+    const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * esz, (cuuint64_t)s2 * esz};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)b1, (cuuint32_t)b2};
     const cuuint32_t one[3] = {1, 1, 1};
     return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
               box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -908,19 +878,39 @@ bool map_pages(CUtensorMap *m, const void *base, const Pages &c, bool fp8, bool 
 // Thread blocks: one for each SM, and no more than the longest lengths that the table holds would use.
 int tiles_blocks(const PAttn &a) {
     const long long rows = a.cu ? a.total_q : (long long)a.batch * a.max_q;
-    const double items = (double)a.c.h_kv * ((double)rows * a.g / kRows + a.batch);
+    const double items = (double)a.c.h_kv * ((double)rows / (2 * (kBlock / a.g)) + a.batch);
     const double blocks = items * ((double)a.max_pages * a.c.page_size + 2 * kItemKeys) / (kBlock * kMinBlocks) + 1;
     return blocks < kSm ? (int)blocks : kSm;
+}
+
+// Where the join's rows are: a tile's halves hold whole queries.
+struct HalfRows {
+    template <typename A>
+    static __device__ __forceinline__ bool place(const A &a, int tile, int col, int &i, int &j) {
+        const int row = col & (kBlock - 1), own = row / a.g;
+        i = (2 * tile + col / kBlock) * a.half + own;
+        j = row - own * a.g;
+        return own < a.half;
+    }
+};
+
+// Bytes that queries of another type take (queries_kernel).
+size_t converted_bytes(const PAttn &a) {
+    const size_t rows = (size_t)a.total_q * a.h_q;
+    return (a.k_scale != nullptr) == a.q_codes ? 0 : align256(rows * 2 * kHeadDim) + align256(rows);
 }
 
 }  // namespace
 
 size_t cache_tiles_scratch_bytes(const PAttn &a) {
     const size_t n = tiles_blocks(a);
-    return align256(n * sizeof(Open)) + align256(n * 2 * kRows * sizeof(float2)) + n * 2 * kRows * kHeadDim * sizeof(float);
+    return align256(n * sizeof(Open)) + align256(n * 2 * kRows * sizeof(float2)) + n * 2 * kRows * kHeadDim * sizeof(float) +
+           converted_bytes(a);
 }
 
-cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long limit_ns, cudaStream_t st) {
+cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long long limit_ns, cudaStream_t st) {
+    PAttn a = args;
+    a.half = kBlock / a.g;
     const size_t n = tiles_blocks(a);
     char *p = static_cast<char *>(scratch);
     Scratch sc;
@@ -929,16 +919,37 @@ cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long
     sc.ml = reinterpret_cast<float2 *>(p);
     p += align256(n * 2 * kRows * sizeof(float2));
     sc.o = reinterpret_cast<float *>(p);
+    p += n * 2 * kRows * kHeadDim * sizeof(float);
     const bool fp8 = a.k_scale != nullptr;
-    CUtensorMap map_k, map_v;
-    if (!map_pages(&map_k, a.c.k, a.c, fp8, true) || !map_pages(&map_v, a.c.v, a.c, fp8, !fp8)) return cudaErrorInvalidValue;
+    const long long rows = (long long)a.total_q * a.h_q;
+    const void *q = a.q;
+    long long q_tok = a.q_stride_tok, q_head = a.q_stride_head, q_rows = a.total_q;
+    cudaError_t e;
+    if (converted_bytes(a)) {
+        signed char *exponent = reinterpret_cast<signed char *>(p + align256((size_t)rows * 2 * kHeadDim));
+        const auto kernel = fp8 ? queries_kernel<true> : queries_kernel<false>;
+        if ((e = launch_chained(kernel, (unsigned)((rows + 15) / 16), 256, 0, st, a, (void *)p, exponent)) != cudaSuccess) return e;
+        q = p;
+        q_head = kHeadDim;
+        q_tok = (long long)a.h_q * kHeadDim;
+        if (fp8) {
+            q_rows = 2ll * a.total_q;
+            a.q_exponent = exponent;
+        }
+    }
+    CUtensorMap map_q, map_k, map_v;
+    const Pages &c = a.c;
+    const long long tokens = (long long)c.num_pages * c.page_size, pitch = (long long)c.h_kv * kHeadDim;
+    const int box = c.page_size < kBlock ? c.page_size : kBlock;
+    if (!make_map(&map_q, q, a.h_q, q_rows, q_head, q_tok, a.g, a.half, fp8, true) ||
+        !make_map(&map_k, c.k, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, true) ||
+        !make_map(&map_v, c.v, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, !fp8))
+        return cudaErrorInvalidValue;
     const auto kernel = fp8 ? tiles_kernel<true> : tiles_kernel<false>;
-    const int smem = fp8 ? kSmemFp8 : kSmemBf16;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if ((e = launch_chained(kernel, (unsigned)n, kTilesThreads, smem, st, a, sc, map_k, map_v, limit_ns)) != cudaSuccess) return e;
-    return launch_chained(join_kernel<kRows / 8, kSm, PAttn>, (unsigned)n * 8, kJoinWarps * 32, 0, st, a, sc,
-                          (int)n);
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    if ((e = launch_chained(kernel, (unsigned)n, kTilesThreads, kSmem, st, a, sc, map_q, map_k, map_v, limit_ns)) != cudaSuccess)
+        return e;
+    return launch_chained(join_kernel<HalfRows, kRows, kSm, PAttn>, (unsigned)n * 8, kJoinWarps * 32, 0, st, a, sc, (int)n);
 }
 
 }  // namespace fp
