@@ -18,9 +18,10 @@
 // over a long cache spread over all SMs.  A tile's weight is linear in its number, which makes
 // sums and searches closed.  An item that a range's end cuts leaves partial results to the join.
 //
-// Roles (16 warps): the issuer of products, the walk over the items, the copies of queries and
-// those of keys and values (TMA, through the block table), loaders that convert or clean, and a
-// softmax warpgroup for each half, a thread a row.  bf16 tiles of K and V share a ring of 5;
+// Roles (16 warps): the walk over the items, the issuer of products (and of the queries'
+// copies), a thread that follows the tiles for it, the copies of keys and values (TMA, through
+// the block table), loaders that convert or clean, and a softmax warpgroup for each half, a
+// thread a row.  bf16 tiles of K and V share a ring of 5;
 // e4m3 keys have one of 4, values one of 2 that the loaders fill from two staged tiles.  Every
 // wait is bounded.  The roles' code is kept short: together it has to fit the instruction
 // caches (with the conversion written out eight times a step took 5100 clocks and not 3700).
@@ -58,11 +59,11 @@ static_assert(kSmemK + kRingBf16 * kTile == kSmemEnd && kSmemStage + 2 * kHalf =
 // Barriers: queries, tiles full and empty (bf16: of the ring; e4m3: of K, then V), S ready, P
 // ready, O ready, items, staged tiles (bf16: tiles to be cleaned, of which the ring may hold
 // three) full and empty (cleaned).
-enum { QF = 0, QE = 2, TF = 4, TE = 10, SF = 16, PF = 18, OF = 20, MF = 22, ME = 24, GF = 26, GE = 29, DR = 32, kBars = 33 };
+enum { QF = 0, TF = 2, TE = 8, SF = 14, PF = 16, OF = 18, MF = 20, ME = 22, GF = 24, GE = 27, DR = 30, kBars = 31 };
 constexpr int kUnclean = (kRingBf16 + 1) / 2;
 static_assert(kUnclean == GE - GF, "barriers of tiles to be cleaned");
 constexpr int VF = TF + kRingK, VE = TE + kRingK;
-constexpr int kItemReaders = 1 + 1 + 1 + 8 + 4;  // issuer, queries, copies, softmax warps, loaders' warps
+constexpr int kItemReaders = 1 + 1 + 1 + 8 + 4;  // issuer, what follows for it, copies, softmax warps, loaders' warps
 
 // A piece of an item, as the roles read it.
 struct Item {
@@ -144,6 +145,27 @@ struct Waits {
     }
 };
 
+// Products with a descriptor's low word (address and leading offset) as they come and the high
+// one, alike for all 128-byte swizzled tiles here, as a constant: the issuer's time is that of
+// its instructions, and half a descriptor's arithmetic is half of it.
+constexpr uint32_t kDescHigh = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t at, uint32_t leading) { return (at >> 4 & 0x3fffu) | leading >> 4 << 16; }
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
+                 : "memory");
+}
+__device__ __forceinline__ void product_ss_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
+                 : "memory");
+}
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t more) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(id), "r"(more), "n"(kDescHigh)
+                 : "memory");
+}
+
 template <bool kFp8>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     if (kFp8) {
@@ -205,6 +227,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             uint32_t count = 1;
             if (k == PF || k == PF + 1 || (k >= GE && k < GE + kUnclean)) count = 128;
             if (kFp8 && (k == VF || k == VF + 1)) count = 128;
+            if (k == PF) count = 129;
             if (k == MF || k == MF + 1) count = 32;
             if (k == ME || k == ME + 1) count = kItemReaders;
             mbar_init(bar(k), count);
@@ -316,67 +339,69 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             // ================= the products' issuer =================
             constexpr uint32_t kIdS = kFp8 ? idesc_e4m3(128, 128, false) : idesc_bf16(128, 128, false);
             constexpr uint32_t kIdO = kFp8 ? idesc_f16(128, 128, true) : idesc_bf16(128, 128, true);
-            const uint64_t dq = smem_desc_sw128(base + kSmemQ, 16, 1024), dk = smem_desc_sw128(base + kSmemK, 16, 1024);
-            const uint64_t dv = smem_desc_sw128(base + (kFp8 ? kSmemV : kSmemK), kHalf, 1024);
-            const bool terms = kFp8 && !a.q_scale;           // two of the queries
+            const uint32_t dq = desc_low(base + kSmemQ, 16), dk = desc_low(base + kSmemK, 16);
+            const uint32_t dv = desc_low(base + (kFp8 ? kSmemV : kSmemK), kHalf);
+            const int terms = kFp8 && a.q_scale ? 1 : 2;     // tiles of a half's queries: bf16 64 dims each, e4m3 a term each
             const auto issue_s = [&](int t, uint32_t slot) {
-                const uint64_t qt = dq + ((t * kTile) >> 4), ks = dk + ((slot * (kFp8 ? kHalf : kTile)) >> 4);
+                const uint32_t qt = dq + ((t * kTile) >> 4), ks = dk + ((slot * (kFp8 ? kHalf : kTile)) >> 4);
                 if (kFp8) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + kk * 2, ks + kk * 2, kIdS, kk > 0);
-                    if (terms)
+                    for (int kk = 0; kk < 4; ++kk) product_ss_f8(tmem + t * 256, qt + kk * 2, ks + kk * 2, kIdS, kk > 0);
+                    if (terms == 2)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + t * 256, qt + (kHalf >> 4) + kk * 2, ks + kk * 2, kIdS, true);
+                        for (int kk = 0; kk < 4; ++kk) product_ss_f8(tmem + t * 256, qt + (kHalf >> 4) + kk * 2, ks + kk * 2, kIdS, true);
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        mma_ss(tmem + t * 256, qt + off, ks + off, kIdS, kk > 0);
+                        product_ss(tmem + t * 256, qt + off, ks + off, kIdS, kk > 0);
                     }
                 }
                 tc_commit(bar(SF + t));
             };
             const auto issue_o = [&](int t, uint32_t slot, bool more) {
+                const uint32_t vs = dv + ((slot * kTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, dv + ((slot * kTile + kk * 16 * 128) >> 4), kIdO, more || kk > 0);
+                    product_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8, vs + ((kk * 16 * 128) >> 4), kIdO, more || kk > 0);
             };
             // it: blocks so far.  Their tiles: bf16 K in place 2 it of the ring, V behind it
-            uint32_t it = 0, edges = 0, phase0 = 0, phase1 = 0, items0 = 0, items1 = 0;
+            uint32_t it = 0, phase0 = 0, phase1 = 0, items0 = 0, items1 = 0;
             for (int k = 0;; ++k) {
                 const int b = k & 1;
                 if (!wait(bar(MF + b), k >> 1)) break;
                 const Item &item = ctl.item[b];
-                const int live = item.live, count = item.c1 - item.c0, edge = kFp8 ? INT_MAX : item.edge - item.c0;
-                const bool two = item.rows - 2 * a.half * item.tile > a.half;
+                if (!item.live) break;
+                const int i0 = 2 * a.half * item.tile, count = item.c1 - item.c0;
+                const bool two = item.rows - i0 > a.half;
+                if (count) {
+                    // the weights of the item before are there, so its last products with the queries are done
+                    for (int t = 0; t < (two ? 2 : 1); ++t) {
+                        mbar_expect_tx(bar(QF + t), terms * a.half * a.g * 128);
+                        for (int x = 0; x < terms; ++x)
+                            tma_load_3d(base + kSmemQ + t * kTile + x * kHalf, &map_q, bar(QF + t), kFp8 ? 0 : 64 * x, item.kv * a.g,
+                                        item.row0 + i0 + t * a.half + (kFp8 ? x * a.total_q : 0));
+                    }
+                }
                 mbar_arrive(bar(ME + b));
-                if (!live) break;
                 if (count == 0) continue;
-                if (!wait(bar(QF), items0++) || (two && !wait(bar(QF + 1), items1++))) break;
+                ++items0;
+                items1 += two;
+                if (!wait(bar(QF), items0 - 1) || (two && !wait(bar(QF + 1), items1 - 1))) break;
+                if (!(kFp8 ? wait(bar(TF + it % kRingK), it / kRingK) : wait(bar(TF + 2 * it % kRingBf16), 2 * it / kRingBf16))) break;
                 bool good = true;
                 // S of block j behind O of block j - 1, half by half; written out for both halves (as a
                 // loop over them it cost 8 %)
                 for (int j = 0; j <= count; ++j) {
-                    const uint32_t x = 2 * (it - 1) + 1;             // V of the block before
-                    const uint32_t vs = kFp8 ? (it - 1) & 1 : x % kRingBf16, ks = kFp8 ? it % kRingK : (2 * it) % kRingBf16;
+                    const uint32_t vs = kFp8 ? (it - 1) & 1 : (2 * it - 1) % kRingBf16, ks = kFp8 ? it % kRingK : (2 * it) % kRingBf16;
                     if (j > 0) {
-                        if (j - 1 >= edge) {
-                            good = wait(bar(GE + edges % kUnclean), edges / kUnclean);
-                            ++edges;
-                        } else {
-                            good = kFp8 ? wait(bar(VF + vs), (it - 1) >> 1) : wait(bar(TF + vs), x / kRingBf16);
-                        }
-                        if (!good || !(good = wait(bar(PF), phase0++))) break;
+                        // the first half's weights, V of this block and K of the next
+                        if (!(good = wait(bar(PF), phase0++))) break;
                         tc_fence_after();
                         issue_o(0, vs, j > 1);
                         if (j == count) tc_commit(bar(OF));
                     }
-                    if (j < count) {
-                        if (!(good = kFp8 ? wait(bar(TF + ks), it / kRingK) : wait(bar(TF + ks), 2 * it / kRingBf16))) break;
-                        tc_fence_after();
-                        issue_s(0, ks);
-                        if (j + 1 == count) tc_commit(bar(QE));
-                    }
+                    if (j < count) issue_s(0, ks);
                     if (j > 0) {
                         if (two) {
                             if (!(good = wait(bar(PF + 1), phase1++))) break;
@@ -387,51 +412,49 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                         tc_commit(bar((kFp8 ? VE : TE) + vs));
                     }
                     if (j < count) {
-                        if (two) {
-                            issue_s(1, ks);
-                            if (j + 1 == count) tc_commit(bar(QE + 1));
-                        }
+                        if (two) issue_s(1, ks);
                         tc_commit(bar(TE + ks));
                         ++it;
                     }
                 }
                 if (!good) break;
             }
-            if (ld_shared_volatile(wait.abort)) {        // every product issued is done before the block leaves
+            if (ld_shared_volatile(wait.abort)) {        // products issued and copies armed are done before the block leaves
                 tc_commit(bar(DR));
                 mbar_wait_drain(bar(DR), 0);
+                if (items0) mbar_wait_drain(bar(QF), (items0 - 1) & 1);
+                if (items1) mbar_wait_drain(bar(QF + 1), (items1 - 1) & 1);
             }
         } else if (warp == 2 && lane == 0) {
-            // ================= queries =================
-            uint32_t items[2] = {0, 0};
+            // ================= what the issuer need not wait for itself =================
+            // A wait costs it 150 to 250 clocks even where nothing is waited for.  So this thread
+            // follows the tiles, in their order, and arrives with the first half's weights.
+            uint32_t it = 0, edges = 0;
             for (int k = 0;; ++k) {
                 const int b = k & 1;
                 if (!wait(bar(MF + b), k >> 1)) break;
                 const Item &item = ctl.item[b];
                 if (!item.live) break;
-                const int i0 = 2 * a.half * item.tile, count = item.c1 - item.c0;
-                bool good = true;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (count == 0 || item.rows - i0 <= t * a.half) continue;
-                    // the products of the item before are done with their queries
-                    if (good && items[t]) good = wait(bar(QE + t), items[t] - 1);
-                    if (!good) continue;
-                    const int row = item.row0 + i0 + t * a.half;
-                    const int boxes = kFp8 && a.q_scale ? 1 : 2;     // bf16: 64 dims each; e4m3: a term each
-                    mbar_expect_tx(bar(QF + t), boxes * a.half * a.g * 128);
-                    for (int x = 0; x < boxes; ++x)
-                        tma_load_3d(base + kSmemQ + t * kTile + x * kHalf, &map_q, bar(QF + t), kFp8 ? 0 : 64 * x, item.kv * a.g,
-                                    row + (kFp8 ? x * a.total_q : 0));
-                    ++items[t];
+                const int count = item.c1 - item.c0, edge = kFp8 ? INT_MAX : item.edge - item.c0;
+                const auto keys = [&](uint32_t i) {
+                    return kFp8 ? wait(bar(TF + i % kRingK), i / kRingK) : wait(bar(TF + 2 * i % kRingBf16), 2 * i / kRingBf16);
+                };
+                bool good = true;                        // the item's first K is the issuer's to wait for
+                for (int j = 0; j < count && good; ++j, ++it) {
+                    const uint32_t x = 2 * it + 1;
+                    if (j >= edge) {
+                        good = wait(bar(GE + edges % kUnclean), edges / kUnclean);
+                        ++edges;
+                    } else {
+                        good = kFp8 ? wait(bar(VF + (it & 1)), it >> 1) : wait(bar(TF + x % kRingBf16), x / kRingBf16);
+                    }
+                    if (good && j + 1 < count) good = keys(it + 1);
+                    if (good && it) good = wait(bar(PF), it - 1);        // one arrival a phase
+                    if (good) mbar_arrive(bar(PF));
                 }
-                mbar_arrive(bar(ME + b));
                 if (!good) break;
+                mbar_arrive(bar(ME + b));
             }
-            if (ld_shared_volatile(wait.abort))
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (items[t]) mbar_wait_drain(bar(QF + t), (items[t] - 1) & 1);
         } else if (warp == 3) {
             // ================= keys and values =================
             const int box = a.c.page_size < kBlock ? a.c.page_size : kBlock, boxes = kBlock / box;     // rows of one; boxes of a block
