@@ -664,7 +664,7 @@ cudaError_t launch(const PAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     if (e != cudaSuccess) return e;
     if ((e = launch_chained(columns_kernel<kFp8, NT>, blocks, kThreads, smem, st, a, sc)) != cudaSuccess) return e;
     if (a.whole) return cudaSuccess;
-    return launch_chained(join_kernel<InOrder<8 * NT>, 8 * NT, most_blocks<kFp8>(), PAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0,
+    return launch_chained(join_kernel<NT, most_blocks<kFp8>(), PAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0,
                           st, a, sc, blocks);
 }
 

@@ -122,6 +122,7 @@ struct Tiles {
 __device__ __forceinline__ Tiles tiles_in(const PAttn &a, const Request &q) {
     Tiles t;
     t.n = (long long)q.rows * a.g > a.most_columns ? (q.rows + 2 * a.half - 1) / (2 * a.half) : 0;
+    if (q.len == 0 && t.n) t.n = 1;              // zeros for all its rows, as one item
     t.start = q.len - q.lq;
     // a start past 2^27 counts as that: sums of weights stay in 64 bits
     t.base = kItemKeys + min(max(t.start, 0), 1 << 27);
@@ -196,32 +197,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     const uint32_t base = smem_u32(smem), bars = smem_u32(ctl.bars);
     const auto bar = [&](int k) { return bars + 8u * (uint32_t)k; };
     const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
-    after_previous();
-
-    // -- this block's range of units ------------------------------------------------
-    const int each = (a.batch + kTilesThreads - 1) / kTilesThreads;
-    Request q = {0, 0, 0, 0};
-    long long n = 0, total;
-    for (int r = tid * each; r < min(a.batch, (tid + 1) * each); ++r) n += units_of(a, tiles_in(a, q = request_of(a, r)));
-    long long low = scan_all(n, &total, ctl.sums);
-    const long long want = total / (kBlock * kMinBlocks) + 1;
-    const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
-    if (tid == 0) sc.open[blockIdx.x].parts = 0;
-    if ((int)blockIdx.x >= blocks) return;
-    const long long share = quotient(total, blocks);
-    const int longer = (int)(total - share * blocks);
-    const long long first = blockIdx.x * share + min((int)blockIdx.x, longer), end = first + share + ((int)blockIdx.x < longer);
-    if (low <= first && first < low + n) {
-        int r = tid * each;
-        if (each > 1)
-            for (;; ++r) {
-                n = units_of(a, tiles_in(a, request_of(a, r)));
-                if (first < low + n || r + 1 == a.batch) break;
-                low += n;
-            }
-        ctl.r = r;
-        ctl.at = low;
-    }
+    // barriers and TMEM while the kernel before ends
     if (tid == 0) {
         for (int k = 0; k < kBars; ++k) {
             uint32_t count = 1;
@@ -239,6 +215,36 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     if (warp == 0) {
         tmem_alloc(smem_u32(&ctl.tmem), 512);
         tmem_relinquish();
+    }
+    after_previous();
+
+    // -- this block's range of units ------------------------------------------------
+    const int each = (a.batch + kTilesThreads - 1) / kTilesThreads;
+    Request q = {0, 0, 0, 0};
+    long long n = 0, total;
+    for (int r = tid * each; r < min(a.batch, (tid + 1) * each); ++r) n += units_of(a, tiles_in(a, q = request_of(a, r)));
+    long long low = scan_all(n, &total, ctl.sums);
+    const long long want = total / (kBlock * kMinBlocks) + 1;
+    const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
+    if (tid == 0) sc.open[blockIdx.x].parts = 0;
+    if ((int)blockIdx.x >= blocks) {
+        __syncthreads();
+        if (warp == 0) tmem_dealloc(ctl.tmem, 512);
+        return;
+    }
+    const long long share = quotient(total, blocks);
+    const int longer = (int)(total - share * blocks);
+    const long long first = blockIdx.x * share + min((int)blockIdx.x, longer), end = first + share + ((int)blockIdx.x < longer);
+    if (low <= first && first < low + n) {
+        int r = tid * each;
+        if (each > 1)
+            for (;; ++r) {
+                n = units_of(a, tiles_in(a, request_of(a, r)));
+                if (first < low + n || r + 1 == a.batch) break;
+                low += n;
+            }
+        ctl.r = r;
+        ctl.at = low;
     }
     tc_fence_before();
     __syncthreads();
@@ -665,7 +671,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             if (!item.live) break;
             const int i0 = 2 * a.half * item.tile + t * a.half, i = i0 + own, head = item.kv * a.g + row - own * a.g;
             const bool valid = own < a.half && i < item.rows;
-            if (item.rows <= i0) {                       // no row in this half
+            if (item.len && item.rows <= i0) {           // no row in this half
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ME + b));
                 continue;
@@ -768,9 +774,18 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             const float v_scale = kFp8 ? __ldg(a.v_scale + item.kv) : 1.f;
             const float by = !whole ? v_scale : l == 0.f ? 0.f : v_scale / l;
             const int not_finite = *reinterpret_cast<const volatile int *>(&item.not_finite);
-            const long long slot = ((long long)blockIdx.x * 2 + (item.opens ? 1 : 0)) * kRows + t * kBlock + row;
+            const long long slot = (long long)blockIdx.x * 2 + (item.opens ? 1 : 0);
+            if (item.len == 0) {                         // all rows of the request: half a warp each
+                const int lane16 = lane & 15, from = 2 * (warp - 8) + (lane >> 4);
+                for (int r = from; r < item.rows * a.g; r += 16) {
+                    const int j = r / item.rows, at = item.row0 + r - j * item.rows, h = item.kv * a.g + j;
+                    reinterpret_cast<uint4 *>(a.out + ((long long)at * a.h_q + h) * kHeadDim)[lane16] = make_uint4(0, 0, 0, 0);
+                    if (a.lse && lane16 == 0) a.lse[(long long)h * a.total_q + at] = -INFINITY;
+                }
+            }
+            const unsigned long long mine = valid ? (unsigned long long)(a.out + (out_row * a.h_q + head) * kHeadDim) : 0;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 4 && item.len; ++c) {
                 uint32_t o[32];
                 if (count > 0) {
                     tmem_ld32(o_at + c * 32, o);
@@ -786,23 +801,38 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (item.from[32 * c + e] < keys) o[e] = 0x7fffffffu;
-                if (!valid) continue;
                 if (whole) {
-                    uint4 *to = reinterpret_cast<uint4 *>(a.out + (out_row * a.h_q + head) * kHeadDim + 32 * c);
+                    // 64 bytes of a row each: four lanes swap pieces, so that they write a row together
+                    // and not 16 bytes of a row of their own each
+                    uint32_t w[4][4];                    // [piece][word]
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        to[e] = make_uint4(pack16<false>(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                                           pack16<false>(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                                           pack16<false>(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                                           pack16<false>(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-                } else {
-                    uint4 *to = reinterpret_cast<uint4 *>(sc.o + slot * kHeadDim + 32 * c);
+                    for (int e = 0; e < 16; ++e) w[e / 4][e % 4] = pack16<false>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int d = 1; d <= 2; d *= 2) {
+                        const bool up = lane & d;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            if (x & d) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t got = __shfl_xor_sync(~0u, up ? w[x][e] : w[x | d][e], d);
+                                if (up) w[x][e] = got; else w[x | d][e] = got;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {        // piece lane % 4 of the row of lane (lane & ~3) + x
+                        const unsigned long long to = __shfl_sync(~0u, mine, (lane & ~3) + x);
+                        if (to) reinterpret_cast<uint4 *>(to)[4 * c + (lane & 3)] = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                    }
+                } else {                                 // [4 dims][row], rows side by side
+                    uint4 *to = reinterpret_cast<uint4 *>(sc.o) + (slot * 32 + 8 * c) * kRows + t * kBlock + row;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e * kRows] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
-            if (valid && !whole) sc.ml[slot] = make_float2(m, l);
-            else if (valid && a.lse) a.lse[(long long)head * a.total_q + out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (!whole) sc.ml[slot * kRows + t * kBlock + row] = make_float2(m, l);
+            else if (valid && a.lse && item.len) a.lse[(long long)head * a.total_q + out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             // the next item's first product over O follows its weights, which follow these reads
             tc_fence_before();
             __syncwarp();
@@ -906,16 +936,100 @@ int tiles_blocks(const PAttn &a) {
     return blocks < kSm ? (int)blocks : kSm;
 }
 
-// Where the join's rows are: a tile's halves hold whole queries.
-struct HalfRows {
-    template <typename A>
-    static __device__ __forceinline__ bool place(const A &a, int tile, int col, int &i, int &j) {
-        const int row = col & (kBlock - 1), own = row / a.g;
-        i = (2 * tile + col / kBlock) * a.half + own;
-        j = row - own * a.g;
-        return own < a.half;
+// Joins the parts of the items that several blocks share: part 0 in the first block's second
+// slot, the others in the first slots of the blocks behind it.  A task is 8 rows of an open
+// item; a lane has every fourth piece of 4 dims of one.  Where there are few tasks a block
+// takes one, its warps a share of the parts each; else a warp does.
+__global__ void __launch_bounds__(kJoinWarps * 32) tiles_join_kernel(PAttn a, Scratch sc, int blocks) {
+    __shared__ Open list[kSm];
+    __shared__ int first[kSm];
+    __shared__ int opens_in[kJoinWarps];
+    __shared__ float4 part_o[kJoinWarps][8][32];
+    __shared__ float part_l[kJoinWarps][32];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    after_previous();
+    let_next();
+    static_assert(kSm <= kJoinWarps * 32, "a thread for each block");
+    Open rec;
+    rec.parts = 0;
+    if ((int)threadIdx.x < blocks) rec = sc.open[threadIdx.x];
+    const unsigned vote = __ballot_sync(~0u, rec.parts > 0);
+    if (lane == 0) opens_in[warp] = __popc(vote);
+    __syncthreads();
+    int opens = 0, at = __popc(vote & ((1u << lane) - 1));
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (w < warp) at += opens_in[w];
+        opens += opens_in[w];
     }
-};
+    if (rec.parts > 0) {
+        list[at] = rec;
+        first[at] = threadIdx.x;
+    }
+    __syncthreads();
+    const int tasks = opens * (kRows / 8), row8 = lane & 7, piece0 = lane >> 3;
+    const bool wide = tasks <= (int)gridDim.x;
+    const int step = wide ? 1 : kJoinWarps;
+    for (int task0 = blockIdx.x * step; task0 < tasks; task0 += gridDim.x * step) {
+        const int task = task0 + (wide ? 0 : warp);
+        const bool live = task < tasks;
+        const Open it = list[live ? task / (kRows / 8) : 0];
+        const int b = first[live ? task / (kRows / 8) : 0], row = task % (kRows / 8) * 8 + row8;
+        const int in_half = row & (kBlock - 1), own = in_half / a.g, i = (2 * it.tile + row / kBlock) * a.half + own;
+        const bool there = live && own < a.half && i < it.rows;
+        float top = -INFINITY, l = 0.f;
+        float4 o[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (__any_sync(~0u, there)) {
+            const auto slot = [&](int p) { return (long long)(b + p) * 2 + (p == 0); };
+            for (int p = piece0; p < it.parts; p += 4) top = fmaxf(top, sc.ml[slot(p) * kRows + row].x);
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+            for (int p = wide ? warp : 0; p < it.parts; p += wide ? kJoinWarps : 1) {
+                const float2 e = sc.ml[slot(p) * kRows + row];
+                const float4 *from = reinterpret_cast<const float4 *>(sc.o) + (slot(p) * 32 + piece0) * kRows + row;
+                float4 v[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) v[x] = from[4 * x * kRows];
+                const float f = e.x == -INFINITY ? 0.f : exp2f(e.x - top);
+                l += e.x == -INFINITY ? e.y : f * e.y;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    o[x].x = fmaf(f, v[x].x, o[x].x);
+                    o[x].y = fmaf(f, v[x].y, o[x].y);
+                    o[x].z = fmaf(f, v[x].z, o[x].z);
+                    o[x].w = fmaf(f, v[x].w, o[x].w);
+                }
+            }
+        }
+        if (wide) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) part_o[warp][x][lane] = o[x];
+            part_l[warp][lane] = l;
+            __syncthreads();
+            if (warp == 0)
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    l += part_l[w][lane];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 v = part_o[w][x][lane];
+                        o[x].x += v.x, o[x].y += v.y, o[x].z += v.z, o[x].w += v.w;
+                    }
+                }
+        }
+        if (there && !(wide && warp)) {
+            const int head = it.kv * a.g + in_half - own * a.g;
+            const long long out_row = it.row0 + i;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint2 *to = reinterpret_cast<uint2 *>(a.out + (out_row * a.h_q + head) * kHeadDim) + piece0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                to[4 * x] = make_uint2(pack16<false>(o[x].x * inv, o[x].y * inv), pack16<false>(o[x].z * inv, o[x].w * inv));
+            if (a.lse && piece0 == 0) a.lse[(long long)head * a.total_q + out_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+        }
+        if (wide) __syncthreads();
+    }
+}
 
 // Bytes that queries of another type take (queries_kernel).
 size_t converted_bytes(const PAttn &a) {
@@ -972,7 +1086,7 @@ cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long l
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
     if ((e = launch_chained(kernel, (unsigned)n, kTilesThreads, kSmem, st, a, sc, map_q, map_k, map_v, limit_ns)) != cudaSuccess)
         return e;
-    return launch_chained(join_kernel<HalfRows, kRows, kSm, PAttn>, (unsigned)n * 8, kJoinWarps * 32, 0, st, a, sc, (int)n);
+    return launch_chained(tiles_join_kernel, (unsigned)n * 4, kJoinWarps * 32, 0, st, a, sc, (int)n);
 }
 
 }  // namespace fp

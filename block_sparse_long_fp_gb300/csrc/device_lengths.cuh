@@ -122,21 +122,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // takes a task, its warps a share of the parts each; else a warp does.
 constexpr int kJoinWarps = 8;
 
-// Columns of a tile in order: query after query, the g heads of each together.
-template <int kCols>
-struct InOrder {
-    template <typename A>
-    static __device__ __forceinline__ bool place(const A &a, int tile, int col, int &i, int &j) {
-        const int cc = tile * kCols + col;
-        i = cc / a.g;
-        j = cc - i * a.g;
-        return true;
-    }
-};
-
-// Place: a column's query of the request and head of the group.  kMost: blocks at most.
-template <typename Place, int kCols, int kMost, typename A>
+// kMost: blocks at most.
+template <int NT, int kMost, typename A>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(A a, Scratch sc, int blocks) {
+    constexpr int kCols = 8 * NT;
     constexpr int kEach = (kMost + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
     __shared__ Open list[kMost];
     __shared__ int first[kMost], count[kEach][kJoinWarps];
@@ -181,12 +170,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(A a, Scratch sc, 
         const bool live = task < opens * kCols;
         const int b = first[live ? task / kCols : 0], col = task % kCols;
         const Open it = list[live ? task / kCols : 0];
-        int i, j;
-        const bool there = Place::place(a, it.tile, col, i, j);
-        const int head = it.kv * a.g + j;
+        const int cc = it.tile * kCols + col, i = cc / a.g, head = it.kv * a.g + cc % a.g;
         float top = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live && there && i < it.rows) {
+        if (live && i < it.rows) {
             const auto slot = [&](int p) { return ((long long)(b + p) * 2 + (p == 0)) * kCols + col; };
             for (int p = lane; p < it.parts; p += 32) top = fmaxf(top, sc.ml[slot(p)].x);
 #pragma unroll
@@ -208,7 +195,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(A a, Scratch sc, 
             part_o[warp][lane] = o;
             if (lane == 0) part_l[warp] = l;
             __syncthreads();
-            if (warp == 0 && there && i < it.rows) {
+            if (warp == 0 && i < it.rows) {
                 for (int w = 1; w < kJoinWarps; ++w) {
                     const float4 v = part_o[w][lane];
                     l += part_l[w];

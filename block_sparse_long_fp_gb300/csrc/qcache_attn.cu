@@ -808,7 +808,7 @@ cudaError_t launch(const QAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     if (e != cudaSuccess) return e;
     if ((e = launch_chained(attn_kernel<NG, NT>, blocks, kThreads, smem, st, a, sc)) != cudaSuccess) return e;
     if (a.whole) return cudaSuccess;
-    return launch_chained(join_kernel<InOrder<8 * NT>, 8 * NT, kSm * blocks_per_sm<1>(), QAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0, st, a, sc, blocks);
+    return launch_chained(join_kernel<NT, kSm * blocks_per_sm<1>(), QAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0, st, a, sc, blocks);
 }
 
 template <int NT>

@@ -431,7 +431,7 @@ def check_attn(s, got, lse, scale=None, rows=None):
     none = np.isneginf(want_lse[:, :n])
     assert np.array_equal(np.isneginf(lse), none)
     assert not got[none.T].any()
-    assert np.all(np.abs(lse - want_lse[:, :n])[~none] <= lse_tol[:, :n][~none])
+    assert np.all(np.abs(lse[~none] - want_lse[:, :n][~none]) <= lse_tol[:, :n][~none])
 
 
 def run_attn(s, max_q=None, **kw):
@@ -670,6 +670,18 @@ def test_attn_of_many_rows(fp, reqs, h_q, h, page, dtype, q_dtype):
     check_attn(s, out, lse)
     again, lse2 = run_attn(s)
     assert bool((again == out).all()) and bool((lse2 == lse).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_of_many_rows_without_keys(fp, dtype):
+    """Requests that left the batch (all rows), and rows before the first key, of one half of a tile and of more."""
+    for reqs in ([(0, 40)], [(0, 500), (700, 90), (0, 33)], [(30, 400), (1, 300), (0, 129)], [(0, 70)] * 5):
+        s = attn_case(fp, reqs, 10, 2, 32, dtype, "bf16", seed=len(reqs))
+        out, lse = run_attn(s)
+        check_attn(s, out, lse)
+        if len({m for _, m in reqs}) == 1:
+            check_attn(s, *s["c"].attn(s["q"], i32(s["table"]), i32(s["lens"])))
+        assert s["c"].device_status() == 0
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
