@@ -676,14 +676,15 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 if (lane == 0) mbar_arrive(bar(ME + b));
                 continue;
             }
-            const int keys = valid ? max(0, min(item.len, item.len - item.lq + i + 1)) : 0;
+            // a row that is none attends all with logits of 0, whatever its queries' place holds: masking it would
+            // cost its warp the masks of every block
+            const int keys = valid ? max(0, min(item.len, item.len - item.lq + i + 1)) : INT_MAX;
             const long long out_row = item.row0 + i;
             float cs = a.scale * kLog2e;                             // base-2 logits
             if (kFp8) cs *= __ldg(a.k_scale + item.kv);
-            if (valid) {
-                if (a.q_scale) cs *= __ldg(a.q_scale + head);
-                else if (kFp8) cs *= pow2f(-a.q_exponent[out_row * a.h_q + head]);
-            }
+            if (!valid) cs = 0.f;
+            else if (a.q_scale) cs *= __ldg(a.q_scale + head);
+            else if (kFp8) cs *= pow2f(-a.q_exponent[out_row * a.h_q + head]);
             const int count = item.c1 - item.c0, key0 = item.c0 * kBlock;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
