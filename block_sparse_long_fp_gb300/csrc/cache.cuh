@@ -1,6 +1,8 @@
 // The bf16 / e4m3 paged K/V cache and rotary positions as their kernels see them.
 #pragma once
 
+#include <atomic>
+
 #include "qcache.cuh"
 
 namespace fp {
@@ -67,5 +69,27 @@ size_t cache_tiles_scratch_bytes(const PAttn &a);
 cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long limit_ns, cudaStream_t st);
 // the limit of bounded waits (fp_set_wait_limit_ns)
 unsigned long long wait_limit_ns();
+
+// A launch with more shared memory than the default limit, which a kernel is given once on
+// each device (it takes as long as the launch).  A device that was reset since is told again.
+template <typename... P, typename... A>
+cudaError_t launch_large(std::atomic<unsigned long long> &told, void (*kernel)(P...), unsigned grid, unsigned block, int smem,
+                         cudaStream_t st, A... args) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = device < 64 ? 1ull << device : 0;
+    const bool known = told.load(std::memory_order_relaxed) & bit;
+    for (int attempt = known ? 0 : 1; attempt < 2; ++attempt) {
+        if (attempt) {
+            if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+            told.fetch_or(bit, std::memory_order_relaxed);
+        }
+        e = launch_chained(kernel, grid, block, (size_t)smem, st, args...);
+        if (e != cudaErrorInvalidValue || attempt) return e;
+        cudaGetLastError();
+    }
+    return e;
+}
 
 }  // namespace fp

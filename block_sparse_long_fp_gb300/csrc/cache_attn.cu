@@ -6,8 +6,10 @@
 // K and V^T fragments come out of shared memory by ldmatrix, and the weights become the
 // second product's operand by an 8 x 8 transpose in registers.
 // A bf16 cache takes bf16 operands: queries as they are (e4m3 ones exactly), weights rounded
-// to bf16 (2^-8 of each).  e4m3 codes become fp16, exactly, in registers; queries fp16 under
-// a power of two per row (exact within 2^-29 of the row's largest), weights fp16 (2^-11).
+// to bf16 (2^-8 of each).  Of an e4m3 cache K's codes are multiplied as they are (m16n8k32),
+// with e4m3 queries, or with bf16 ones under a power of two as two e4m3 terms of 4 bits each,
+// which hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it;
+// V's become fp16, exactly, in registers, weights fp16 (2^-11).
 // For V^T two keys of a dim have to meet in a register: the 16-bit transpose brings two dims
 // of two keys, which a byte permutation sorts, and a tile's rows stand for even, then odd dims.
 //
@@ -65,6 +67,13 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 32 dims of e4m3 codes: a register holds four, as ldmatrix brings them.
+__device__ __forceinline__ void mma32(float c[4], const uint32_t a[4], uint2 b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
 __device__ __forceinline__ void load4(uint32_t r[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -97,8 +106,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return ((w & 0x7fff7fffu) + (kFp8 ? 0x04000400u : 0x00800080u)) & 0x80008000u;
 }
 
-// What one lane holds of 8 columns: queries as B fragments of 8 steps of 16 dims, and what a
-// column's products have to be scaled by to be base-2 logits.
+// What one lane holds of 8 columns: queries as B fragments of 8 steps of 16 dims -- for an e4m3
+// cache of 4 steps of 32, and the second terms' behind them -- and what a column's products have
+// to be scaled by to be base-2 logits.
 struct Queries {
     uint2 f[8];
     float factor;              // of column lane / 4
@@ -149,17 +159,18 @@ __device__ __forceinline__ RawQuery fetch_query(const PAttn &a, const Request &q
 template <bool kFp8>
 __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Queries &out) {
     out.factor = raw.scale;
-    if (e4m3) {
+    if (kFp8 && e4m3) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) out.f[s] = make_uint2(raw.w[2 * s].x, raw.w[2 * s + 1].x);
+    } else if (e4m3) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            uint32_t b[2] = {kFp8 ? halves_of(raw.w[s].x) : halves_of(raw.w[s].x),
-                             kFp8 ? halves_of(raw.w[s].x >> 16) : halves_of(raw.w[s].y)};
-            if (!kFp8)
+            uint32_t b[2] = {halves_of(raw.w[s].x), halves_of(raw.w[s].y)};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&b[e]));
-                    b[e] = pack_pair<false>(v.x, v.y);
-                }
+            for (int e = 0; e < 2; ++e) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&b[e]));
+                b[e] = pack_pair<false>(v.x, v.y);
+            }
             out.f[s] = make_uint2(b[0], b[1]);
         }
     } else if (!kFp8) {
@@ -176,17 +187,23 @@ __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Que
             }
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const int ex = fp16_scale_exp(__float_as_uint(top));
+        const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
         const float up = pow2f(ex);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            uint32_t b[2];
+            uint32_t term[2] = {0, 0};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t w = e ? raw.w[s].y : raw.w[s].x;
-                b[e] = pack_pair<true>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                const float x = __uint_as_float(w << 16) * up, y = __uint_as_float(w & 0xffff0000u) * up;
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3), back = halves_of(hi);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x - v.x, y - v.y), __NV_SATFINITE, __NV_E4M3);
+                term[0] |= hi << 16 * e;
+                term[1] |= lo << 16 * e;
             }
-            out.f[s] = make_uint2(b[0], b[1]);
+            (s & 1 ? out.f[s / 2].y : out.f[s / 2].x) = term[0];
+            (s & 1 ? out.f[4 + s / 2].y : out.f[4 + s / 2].x) = term[1];
         }
         out.factor *= pow2f(-ex);
     }
@@ -268,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
     const long long pitch = (long long)a.c.h_kv * kRow;               // bytes from token to token
     // A row's 16-byte pieces lie in shared memory at their number XOR the row's (mod 8), so that the
     // eight rows of a matrix are in eight groups of banks.  Rows are copied kRowsAt at a time.
+    const bool terms = a.q_scale == nullptr;      // e4m3 cache: two of each query
     const int copy_row = lane / kRowLanes, copy_piece = lane % kRowLanes;
     const uint32_t copy_at = copy_row * kRow + ((copy_piece ^ copy_row) << 4);
     // Matrices of a load: K rows 0-7 and 8-15 of one piece, then of the next; V (transposed) for bf16
@@ -413,19 +431,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
                 uint32_t w[4];
                 load4(w, (chunk + k_lane) ^ (s << 5));
 #pragma unroll
-                for (int u = 0; u < (kFp8 ? 2 : 1); ++u) {
-                    uint32_t k[4] = {w[0], w[1], w[2], w[3]};
-                    const int ks = kFp8 ? 2 * s + u : s;
+                for (int t = 0; t < L; ++t) {
+                    const auto query = [&](int i) { return kSharedQ ? s_frag[t][i][lane] : qs[kSharedQ ? 0 : t].f[i]; };
+                    float *sums = x[kChains == 2 ? s & 1 : t];
                     if (kFp8) {
-                        k[0] = halves_of(w[2 * u]);
-                        k[1] = halves_of(w[2 * u + 1]);
-                        k[2] = halves_of(w[2 * u] >> 16);
-                        k[3] = halves_of(w[2 * u + 1] >> 16);
-                    }
-#pragma unroll
-                    for (int t = 0; t < L; ++t) {
-                        const uint2 f = kSharedQ ? s_frag[t][ks][lane] : qs[kSharedQ ? 0 : t].f[ks];
-                        mma16<kFp8>(x[kChains == 2 ? ks & 1 : t], k, f.x, f.y);
+                        mma32(sums, w, query(s));
+                        if (terms) mma32(sums, w, query(4 + s));
+                    } else {
+                        const uint2 f = query(s);
+                        mma16<false>(sums, w, f.x, f.y);
                     }
                 }
             }
@@ -660,9 +674,9 @@ cudaError_t launch(const PAttn &a, const Scratch &sc, int blocks, cudaStream_t s
     constexpr int ring = stages<kFp8, NT>() * chunk_bytes<kFp8>(), smem = kWarps * ring + 256;
     static_assert(ring >= 8 * NT * kOutStride * 4, "a warp's result fits its ring");
     static_assert(ring % 256 == 0, "rings stay aligned");
-    cudaError_t e = cudaFuncSetAttribute(columns_kernel<kFp8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> told{0};
+    const cudaError_t e = launch_large(told, columns_kernel<kFp8, NT>, blocks, kThreads, smem, st, a, sc);
     if (e != cudaSuccess) return e;
-    if ((e = launch_chained(columns_kernel<kFp8, NT>, blocks, kThreads, smem, st, a, sc)) != cudaSuccess) return e;
     if (a.whole) return cudaSuccess;
     return launch_chained(join_kernel<NT, most_blocks<kFp8>(), PAttn>, blocks < 2 * kSm ? blocks : 2 * kSm, kJoinWarps * 32, 0,
                           st, a, sc, blocks);

@@ -126,6 +126,7 @@ __device__ __forceinline__ Tiles tiles_in(const PAttn &a, const Request &q) {
     t.start = q.len - q.lq;
     // a start past 2^27 counts as that: sums of weights stay in 64 bits
     t.base = kItemKeys + min(max(t.start, 0), 1 << 27);
+    if (q.len == 0) t.base += (long long)q.rows * a.g / 4;
     return t;
 }
 __device__ __forceinline__ long long units_before(const PAttn &a, const Tiles &t, long long tile) {
@@ -778,6 +779,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             const long long slot = (long long)blockIdx.x * 2 + (item.opens ? 1 : 0);
             if (item.len == 0) {                         // all rows of the request: half a warp each
                 const int lane16 = lane & 15, from = 2 * (warp - 8) + (lane >> 4);
+#pragma unroll 4
                 for (int r = from; r < item.rows * a.g; r += 16) {
                     const int j = r / item.rows, at = item.row0 + r - j * item.rows, h = item.kv * a.g + j;
                     reinterpret_cast<uint4 *>(a.out + ((long long)at * a.h_q + h) * kHeadDim)[lane16] = make_uint4(0, 0, 0, 0);
@@ -1083,9 +1085,9 @@ cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long l
         !make_map(&map_k, c.k, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, true) ||
         !make_map(&map_v, c.v, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, !fp8))
         return cudaErrorInvalidValue;
-    const auto kernel = fp8 ? tiles_kernel<true> : tiles_kernel<false>;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
-    if ((e = launch_chained(kernel, (unsigned)n, kTilesThreads, kSmem, st, a, sc, map_q, map_k, map_v, limit_ns)) != cudaSuccess)
+    static std::atomic<unsigned long long> told[2];
+    if ((e = launch_large(told[fp8], fp8 ? tiles_kernel<true> : tiles_kernel<false>, (unsigned)n, kTilesThreads, kSmem, st, a, sc,
+                          map_q, map_k, map_v, limit_ns)) != cudaSuccess)
         return e;
     return launch_chained(tiles_join_kernel, (unsigned)n * 4, kJoinWarps * 32, 0, st, a, sc, (int)n);
 }
