@@ -32,11 +32,15 @@ namespace fp {
 namespace {
 
 constexpr int kMinChunks = 2 * kWarps;       // least work worth a thread block
-// What starting and ending an item costs, in chunks, and what a chunk costs by the octets in use.
+// What starting and ending an item costs, in chunks, and what a chunk costs by the octets in use
+// (bf16 more for its bytes, e4m3 for its instructions).  32 requests up to 8192 of 1 to 8 tokens
+// (32/8 heads), us with items of 8 + 2 octets, 16 + 4, 24 + 6 chunks: bf16 116, 101, 101; e4m3 of
+// 14 + 2, 28 + 4, 40 + 6: 123, 128, 134; with 1, 2, 4, 10 for a chunk without octets e4m3 131, 123,
+// 130, 137.
 template <bool kFp8, int NT>
-constexpr int item_chunks() { return (kFp8 ? 14 : 8) + 2 * NT; }
-template <int NT>
-__device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : 4 + octets; }
+constexpr int item_chunks() { return kFp8 ? 14 + 2 * NT : 16 + 4 * NT; }
+template <bool kFp8, int NT>
+__device__ __forceinline__ int chunk_units(int octets) { return NT == 1 ? 1 : (kFp8 ? 2 : 4) + octets; }
 // Longest cache, by the width of its table, that is not cut (one launch instead of two).
 constexpr int kWholeChunks = 64;
 
@@ -47,7 +51,7 @@ constexpr int chunk_bytes() { return 2 * kChunk * row_bytes<kFp8>(); }
 template <bool kFp8, int NT>
 constexpr int blocks_per_sm() { return NT == 1 && kFp8 ? 3 : 2; }
 template <bool kFp8, int NT>
-constexpr int stages() { return kFp8 ? (NT == 1 ? 4 : 6) : 3; }
+constexpr int stages() { return kFp8 && NT > 1 ? 6 : 3; }
 template <bool kFp8>
 constexpr int most_blocks() { return kSm * blocks_per_sm<kFp8, 1>(); }
 
@@ -236,14 +240,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
         const int tiles = tiles_of_columns(q);
         if (tiles == 0 || a.whole) return (long long)a.c.h_kv * tiles;
         return (long long)a.c.h_kv * (kItem + chunks_of(q)) *
-               ((tiles - 1) * chunk_units<NT>(NT) + chunk_units<NT>(octets_of(q, tiles - 1)));
+               ((tiles - 1) * chunk_units<kFp8, NT>(NT) + chunk_units<kFp8, NT>(octets_of(q, tiles - 1)));
     };
     const int each = (a.batch + kThreads - 1) / kThreads;      // requests a thread adds up
     Request q = {0, 0, 0, 0};
     long long n = 0, total;
     for (int r = tid * each; r < min(a.batch, (tid + 1) * each); ++r) n += units(q = request_of(a, r));
     long long low = block_scan(n, &total, warp_sums);
-    const long long want = a.whole ? total : total / (kMinChunks * chunk_units<NT>(NT)) + 1;
+    const long long want = a.whole ? total : total / (kMinChunks * chunk_units<kFp8, NT>(NT)) + 1;
     const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
     if (tid == 0 && !a.whole) sc.open[blockIdx.x].parts = 0;
     if ((int)blockIdx.x >= blocks) return;
@@ -270,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
     int tiles = tiles_of_columns(q), chunks = chunks_of(q);
     int kv, tile;                                 // of the current item
     {
-        const long long full = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<NT>(NT);
-        const long long last = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<NT>(octets_of(q, tiles - 1));
+        const long long full = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<kFp8, NT>(NT);
+        const long long last = a.whole ? 1 : (long long)(kItem + chunks) * chunk_units<kFp8, NT>(octets_of(q, tiles - 1));
         const long long head = (tiles - 1) * full + last;
         kv = (int)quotient(first - item0, head);
         item0 += kv * head;
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
             chunks = chunks_of(q);
             kv = tile = 0;
         }
-        const int octets = octets_of(q, tile), weight = chunk_units<NT>(octets);
+        const int octets = octets_of(q, tile), weight = chunk_units<kFp8, NT>(octets);
         const long long next = a.whole ? item0 + 1 : item0 + (long long)(kItem + chunks) * weight;
         const int c0 = a.whole ? 0 : max(0, (int)((uint32_t)(at - item0) / weight) - kItem);    // an item is below 2^31 units
         const int c1 = a.whole ? chunks : max(0, (int)((uint32_t)(min(end, next) - item0) / weight) - kItem);

@@ -20,7 +20,7 @@ namespace fp {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAhead = 3;                      // rows of a group whose loads are in flight together
+constexpr int kAhead = 2;                      // rows of a group whose loads are in flight together
 constexpr int kSm = 152;
 
 enum Layout { kHalf, kInterleaved, kScalar };  // kScalar: half layout, rot / 2 not a multiple of 8
@@ -53,13 +53,14 @@ __device__ __forceinline__ void store8(void *out, long long at, const float *x, 
         *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(out) + at) =
             make_uint2(e4m3_four(x, inv), e4m3_four(x + 4, inv));
     else
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at) =
-            make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+        __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at),
+            make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])));
 }
 
 template <Layout L>
 __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(RotateRows r, int shares) {
     __shared__ __align__(16) float s_cos[kWarps][64], s_sin[kWarps][64];
+    __shared__ __align__(16) __nv_bfloat16 s_row[L == kScalar ? kWarps * 4 : 1][kAhead][kHeadDim];
     after_previous();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, group = lane >> 3, l = lane & 7;
     const long long job = (long long)blockIdx.x * kWarps + warp;
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(RotateRows r, int s
     // first and second element of pair 8 l + e, and where the lane's two runs of 8 start
     const auto first = [&](int pair) { return pair < half ? pair : half + 2 * (pair - half) + half; };
     const auto second = [&](int pair) { return pair < half ? pair + half : half + 2 * (pair - half) + 1 + half; };
-    const int run0 = L == kInterleaved ? 8 * l : half > 8 * l ? 8 * l : 16 * l;
-    const int run1 = L == kInterleaved ? 8 * l + 64 : half > 8 * l ? 8 * l + half : 16 * l + 8;
+    const int run0 = L == kInterleaved ? 8 * l : L == kHalf && half > 8 * l ? 8 * l : 16 * l;
+    const int run1 = L == kInterleaved ? 8 * l + 64 : L == kHalf && half > 8 * l ? 8 * l + half : 16 * l + 8;
 
     long long slot = -1;
     if (r.slots) {
@@ -124,21 +125,31 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(RotateRows r, int s
         for (int i = 0; i < kAhead; ++i) {
             row[i] = row_of(h0 + 4 * i + group);
             if (row[i].part < 0) continue;
-            if (L != kScalar) {
-                w[i][0] = *reinterpret_cast<const uint4 *>(row[i].in + run0);
-                w[i][1] = *reinterpret_cast<const uint4 *>(row[i].in + run1);
+            w[i][0] = __ldcs(reinterpret_cast<const uint4 *>(row[i].in + run0));
+            w[i][1] = __ldcs(reinterpret_cast<const uint4 *>(row[i].in + run1));
+        }
+        // pairs that lie across the runs of 8 meet through shared memory
+        __nv_bfloat16 (*mine)[kHeadDim] = s_row[L == kScalar ? warp * 4 + group : 0];
+        if (L == kScalar) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (row[i].part < 0) continue;
+                *reinterpret_cast<uint4 *>(mine[i] + run0) = w[i][0];
+                *reinterpret_cast<uint4 *>(mine[i] + run1) = w[i][1];
             }
+            __syncwarp();
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (row[i].part < 0) continue;
             const RowsPart &p = row[i].part == 0 ? r.q : row[i].part == 1 ? r.k : r.v;
+            const bool live = row[i].part >= 0, fp8 = p.scale != nullptr;
+            if (L != kScalar && !live) continue;
             float x[8], y[8];
             if (L == kScalar) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] = __bfloat162float(row[i].in[first(8 * l + e)]);
-                    y[e] = __bfloat162float(row[i].in[second(8 * l + e)]);
+                    x[e] = __bfloat162float(mine[i][first(8 * l + e)]);
+                    y[e] = __bfloat162float(mine[i][second(8 * l + e)]);
                 }
             } else {
                 unpack8(w[i][0], x);
@@ -156,27 +167,37 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_kernel(RotateRows r, int s
                     }
                 }
             }
-            const bool fp8 = p.scale != nullptr;
-            const float inv = fp8 ? 1.f / p.scale[row[i].head] : 1.f;
+            const float inv = live && fp8 ? 1.f / p.scale[row[i].head] : 1.f;
             if (L != kScalar) {
                 store8(p.out, row[i].out + run0, x, fp8, inv);
                 store8(p.out, row[i].out + run1, y, fp8, inv);
             } else {
+                __syncwarp();                    // the row is read: its results take its place
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const long long a = row[i].out + first(8 * l + e), b = row[i].out + second(8 * l + e);
+                    const int a = first(8 * l + e), b = second(8 * l + e);
                     if (fp8) {
                         const __nv_fp8x2_storage_t z =
                             __nv_cvt_float2_to_fp8x2(make_float2(x[e] * inv, y[e] * inv), __NV_SATFINITE, __NV_E4M3);
-                        static_cast<unsigned char *>(p.out)[a] = (unsigned char)(z & 0xff);
-                        static_cast<unsigned char *>(p.out)[b] = (unsigned char)(z >> 8);
+                        reinterpret_cast<unsigned char *>(mine[i])[a] = (unsigned char)(z & 0xff);
+                        reinterpret_cast<unsigned char *>(mine[i])[b] = (unsigned char)(z >> 8);
                     } else {
-                        static_cast<__nv_bfloat16 *>(p.out)[a] = __float2bfloat16_rn(x[e]);
-                        static_cast<__nv_bfloat16 *>(p.out)[b] = __float2bfloat16_rn(y[e]);
+                        mine[i][a] = __float2bfloat16_rn(x[e]);
+                        mine[i][b] = __float2bfloat16_rn(y[e]);
                     }
+                }
+                __syncwarp();
+                const uint4 *from = reinterpret_cast<const uint4 *>(mine[i]);
+                if (live && fp8) {
+                    *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(p.out) + row[i].out + 16 * l) = from[l];
+                } else if (live) {
+                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + row[i].out) + 2 * l;
+                    to[0] = from[2 * l];
+                    to[1] = from[2 * l + 1];
                 }
             }
         }
+        if (L == kScalar) __syncwarp();
     }
 }
 
