@@ -638,9 +638,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
     }
 }
 
-// Requests of more columns go to the tiles of 256 rows.
-constexpr int kMostColumns = 64;
-bool with_tiles(const PAttn &a) { return a.g <= kBlock && (long long)a.max_q * a.g > kMostColumns; }
+// Short caches are not worth cutting: an item stays with one block, and the second launch
+// falls away.
+bool whole_items(const PAttn &a) { return (long long)a.max_pages * (a.c.page_size / kChunk) <= kWholeChunks; }
+
+// Columns up to which a request is worked on by columns, and not by tiles of 256 rows.  us by
+// columns / tiles, 32 requests up to 8192 (32/8 heads): 20 columns bf16 100 / 109, e4m3 98 / 112; 32
+// 105 / 109, 122 / 112; 64 (32/4 heads) 86 / 66, 152 / 73.  Short caches, which are not cut: 4 of 300
+// tokens with 128 columns 13 / 17.
+int most_columns(const PAttn &a) { return whole_items(a) ? 128 : a.k_scale ? 24 : 32; }
+bool with_tiles(const PAttn &a) { return a.g <= kBlock && (long long)a.max_q * a.g > most_columns(a); }
 bool with_columns(const PAttn &a) { return a.cu || !with_tiles(a); }
 
 // Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32;
@@ -668,10 +675,6 @@ int blocks_of(const PAttn &a) {
     const double chunks = items * ((double)a.max_pages * (a.c.page_size / kChunk) + 40);
     return chunks < (double)most * kMinChunks ? (int)(chunks / kMinChunks) + 1 : most;
 }
-
-// Short caches are not worth cutting: an item stays with one block, and the second launch
-// falls away.
-bool whole_items(const PAttn &a) { return (long long)a.max_pages * (a.c.page_size / kChunk) <= kWholeChunks; }
 
 template <bool kFp8, int NT>
 cudaError_t launch(const PAttn &a, const Scratch &sc, int blocks, cudaStream_t st) {
@@ -710,7 +713,7 @@ size_t cache_attn_scratch_bytes(const PAttn &args) {
 cudaError_t launch_cache_attn(const PAttn &args, void *scratch, unsigned long long limit_ns, cudaStream_t st) {
     PAttn a = args;
     a.whole = whole_items(a);
-    a.most_columns = with_tiles(a) ? (a.cu ? kMostColumns : 0) : INT_MAX;
+    a.most_columns = with_tiles(a) ? (a.cu ? most_columns(a) : 0) : INT_MAX;
     if (with_columns(a)) {
         const size_t n = blocks_of(a), cols = tile_columns(a);
         char *p = static_cast<char *>(scratch);

@@ -47,7 +47,7 @@ constexpr int kTilesThreads = 512, kTilesWarps = kTilesThreads / 32;
 constexpr int kRegsControl = 80, kRegsLoad = 80, kRegsSoftmax = 176;
 static_assert(kRegsControl + kRegsLoad + 2 * kRegsSoftmax <= 4 * 128, "register split");
 constexpr int kRows = 2 * kBlock;                // places of a tile's rows
-constexpr int kItemKeys = 384;                   // what an item's start and end cost, in keys
+constexpr int kItemKeys = 512;                   // what an item's start and end cost, in keys (256 to 1024: within 5 %)
 constexpr int kMinBlocks = 4;                    // least blocks of keys worth an SM
 constexpr int kTile = kBlock * kHeadDim * 2, kHalf = kTile / 2;      // bytes; a half: 64 dims
 constexpr int kSmemQ = 0, kSmemK = 2 * kTile;
