@@ -199,7 +199,9 @@ __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Que
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t w = e ? raw.w[s].y : raw.w[s].x;
-                const float x = __uint_as_float(w << 16) * up, y = __uint_as_float(w & 0xffff0000u) * up;
+                // an infinity becomes a NaN: e4m3 would take it for its largest value
+                const float u = __uint_as_float(w << 16), v0 = __uint_as_float(w & 0xffff0000u);
+                const float x = fmaf(u, up, u * 0.f), y = fmaf(v0, up, v0 * 0.f);
                 const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3), back = halves_of(hi);
                 const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&back));
                 const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x - v.x, y - v.y), __NV_SATFINITE, __NV_E4M3);

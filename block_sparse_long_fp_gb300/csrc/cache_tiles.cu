@@ -889,7 +889,8 @@ __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed 
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float u = x[2 * e] * up, y = x[2 * e + 1] * up;
+        // an infinity becomes a NaN: e4m3 would take it for its largest value
+        const float u = fmaf(x[2 * e], up, x[2 * e] * 0.f), y = fmaf(x[2 * e + 1], up, x[2 * e + 1] * 0.f);
         hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(u, y), __NV_SATFINITE, __NV_E4M3);
         const uint32_t back = codes_to_f16(hi[e]);
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));

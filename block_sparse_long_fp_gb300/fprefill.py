@@ -569,7 +569,7 @@ class _Cache(_OnDevice):
                 raise FprefillError(FP_ERR_INVALID, "lse: [h_q, total_q] wanted")
         elif want_lse:
             lse = torch.empty((h_q, total_q), dtype=self._fp32, device=self.device)
-        key = (batch, h_q, total_q, max_q, cu_at == 0, width)
+        key = (batch, h_q, total_q, max_q, cu_at == 0, width, q_scale is None)
         n = self._scratch_bytes.get(key)
         if n is None:
             if len(self._scratch_bytes) >= 512:        # a server's rows may take any number of shapes
@@ -741,6 +741,8 @@ class Rope(_OnDevice):
         _check(lib().fp_rope_turns(freq.ctypes.data, freq.size, turns.ctypes.data), "fp_rope_turns")
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         super().__init__(self.turns.device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()         # any stream may use it from here on
         self.rot, self.layout, self.scale = 2 * freq.size, layout, float(scale)
         self._t = FpRopeTable(self.rot, FP_ROPE_INTERLEAVED if layout == "interleaved" else FP_ROPE_HALF, self.scale,
                               _ptr(self.turns))

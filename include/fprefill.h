@@ -549,7 +549,7 @@ fp_status fp_rope_turns(const double *inv_freq, int n, unsigned long long *turns
  *   x (device bf16): row i, head h at  i * stride_tok + h * stride_head  elements (pointer
  *     and strides multiples of 16 bytes, stride_head >= 128, stride_tok >= stride_head *
  *     (heads - 1) + 128); out the same with its own strides, bf16, or e4m3 codes of
- *     value / out_scale[head] (times the scale's rounded reciprocal; saturated at 448).
+ *     value / out_scale[head] (times the positive scale's rounded reciprocal; saturated at 448).
  *   out may be x itself, with like strides and type; otherwise they do not overlap. */
 typedef struct {
     int rows;                         /* >= 0 */
@@ -573,7 +573,7 @@ fp_status fp_rope(const fp_rope_table *t, const fp_rope_rows *r, void *stream);
  *   Slots that no row names stay as they are.  With `rope`, k (and q) are rotated by
  *   positions[i].  q (may be NULL): every row i, whatever its slot, to row i of q_out, which
  *   may be q itself when both are bf16 with like strides.  bf16 in; out in the cache's type
- *   (q: q_dtype), rounded and scaled as fp_rope's. */
+ *   (q: q_dtype), rounded and scaled as fp_rope's.  Rows do not overlap the caches. */
 typedef struct {
     void *k, *v;                      /* DEVICE [num_pages, page_size, h_kv, d], 16-byte aligned */
     int num_pages, page_size;         /* page_size as above; num_pages * page_size <= 2^31 - 1 */
@@ -602,14 +602,19 @@ fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, cons
  *
  *   As fp_qcache_attn, over the bf16 values, or the e4m3 codes times their head's scales, of
  *   `c`: the same query structure, results, refusals, status and scratch rules (with
- *   fp_cache_attn_scratch_bytes()).  Queries are bf16 or e4m3, whatever the cache's type.
- *   Keys and values that a row does not attend may be anything.  In a value that a row
- *   attends, a NaN or an infinity makes that dim of the row one that is not finite; in a key,
- *   a NaN makes the row NaN.
+ *   fp_cache_attn_scratch_bytes(); a call enqueues up to five kernels).  Queries are bf16 or
+ *   e4m3, whatever the cache's type; scales are positive.
+ *   A NaN in a query makes its row NaN, and so does one in a key that the row attends; what an
+ *   infinity in either makes of the row is not defined.  In a value that a row attends, a NaN
+ *   or an infinity makes that dim of the row one that is not finite.  Other rows and dims are
+ *   what they would be without, and keys and values that a row does not attend may be
+ *   anything.  Finite values are below 2^100 in magnitude.
  *   Logits and sums are fp32.  Weights enter the sum of values in bf16 for a bf16 cache (half
  *   a step, 2^-9 of each), in fp16 for an e4m3 one (2^-12; nothing below 2^-34 of the row's
- *   largest), where bf16 queries enter as fp16 under a power of two of the row (nothing
- *   below 2^-39 of its largest). */
+ *   largest), where bf16 queries enter as two e4m3 terms under a power of two of the row
+ *   (exact down to 2^-10 of the row's largest element, the rest to 2^-18 of it).
+ *   Requests of many rows have bounded waits in their kernel, as the prefill's: one that runs
+ *   out records FP_ERR_TIMEOUT, and until fp_reset_status such requests are left unwritten. */
 size_t fp_cache_attn_scratch_bytes(const fp_cache *c, const fp_qcache_query *q);
 fp_status fp_cache_attn(const fp_cache *c, const fp_qcache_query *q, void *out, float *lse_opt, void *scratch,
                         size_t scratch_bytes, void *ws, size_t ws_bytes, void *stream);

@@ -773,3 +773,189 @@ def test_attn_of_many_rows_captured(fp, dtype):
         g.replay()
         check_attn(dict(s, lens=new), *out)
     assert s["c"].device_status() == 0
+
+
+def test_attn_of_both_query_types_on_one_cache(fp):
+    """The scratch of a call depends on the queries' type too."""
+    a = attn_case(fp, [(700, 200)], 8, 2, 64, "bf16", "bf16", seed=1)
+    b = attn_case(fp, [(700, 200)], 8, 2, 64, "bf16", "e4m3", seed=1)
+    for s in (a, b, a):
+        check_attn(dict(s, c=a["c"]), *a["c"].attn(s["q"], i32(s["table"]), i32(s["lens"]), q_scale=s["q_scale"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq,h_q", [(2, 320), (40, 256), (70, 22)])
+def test_attn_of_wide_groups(fp, dtype, lq, h_q):
+    """More query heads a kv head than a tile's half has rows, as many, and a count that leaves rows over."""
+    s = attn_case(fp, [(300, lq), (90, 1)], h_q, 2, 32, dtype, "bf16", seed=8)
+    check_attn(s, *run_attn(s))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_of_many_requests(fp, dtype):
+    """More requests than a block has threads, those of one row among those of many."""
+    rng = np.random.default_rng(3)
+    reqs = [(int(n), int(min(n, m))) for n, m in zip(rng.integers(0, 200, 900), rng.choice([1, 1, 1, 5, 40], 900))]
+    s = attn_case(fp, reqs, 4, 2, 16, dtype, "bf16", seed=2)
+    check_attn(s, *run_attn(s))
+    s = attn_case(fp, [(int(n), 1) for n in rng.integers(0, 60, 4096)], 2, 1, 16, dtype, "e4m3", seed=2)
+    check_attn(s, *run_attn(s))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq", [1, 60])
+def test_attn_queries_that_are_not_finite(fp, dtype, lq):
+    """Their rows, and no others."""
+    s = attn_case(fp, [(400, lq), (90, 1)], 8, 2, 32, dtype, "bf16", seed=5)
+    s["q"][0, 3, 17] = math.nan
+    s["q"][lq, 1, 100] = math.inf
+    s["q"][lq - 1, 6, 5] = -math.inf
+    got, lse = run_attn(s)
+    got, lse = host(got), host(lse)
+    bad = np.zeros(got.shape[:2], bool)
+    bad[0, 3] = True
+    assert np.isnan(got[0, 3]).all() and np.isnan(lse[3, 0])
+    bad[lq, 1] = bad[lq - 1, 6] = True                  # what an infinity makes of its row is not defined
+    ref, ref_lse, tol, lse_tol = reference(dict(s, qv=np.nan_to_num(s["qv"])))
+    assert np.all(np.abs(got - ref)[~bad] <= tol[~bad])
+    assert np.all(np.abs(lse - ref_lse)[~bad.T] <= lse_tol[~bad.T])
+
+
+def test_attn_after_a_wait_that_ran_out(fp):
+    """A status of FP_ERR_TIMEOUT stays, and requests of many rows are left alone, until it is reset."""
+    import torch
+    s = attn_case(fp, [(500, 100), (90, 1)], 8, 2, 64, "bf16", "bf16", seed=5)
+    out = torch.full((101, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    s["c"]._ws[0] = 6
+    run_attn(s, out=out)
+    assert s["c"].device_status() == 6
+    assert bool((out[:100] == 3).all())
+    s["c"].reset_status()
+    check_attn(s, *run_attn(s, out=out))
+    assert s["c"].device_status() == 0
+
+
+def test_attn_two_streams_of_many_rows(fp):
+    """Calls on two streams, and threads on one, have scratch of their own or one after the other."""
+    import threading
+    import torch
+    a = attn_case(fp, [(3000, 100), (90, 1), (700, 300)], 16, 4, 64, "e4m3", "bf16", seed=1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], [], [], []]
+
+    def work(i):
+        with torch.cuda.stream(streams[i % 2]):
+            for _ in range(4):
+                got[i].append(run_attn(a))
+            streams[i % 2].synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs in got:
+        for o in outs:
+            check_attn(a, *o)
+
+
+# -- together ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_prompts_then_decode_steps(fp, dtype):
+    """Tables, append with rotation, attention: two prompts, whose attention the prefill kernels compute too, a
+    chunk that starts inside a block, then decode steps replayed from a graph."""
+    import torch
+    h_q, h, page, pool = 8, 2, 32, 64
+    prompts, steps = [300, 77], 5
+    f = FREQ["long"]
+    rope = fp.Rope(f)
+    fp8 = dtype == "e4m3"
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    kc, vc = (torch.zeros((pool, page, h, 128), dtype=kind, device="cuda") for _ in range(2))
+    ks, vs, qs = (f32(np.full(n, 0.02)) if fp8 else None for n in (h, h, h_q))
+    cache = fp.KVCache(kc, vc, ks, vs)
+    table = i32(np.zeros((2, 20)))
+    free = i32(np.random.default_rng(0).permutation(pool))
+    lens, head = i32([0, 0]), i32([0])
+    done = [0, 0]
+    seed = [100]
+    qs_all, keep = [], []
+
+    def rows(n):
+        seed[0] += 1
+        return bf16(seed[0], n, h_q + 2 * h, 128).split([h_q, h, h], 1)
+
+    def step(new, graph=None):
+        nonlocal lens, head
+        n = sum(new)
+        t = fp.PageTables(table, page, pool, n)
+        t.step(lens, i32(new), free, head)
+        q, k, v = rows(n)
+        q = cache.append(k, v, t.slots, rope, t.positions, q=q, q_scale=qs)
+        out, lse = cache.attn(q, table, t.seqlens_k, cu_seqlens_q=t.cu_seqlens_q, max_q=max(new), q_scale=qs)
+        lens, head = t.seqlens_k.clone(), t.free_head.clone()
+        for r in range(2):
+            done[r] += new[r]
+        assert t.device_status() == 0 and cache.device_status() == 0
+        return q, out, lse
+
+    def check(new, q, out, lse):
+        s = dict(c=cache, q=q, q_scale=qs, table=table.cpu().numpy(), lens=list(done), lq=new, cu=np.concatenate([[0], np.cumsum(new)]))
+        scale = 0.02 if fp8 else 1.0
+        s["qv"], s["kv"], s["vv"] = host(q) * scale, host(kc) * scale, host(vc) * scale
+        check_attn(s, out, lse)
+
+    q, out, lse = step(prompts)
+    check(prompts, q, out, lse)
+    layer = fp.Layer(q, kc, vc, table, [0, 300, 377], prompts, [0, 0], h_q, h, dtype=dtype, q_scale=qs, k_scale=ks, v_scale=vs)
+    prefill, prefill_lse = layer.dense_attn()
+    # both within a rounding of bf16 (2^-8) of outputs up to 4; the prefill's e4m3 weights add 2^-4 of theirs
+    bound = 4 * 2.0 ** -7 + (2.0 ** -4 * 2 if fp8 else 0)
+    assert float((prefill.float() - out.float()).abs().max()) <= bound
+    assert float((prefill_lse - lse).abs().max()) <= 1e-2
+    new = [100, 3]
+    check(new, *step(new))                                 # from positions 300 and 77
+    # decode: one graph, its inputs overwritten in place
+    t = fp.PageTables(table, page, pool, 2)
+    t.seqlens_k.copy_(lens)
+    t.free_head.copy_(head)
+    qkv, ones = bf16(7, 2, h_q + 2 * h, 128), i32([1, 1])
+    qd, kd, vd = qkv.split([h_q, h, h], 1)
+
+    def decode():
+        t.step(t.seqlens_k, ones, free, t.free_head)
+        q = cache.append(kd, vd, t.slots, rope, t.positions, q=qd, q_scale=qs)
+        return (q, *cache.attn(q, table, t.seqlens_k, q_scale=qs))
+    saved = t.seqlens_k.clone(), t.free_head.clone(), table.clone()
+    decode()                                               # first calls are not captured
+    t.seqlens_k.copy_(saved[0])
+    t.free_head.copy_(saved[1])
+    table.copy_(saved[2])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q, out, lse = decode()
+    for i in range(steps):
+        qkv.copy_(bf16(50 + i, 2, h_q + 2 * h, 128))
+        g.replay()
+        done[0], done[1] = done[0] + 1, done[1] + 1
+        assert t.seqlens_k.tolist() == done
+        check([1, 1], q, out, lse)
+        if not fp8:
+            close(host(q), oc.rope(host(qd), np.array(done) - 1, f), reach_of(host(qd), 64, False, 1.0))
+
+
+def test_rotated_keys_into_the_4_bit_cache(fp):
+    """A rope of its own beside a cache of another form, and keys turned back from it."""
+    import torch
+    c = fp.QCache.empty(8, 64, 2, 32)
+    c.data.zero_()
+    rope = fp.Rope(FREQ["short"])
+    k, v, pos, slots = bf16(1, 90, 2, 128), bf16(2, 90, 2, 128), i32(np.arange(90) + 1000), i32(np.random.default_rng(0).permutation(512)[:90])
+    c.write(rope.apply(k, pos), v, slots)
+    back, _ = c.read(slots)
+    again = rope.apply(back, pos, inverse=True)
+    # a group of 32 rotated dims spans up to 2 * 1.5 * 4.5; a code is within 1 / 30 of that, two dims meet, bf16 rounds thrice
+    span = 2 * 1.5 * 4.5
+    assert float((again.float() - k.float()).abs().max()) <= 2 * span / 30 + 3 * 2.0 ** -8 * span
