@@ -607,12 +607,12 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     };
                     if (c0 + j < edge) {
 #pragma unroll 1
-                        for (int p = 0; p < 8; p += 4) {
-                            uint4 w[4];
+                        for (int p = 0; p < 8; p += 2) {
+                            uint4 w[2];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[i] = ld_shared_v4(from + (p + i) * 2048);
+                            for (int i = 0; i < 2; ++i) w[i] = ld_shared_v4(from + (p + i) * 2048);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < 2; ++i) {
                                 uint32_t h[8];
                                 convert(w[i], h);
                                 put(row0 + 16 * (p + i), h);
