@@ -26,6 +26,18 @@
 // wait is bounded.  The roles' code is kept short: together it has to fit the instruction
 // caches (with the conversion written out eight times a step took 5100 clocks and not 3700).
 //
+// Bounds: the chain from S through a half's softmax back to the next S, with the issuer's
+// instructions between: 1.5 us a block of 128 keys (2900 clocks; the products alone take 2048,
+// which 8 softmax warps beside them, reading and writing TMEM, do not slow).  A chunk of 2048
+// behind 32785 tokens (32/4 heads, bf16, 1.13e12 FLOP) 684 us, 1660 TFLOP/s, 0.86 of the measured
+// burst rate, 0.96 of the sustained one; e4m3 703 us with e4m3 queries, 758 with bf16 ones (two
+// terms of S).  An item's start and end cost some 4 us, a launch 6 before its first block.
+// What it took: the issuer not waiting for tiles itself 810 to 718, results stored by runs of
+// rows 718 to 688.  Measured and left out: an issuer for each half (994 instead of 807: their
+// products mix on one pipe), all lanes of the issuer's warp at its instructions (897), P handed
+// over by halves (848), loops over its 8 products (832 to 1096), P packed by integers
+// instead of conversions (720 instead of 685).
+//
 // What a row does not attend may be anything, and a weight of zero does not keep a NaN out of
 // a product: the loaders clear values behind a request's last token, and take values that are
 // not finite out of the blocks that some of the tile's rows do not attend whole.  The item
