@@ -588,7 +588,8 @@ def test_attn_refusals(fp):
     assert out.shape == (0, 4, 128) and lse.shape == (4, 0)
 
 
-def test_attn_past_4_gb(fp):
+@pytest.mark.parametrize("lq", [2, 200])
+def test_attn_past_4_gb(fp, lq):
     """A request whose last pages lie past 2^32 bytes of the cache."""
     import torch
     page, h, pages = 128, 8, 20000
@@ -598,7 +599,7 @@ def test_attn_past_4_gb(fp):
     ids = [pages - 1, 3, pages - 2]
     for j, p in enumerate(ids):
         k[p], v[p] = bf16(j, page, h, 128), bf16(10 + j, page, h, 128)
-    s = dict(c=c, q=bf16(30, 2, 16, 128), q_scale=None, table=np.array([ids]), lens=[300], lq=[2], cu=np.array([0, 2]))
+    s = dict(c=c, q=bf16(30, lq, 16, 128), q_scale=None, table=np.array([ids]), lens=[300], lq=[lq], cu=np.array([0, lq]))
     small = np.array([[0, 1, 2]])
     s["qv"] = host(s["q"])
     out, lse = run_attn(s)
@@ -833,6 +834,46 @@ def test_attn_after_a_wait_that_ran_out(fp):
     s["c"].reset_status()
     check_attn(s, *run_attn(s, out=out))
     assert s["c"].device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq", [3, 40])
+def test_attn_over_a_long_axis(fp, dtype, lq):
+    """262144 tokens: few rows over all SMs, sums of many parts."""
+    s = attn_case(fp, [(262144, lq)], 4, 1, 64, dtype, "bf16", seed=3, k_scale=0.3)
+    check_attn(s, *run_attn(s))
+
+
+@pytest.mark.parametrize("what", ["append", "columns", "tiles"])
+def test_first_call_of_a_process_is_captured(what):
+    """No call needs one before it outside the graph."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from block_sparse_long_fp_gb300 import fprefill as fp
+k, v = (torch.randn(8, 64, 2, 128, device="cuda").bfloat16() for _ in range(2))
+c, r, q = fp.KVCache(k, v), fp.Rope([1.0, 0.1]), torch.randn(300, 8, 128, device="cuda").bfloat16()
+slots = torch.arange(300, dtype=torch.int32, device="cuda")
+table, lens = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8), torch.tensor([300], dtype=torch.int32, device="cuda")
+cu = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+what = %r
+def call():
+    if what == "append":
+        return c.append(q[:, :2], q[:, 2:4], slots, r, slots, q=q)
+    return c.attn(q[:1] if what == "columns" else q, table, lens, max_q=1 if what == "columns" else 300)[0]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = call()
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(a, call()) and c.device_status() == 0
+""" % what
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_attn_two_streams_of_many_rows(fp):
