@@ -656,14 +656,28 @@ bool whole_items(const PAttn &a) { return (long long)a.max_pages * (a.c.page_siz
 // tokens with 128 columns 13 / 17.
 int most_columns(const PAttn &a) { return whole_items(a) ? 128 : a.k_scale ? 24 : 32; }
 bool with_tiles(const PAttn &a) { return a.g <= kBlock && (long long)a.max_q * a.g > most_columns(a); }
-bool with_columns(const PAttn &a) { return a.cu || !with_tiles(a); }
+// Whether requests of up to 8 columns are left to the columns where others go to tiles: a launch
+// more, and an e4m3 cache's values that are not converted for a row or two, against tiles that hold
+// all requests at once.  us by both / by tiles alone, 64 requests of 4096 to 8192 (64/8 heads), q rows
+// in a part of them and 1 in the others: bf16 q 10 in 50% 288 / 281, 10 in 2% 276 / 278; 32/4 heads
+// 155 / 150 and 164 / 151; but 128 requests to 4096, 64 in 5% 293 / 327, 256 in 1% 286 / 328.  e4m3 q 10
+// in 2% 185 / 289, in 50% 248 / 294, in all 303 / 296.  12 to 32 heads a KV head: bf16 203 / 191 and
+// 181 / 161, e4m3 164 / 156, 177 / 172 and (2% of 16 rows) 157 / 171.
+// A request of more than 8 columns would read its keys once for every 8 of them: drafts of 1 to 5 rows,
+// bf16 588 by such columns, 276 by tiles.
+constexpr int kBeside = 8;
+bool with_columns(const PAttn &a) {
+    if (!with_tiles(a)) return true;
+    if (!a.cu || a.g > kBeside) return false;
+    return a.k_scale ? a.total_q != (long long)a.batch * a.max_q : (long long)a.max_q * a.g > kBlock;
+}
 
 // Columns of a tile.  Where every request has max_q rows, as many as it has, up to 32;
-// where the rows differ, what most of them fill, by the mean that the host knows; beside
-// tiles of rows, what a decoding request fills.
+// where the rows differ, what most of them fill, by the mean that the host knows.
 int tile_columns(const PAttn &a) {
-    const long long cols = with_tiles(a) ? a.g : (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
-    const bool ragged = a.cu && !with_tiles(a) && a.total_q != (long long)a.batch * a.max_q;
+    if (with_tiles(a)) return kBeside;
+    const long long cols = (long long)a.max_q * a.g, all = (long long)a.total_q * a.g;
+    const bool ragged = a.cu && a.total_q != (long long)a.batch * a.max_q;
     if (cols <= 8 || (ragged && all <= 8ll * a.batch)) return 8;
     return cols <= 16 || (ragged && all <= 16ll * a.batch) ? 16 : 32;
 }
@@ -721,7 +735,7 @@ size_t cache_attn_scratch_bytes(const PAttn &args) {
 cudaError_t launch_cache_attn(const PAttn &args, void *scratch, unsigned long long limit_ns, cudaStream_t st) {
     PAttn a = args;
     a.whole = whole_items(a);
-    a.most_columns = with_tiles(a) ? (a.cu ? most_columns(a) : 0) : INT_MAX;
+    a.most_columns = with_tiles(a) ? (with_columns(a) ? kBeside : 0) : INT_MAX;
     if (with_columns(a)) {
         const size_t n = blocks_of(a), cols = tile_columns(a);
         char *p = static_cast<char *>(scratch);

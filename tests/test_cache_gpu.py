@@ -459,6 +459,20 @@ def test_attn(fp, reqs, h_q, h, page, dtype, q_dtype):
     assert bool((again == out).all()) and bool((lse2 == lse).all())
 
 
+@pytest.mark.parametrize("dtype,q_dtype", TYPES)
+@pytest.mark.parametrize("reqs,h_q,h,page", [
+    ([(3000, 9), (1500, 1), (0, 1), (40, 2), (1100, 4), (1700, 1)], 32, 4, 64),       # drafts beside decodes
+    ([(2000 + 300 * i, 5) for i in range(4)], 16, 2, 32),                             # as many each
+    ([(2500, 300), (1200, 1), (1300, 1), (0, 1), (77, 2)], 16, 1, 16),                # a chunk, 16 heads share keys
+    ([(4000, 200), (2600, 8), (1900, 9), (1, 1), (3100, 1)], 3, 3, 128),              # a chunk, none shared
+    ([(1800 + i, 1 + i % 5) for i in range(40)], 9, 1, 64)])
+def test_attn_rows_that_differ(fp, reqs, h_q, h, page, dtype, q_dtype):
+    s = attn_case(fp, reqs, h_q, h, page, dtype, q_dtype, seed=len(reqs) + h_q)
+    check_attn(s, *run_attn(s))
+    check_attn(s, *run_attn(s, max_q=max(s["lq"]) + 7))
+    assert s["c"].device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("lq", [1, 3, 7])
 def test_attn_without_offsets_and_with_wider_bounds(fp, lq, dtype):
