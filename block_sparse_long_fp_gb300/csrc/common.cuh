@@ -62,8 +62,12 @@ struct WsHeader {
 };
 constexpr size_t kWsHeaderBytes = 256;
 
+// The first error stays, but a wait that ran out is recorded over what was found in device
+// data: that leaves results defined, and it does not; and other blocks look for it.
 __device__ __forceinline__ void set_status(int *status, int code) {
-    if (status) atomicCAS(status, 0, code);
+    if (!status) return;
+    if (code == FP_ERR_TIMEOUT) atomicExch(status, code);
+    else atomicCAS(status, 0, code);
 }
 
 // Fused selection: a score row of ncol entries is cut into 8 segments of

@@ -20,7 +20,8 @@
  *    stream).  Argument errors are returned synchronously, before anything
  *    is enqueued.  Errors found by a kernel (a page-table entry out of range,
  *    a bounded wait that timed out) are recorded in a status word inside the
- *    workspace (first error wins) and read back with fp_device_status().
+ *    workspace (the first error, or a wait that ran out) and read back with
+ *    fp_device_status().
  *  - Every workspace is an opaque device buffer of at least the size its
  *    *_workspace_size() query returns.  Its first 256 bytes are a header
  *    holding the status word: zero them once (fp_reset_status) before first
@@ -623,7 +624,9 @@ fp_status fp_cache_attn(const fp_cache *c, const fp_qcache_query *q, void *out, 
 fp_status fp_reset_status(void *ws, void *stream);
 
 /* Wait for `stream`, then read the status word of `ws` into *device_status
- * (an fp_status value; FP_OK when no kernel recorded an error). */
+ * (an fp_status value; FP_OK when no kernel recorded an error): the first error
+ * since the last reset, or FP_ERR_TIMEOUT if there was one, whatever came before
+ * it -- results are not defined then. */
 fp_status fp_device_status(const void *ws, void *stream, int *device_status);
 
 /* Time limit of every bounded wait inside the attention kernel, in
@@ -634,8 +637,8 @@ void fp_set_wait_limit_ns(unsigned long long ns);
 /* Failure-path check of the bounded waits, with no GPU fault: launches one
  * thread that waits, through the kernels' own bounded wait, on an mbarrier
  * that nothing arrives on, for limit_ns nanoseconds (1 .. 1e10).  The wait
- * runs out, FP_ERR_TIMEOUT lands in the status word of ws (first error
- * wins), and the context stays usable: reset the status and carry on.
+ * runs out, FP_ERR_TIMEOUT lands in the status word of ws (over any other
+ * error there), and the context stays usable: reset the status and carry on.
  * Returns FP_ERR_INVALID for a null ws or a limit out of range. */
 fp_status fp_check_wait_timeout(void *ws, unsigned long long limit_ns, void *stream);
 

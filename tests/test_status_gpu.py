@@ -1,0 +1,43 @@
+"""The status word, and kernels that stop: waits that run out or are called off."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fp():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from block_sparse_long_fp_gb300 import build, fprefill
+    build.build()
+    return fprefill
+
+
+def i32(x):
+    import torch
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def pages(fp, tokens, h=2, page=128, seed=0):
+    """A bf16 cache of one request whose pages lie in order, and its table."""
+    import torch
+    n = -(-tokens // page)
+    torch.manual_seed(seed)
+    k, v = (torch.randn((n, page, h, 128), device="cuda").to(torch.bfloat16) for _ in range(2))
+    return fp.KVCache(k, v), torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+
+
+def test_a_wait_that_runs_out_is_recorded_over_bad_device_data(fp):
+    """Bad device data leaves results defined, a wait that ran out does not: the status tells of the wait."""
+    cache, _ = pages(fp, 300)
+    k = cache.k_cache.view(-1, 2, 128)[:3].clone()
+    cache.append(k, k, i32([0, -7, 2]))
+    assert cache.device_status() == fp.FP_ERR_DEVICE_BOUNDS
+    fp._check(fp.lib().fp_check_wait_timeout(cache._ws_ptr, 1_000_000, fp._stream_handle()), "fp_check_wait_timeout")
+    assert cache.device_status() == fp.FP_ERR_TIMEOUT
+    cache.append(k, k, i32([0, -7, 2]))                # and it stays
+    assert cache.device_status() == fp.FP_ERR_TIMEOUT
+    cache.reset_status()
+    assert cache.device_status() == 0
