@@ -94,7 +94,7 @@ struct Control {
     unsigned long long bars[kBars];
     uint32_t tmem, abort;
     long long at;
-    int r, pad;
+    int r, dead;
     union {
         Item item[2];
         long long sums[kTilesWarps];             // of the scan, before the roles part
@@ -230,6 +230,10 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         tmem_relinquish();
     }
     after_previous();
+    // If a wait of this launch or an earlier one on this status ran out: no work, so that a broken launch
+    // ends in one limit and not in one for each block.  Read by one thread: another block may record it
+    // at any time, and all lanes of a warp have to go the same way.
+    const int status = tid == 0 && a.status ? *reinterpret_cast<volatile int *>(a.status) : FP_OK;
 
     // -- this block's range of units ------------------------------------------------
     const int each = (a.batch + kTilesThreads - 1) / kTilesThreads;
@@ -239,7 +243,10 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     long long low = scan_all(n, &total, ctl.sums);
     const long long want = total / (kBlock * kMinBlocks) + 1;
     const int blocks = total == 0 ? 0 : (int)(want < gridDim.x ? want : gridDim.x);
-    if (tid == 0) sc.open[blockIdx.x].parts = 0;
+    if (tid == 0) {
+        sc.open[blockIdx.x].parts = 0;
+        ctl.dead = status == FP_ERR_TIMEOUT;
+    }
     if ((int)blockIdx.x >= blocks) {
         __syncthreads();
         if (warp == 0) tmem_dealloc(ctl.tmem, 512);
@@ -264,9 +271,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     const Waits wait = {smem_u32(&ctl.abort), a.status, limit_ns};
-    // a wait of this launch or an earlier one on this status ran out: no work, so that a broken
-    // launch ends in one limit and not in one for each block
-    const bool dead = a.status && *reinterpret_cast<volatile int *>(a.status) == FP_ERR_TIMEOUT;
+    const bool dead = ctl.dead;
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
