@@ -443,12 +443,12 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 }
                 if (!good) break;
             }
-            if (ld_shared_volatile(wait.abort)) {        // products issued and copies armed are done before the block leaves
-                tc_commit(bar(DR));
-                mbar_wait_drain(bar(DR), 0);
-                if (items0) mbar_wait_drain(bar(QF), (items0 - 1) & 1);
-                if (items1) mbar_wait_drain(bar(QF + 1), (items1 - 1) & 1);
-            }
+            // Products issued and copies armed are done before the block leaves: whether or not this thread
+            // has seen a stop, as others may give up after it went through its last item.
+            tc_commit(bar(DR));
+            mbar_wait_drain(bar(DR), 0);
+            if (items0) mbar_wait_drain(bar(QF), (items0 - 1) & 1);
+            if (items1) mbar_wait_drain(bar(QF + 1), (items1 - 1) & 1);
         } else if (warp == 2 && lane == 0) {
             // ================= what the issuer need not wait for itself =================
             // A wait costs it 150 to 250 clocks even where nothing is waited for.  So this thread
@@ -552,8 +552,8 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ME + b));
             }
-            // after an abort, the copies armed last land before the block leaves
-            if (lane == 0 && ld_shared_volatile(wait.abort)) {
+            // the copies armed last land before the block leaves, here too whatever this thread has seen
+            if (lane == 0) {
                 constexpr uint32_t kRing = kFp8 ? kRingK : kRingBf16;
                 const uint32_t m = kFp8 ? nk : nt, g = kFp8 ? nx : edges;
                 for (uint32_t i = m < kRing ? 0 : m - kRing; i < m; ++i) mbar_wait_drain(bar(TF + i % kRing), (i / kRing) & 1);
