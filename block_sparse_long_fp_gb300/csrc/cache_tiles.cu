@@ -95,6 +95,7 @@ struct Control {
     uint32_t tmem, abort;
     long long at;
     int r, dead;
+    uint32_t left[4];                            // queries copied of each half, tiles of the ring, staged (or unclean) ones
     union {
         Item item[2];
         long long sums[kTilesWarps];             // of the scan, before the roles part
@@ -443,12 +444,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 }
                 if (!good) break;
             }
-            // Products issued and copies armed are done before the block leaves: whether or not this thread
-            // has seen a stop, as others may give up after it went through its last item.
-            tc_commit(bar(DR));
-            mbar_wait_drain(bar(DR), 0);
-            if (items0) mbar_wait_drain(bar(QF), (items0 - 1) & 1);
-            if (items1) mbar_wait_drain(bar(QF + 1), (items1 - 1) & 1);
+            ctl.left[0] = items0, ctl.left[1] = items1;
         } else if (warp == 2 && lane == 0) {
             // ================= what the issuer need not wait for itself =================
             // A wait costs it 150 to 250 clocks even where nothing is waited for.  So this thread
@@ -552,14 +548,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ME + b));
             }
-            // the copies armed last land before the block leaves, here too whatever this thread has seen
-            if (lane == 0) {
-                constexpr uint32_t kRing = kFp8 ? kRingK : kRingBf16;
-                const uint32_t m = kFp8 ? nk : nt, g = kFp8 ? nx : edges;
-                for (uint32_t i = m < kRing ? 0 : m - kRing; i < m; ++i) mbar_wait_drain(bar(TF + i % kRing), (i / kRing) & 1);
-                constexpr uint32_t kStaged = kFp8 ? 2 : kUnclean;
-                for (uint32_t i = g < kStaged ? 0 : g - kStaged; i < g; ++i) mbar_wait_drain(bar(GF + i % kStaged), (i / kStaged) & 1);
-            }
+            if (lane == 0) ctl.left[2] = kFp8 ? nk : nt, ctl.left[3] = kFp8 ? nx : edges;
         }
     } else if (warp < 8) {
         setmaxnreg_dec<kRegsLoad>();
@@ -860,6 +849,21 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         }
     }
     tc_fence_before();
+    __syncthreads();
+    // Nothing is on its way when the block leaves: products and their arrivals on barriers, and after a stop the
+    // copies armed last.  Here all roles have left, so that none gives up after another has looked.
+    if (tid == 0 && !dead) {
+        tc_commit(bar(DR));
+        mbar_wait_drain(bar(DR), 0);
+        if (ld_shared_volatile(wait.abort)) {
+            for (int t = 0; t < 2; ++t)
+                if (ctl.left[t]) mbar_wait_drain(bar(QF + t), (ctl.left[t] - 1) & 1);
+            constexpr uint32_t kRing = kFp8 ? kRingK : kRingBf16, kStaged = kFp8 ? 2 : kUnclean;
+            const uint32_t m = ctl.left[2], g = ctl.left[3];
+            for (uint32_t i = m < kRing ? 0 : m - kRing; i < m; ++i) mbar_wait_drain(bar(TF + i % kRing), (i / kRing) & 1);
+            for (uint32_t i = g < kStaged ? 0 : g - kStaged; i < g; ++i) mbar_wait_drain(bar(GF + i % kStaged), (i / kStaged) & 1);
+        }
+    }
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();

@@ -49,8 +49,8 @@ class Block:
     """One thread block over a list of items: dicts of id, count (blocks of keys), edge (first block that not
     every row attends whole) and two (whether the second half has rows)."""
 
-    def __init__(self, items, fp8, rng, always_drain, cleaning):
-        self.items, self.fp8, self.rng, self.always, self.cleaning = items, fp8, rng, always_drain, 2 if fp8 else cleaning
+    def __init__(self, items, fp8, rng, together, cleaning):
+        self.items, self.fp8, self.rng, self.together, self.cleaning = items, fp8, rng, together, 2 if fp8 else cleaning
         b = {}
         for name, n, count in (("QF", 2, 1), ("TF", RING, 1), ("TE", RING, 1), ("VF", 2, LOADERS), ("VE", 2, 1), ("SF", 2, 1),
                                ("OF", 2, 1), ("MF", 2, 1), ("ME", 2, 3 + 2 * SOFTMAX + LOADERS), ("GF", 3, 1),
@@ -62,6 +62,7 @@ class Block:
         self.products, self.copies, self.slots = [], [], [None, None]
         self.q, self.k, self.v, self.staged = [None, None], {}, {}, {}
         self.o, self.read, self.written, self.cleaned = [None, None], {}, [], {}
+        self.queries, self.armed = [0, 0], {"TF": [], "GF": []}      # copies of each half; (barrier, phase) of the others
 
     def wait(self, name, i, n):
         return Wait(self.bars[name, i], n)
@@ -87,17 +88,22 @@ class Block:
         return (n % RING_K, n // RING_K) if self.fp8 else (2 * n % RING, 2 * n // RING)
 
     def issuer(self):
-        it, phases, items = 0, [0, 0], [0, 0]
-        yield from self._issue(phases, items, it)
-        if self.always or self.stopped:
-            self.commit("DR", 0)
-            yield Wait(self.bars["DR", 0], 0, drain=True)
-            for t in range(2):
-                if items[t]:
-                    yield Wait(self.bars["QF", t], items[t] - 1, drain=True)
+        yield from self._issue()
+        if not self.together and self.stopped:
+            yield from self.drain_products()
+            yield from self.drain_queries()
 
-    def _issue(self, phases, items, it):
-        k = 0
+    def drain_products(self):
+        self.commit("DR", 0)
+        yield Wait(self.bars["DR", 0], 0, drain=True)
+
+    def drain_queries(self):
+        for t in range(2):
+            if self.queries[t]:
+                yield Wait(self.bars["QF", t], self.queries[t] - 1, drain=True)
+
+    def _issue(self):
+        phases, items, it, k = [0, 0], self.queries, 0, 0
         while True:
             item = yield from self.item(k)
             if item is None:
@@ -181,12 +187,22 @@ class Block:
             k += 1
 
     def copier(self):
-        armed = {"TF": [], "GF": []}                 # (barrier, phase) of the copies armed
-        yield from self._copy(armed)
-        if self.always or self.stopped:
-            for name, last in (("TF", RING_K if self.fp8 else RING), ("GF", self.cleaning)):
-                for i, n in armed[name][-last:]:
-                    yield Wait(self.bars[name, i], n, drain=True)
+        yield from self._copy(self.armed)
+        if not self.together and self.stopped:
+            yield from self.drain_copier()
+
+    def drain_copier(self):
+        for name, last in (("TF", RING_K if self.fp8 else RING), ("GF", self.cleaning)):
+            for i, n in self.armed[name][-last:]:
+                yield Wait(self.bars[name, i], n, drain=True)
+
+    def leave(self):
+        """One thread, when all roles have left."""
+        if self.together:
+            yield from self.drain_products()
+        if self.together and self.stopped:
+            yield from self.drain_queries()
+            yield from self.drain_copier()
 
     def _copy(self, armed):
         nt = nk = nx = edges = k = 0
@@ -312,7 +328,8 @@ class Block:
     def run(self, stop=lambda block, live, steps: False):
         rng = self.rng
         roles = [self.walk(), self.issuer(), self.follower(), self.copier()]
-        roles += [self.loader() for _ in range(LOADERS)] + [self.softmax(t) for t in range(2) for _ in range(SOFTMAX)]
+        last = len(roles) + LOADERS + 2 * SOFTMAX                    # leaves behind the others
+        roles += [self.loader() for _ in range(LOADERS)] + [self.softmax(t) for t in range(2) for _ in range(SOFTMAX)] + [self.leave()]
         waits, live, idle, steps = [None] * len(roles), set(range(len(roles))), 0, 0
         speed = [rng.random() ** 2 + 0.02 for _ in roles]
         slow_copies, slow_products = rng.random() ** 3 + 0.02, rng.random() + 0.05
@@ -327,7 +344,7 @@ class Block:
                 self.copies.pop(rng.randrange(min(len(self.copies), 4)))()
                 moved = True
             for i in rng.sample(sorted(live), len(live)):
-                if rng.random() > speed[i]:
+                if rng.random() > speed[i] or (i == last and len(live) > 1):
                     continue
                 w, went = waits[i], None
                 if w is not None:
@@ -348,13 +365,13 @@ class Block:
         return steps
 
 
-def block(seed, fp8, always_drain=True, cleaning=3):
+def block(seed, fp8, together=True, cleaning=3):
     rng = random.Random(2 * seed + fp8)
     items = []
     for i in range(rng.randint(1, 9)):
         n = rng.choice([0, 1, 1, 1, 2, 2, 3, 4, 6])
         items.append(dict(id=i, count=n, edge=max(0, rng.choice([0, 0, n - 1, n - 2, n, n + 3])), two=rng.random() < 0.5))
-    return Block(items, fp8, rng, always_drain, cleaning)
+    return Block(items, fp8, rng, together, cleaning)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -388,7 +405,7 @@ def test_the_model_finds_a_role_that_leaves_before_its_copies_land(fp8):
     """Where a role waits for what it has on its way only if it sees the stop itself, a later stop finds some."""
     with pytest.raises(AssertionError, match="on their way"):
         for seed in range(100):
-            block(seed, fp8, always_drain=False).run(when_a_role_has_left(seed, fp8))
+            block(seed, fp8, together=False).run(when_a_role_has_left(seed, fp8))
 
 
 def test_the_model_finds_three_tiles_in_cleaning_on_two_barriers():
