@@ -61,6 +61,10 @@ static_assert(kRegsControl + kRegsLoad + 2 * kRegsSoftmax <= 4 * 128, "register 
 constexpr int kRows = 2 * kBlock;                // places of a tile's rows
 constexpr int kItemKeys = 512;                   // what an item's start and end cost, in keys (256 to 1024: within 5 %)
 constexpr int kMinBlocks = 4;                    // least blocks of keys worth an SM
+// What waits that may span an item are given beside the limit, for each block of keys (and each 128 rows of
+// zeros) that an item may have: 40 times what one takes.  (A count of blocks that such waits watch, so that their
+// limit starts again with it, cost 3 % of a mixed step in the roles' code.)
+constexpr unsigned long long kBlockNs = 64000;
 constexpr int kTile = kBlock * kHeadDim * 2, kHalf = kTile / 2;      // bytes; a half: 64 dims
 constexpr int kSmemQ = 0, kSmemK = 2 * kTile;
 constexpr int kRingBf16 = 5;                     // K0 V0 K1 V1 ...
@@ -154,9 +158,14 @@ __device__ __forceinline__ long long units_of(const PAttn &a, const Tiles &t) {
 struct Waits {
     uint32_t abort;
     int *status;
-    unsigned long long limit;
+    unsigned long long limit, item_limit;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
         return mbar_wait(bar, parity & 1u, abort, status, limit);
+    }
+    // A wait that may span an item: the walk's for the item before the last, the loaders' for an item's first edge
+    // block, an idle half's for the next item.
+    __device__ __forceinline__ bool through_item(uint32_t bar, uint32_t parity) const {
+        return mbar_wait(bar, parity & 1u, abort, status, item_limit);
     }
 };
 
@@ -203,7 +212,7 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t tile, int row, int piece) 
 template <bool kFp8>
 __global__ void __launch_bounds__(kTilesThreads, 1)
 tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-             const __grid_constant__ CUtensorMap map_v, unsigned long long limit_ns) {
+             const __grid_constant__ CUtensorMap map_v, unsigned long long limit_ns, unsigned long long item_limit_ns) {
     extern __shared__ unsigned char smem_raw[];
     // 1024-byte aligned, as the swizzle wants; addresses by offsets in the shared window
     unsigned char *smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -271,7 +280,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    const Waits wait = {smem_u32(&ctl.abort), a.status, limit_ns};
+    const Waits wait = {smem_u32(&ctl.abort), a.status, limit_ns, item_limit_ns};
     const bool dead = ctl.dead;
 
     if (warp < 4) {
@@ -300,7 +309,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                 const int b = k & 1;
                 Item &it = ctl.item[b];
                 if (k >= 2) {
-                    const bool got = wait(bar(ME + b), ((k >> 1) & 1) ^ 1);
+                    const bool got = wait.through_item(bar(ME + b), ((k >> 1) & 1) ^ 1);
                     if (!__all_sync(~0u, got)) break;
                 }
                 bool live = false;
@@ -557,7 +566,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         uint32_t nv = 0, edges = 0;                      // blocks, edge blocks
         for (int k = 0; !dead; ++k) {
             const int b = k & 1;
-            const bool got = wait(bar(MF + b), k >> 1);
+            const bool got = wait.through_item(bar(MF + b), k >> 1);
             if (!__all_sync(~0u, got)) break;
             Item &item = ctl.item[b];
             if (!item.live) break;
@@ -566,7 +575,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
             for (int j = kFp8 ? 0 : max(0, edge - c0); j < count && good; ++j) {
                 if (!kFp8) {
                     const uint32_t tile = base + kSmemK + ((2 * (nv + j) + 1) % kRingBf16) * kTile;
-                    if (!(good = __all_sync(~0u, wait(bar(GF + edges % kUnclean), edges / kUnclean)))) break;
+                    if (!(good = __all_sync(~0u, wait.through_item(bar(GF + edges % kUnclean), edges / kUnclean)))) break;
                     const int key = (c0 + j) * kBlock + lt;         // a thread a row; can pass 2^31 behind the last token
                     if ((uint32_t)key >= (uint32_t)len) {
 #pragma unroll 4
@@ -672,7 +681,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
         uint32_t phase = 0, items = 0;
         for (int k = 0; !dead; ++k) {
             const int b = k & 1;
-            const bool got = wait(bar(MF + b), k >> 1);
+            const bool got = wait.through_item(bar(MF + b), k >> 1);
             if (!__all_sync(~0u, got)) break;
             const Item &item = ctl.item[b];
             if (!item.live) break;
@@ -1108,8 +1117,9 @@ cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long l
         !make_map(&map_v, c.v, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, !fp8))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> told[2];
+    const unsigned long long item_limit_ns = limit_ns + kBlockNs * ((unsigned long long)(a.max_len + rows / c.h_kv) / kBlock + 1);
     if ((e = launch_large(told[fp8], fp8 ? tiles_kernel<true> : tiles_kernel<false>, (unsigned)n, kTilesThreads, kSmem, st, a, sc,
-                          map_q, map_k, map_v, limit_ns)) != cudaSuccess)
+                          map_q, map_k, map_v, limit_ns, item_limit_ns)) != cudaSuccess)
         return e;
     return launch_chained(tiles_join_kernel, (unsigned)n * 4, kJoinWarps * 32, 0, st, a, sc, (int)n);
 }

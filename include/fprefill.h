@@ -631,7 +631,10 @@ fp_status fp_device_status(const void *ws, void *stream, int *device_status);
 
 /* Time limit of every bounded wait inside the attention kernel, in
  * nanoseconds (default 200 ms; 0 restores the default).  A wait that runs out
- * records FP_ERR_TIMEOUT and the kernel returns instead of hanging. */
+ * records FP_ERR_TIMEOUT and the kernel returns instead of hanging.
+ * fp_cache_attn gives waits that may span a request's keys 64 us more for
+ * every 128 tokens that its table holds and every 128 rows, some 40 times what
+ * they take: no length of a cache is too long for the limit. */
 void fp_set_wait_limit_ns(unsigned long long ns);
 
 /* Failure-path check of the bounded waits, with no GPU fault: launches one

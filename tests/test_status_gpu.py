@@ -41,3 +41,34 @@ def test_a_wait_that_runs_out_is_recorded_over_bad_device_data(fp):
     assert cache.device_status() == fp.FP_ERR_TIMEOUT
     cache.reset_status()
     assert cache.device_status() == 0
+
+
+LONG = 262144                                          # tokens: 3 ms for a tile's way through them
+
+
+def long_chunk(fp, dtype):
+    """A chunk of 1024 rows, 32 heads of one KV head, whose thread blocks hold whole tiles: (cache, call)."""
+    import torch
+    cache, table = pages(fp, LONG, 1)
+    if dtype == "e4m3":
+        ones = torch.ones(1, device="cuda")
+        cache = fp.KVCache(cache.k_cache.to(torch.float8_e4m3fn), cache.v_cache.to(torch.float8_e4m3fn), ones, ones)
+    q = torch.randn((1024, 32, 128), device="cuda").to(torch.bfloat16)
+    lens = i32([LONG])
+    return cache, lambda **kw: cache.attn(q, table, lens, max_q=1024, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_waits_that_span_an_item_have_its_time(fp, dtype):
+    """The limit is a tenth of the time that the walk and the loaders wait for a tile's last keys."""
+    import torch
+    cache, call = long_chunk(fp, dtype)
+    out, lse = call()
+    assert cache.device_status() == 0
+    try:
+        fp.lib().fp_set_wait_limit_ns(300_000)
+        again, lse_again = call()
+        assert cache.device_status() == 0
+    finally:
+        fp.lib().fp_set_wait_limit_ns(0)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
