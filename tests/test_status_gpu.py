@@ -72,3 +72,29 @@ def test_waits_that_span_an_item_have_its_time(fp, dtype):
     finally:
         fp.lib().fp_set_wait_limit_ns(0)
     assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_attn_called_off_while_it_runs(fp, dtype):
+    """FP_ERR_TIMEOUT recorded while tiles are on their way (as by another block, or a call on another stream):
+    they stop, later calls leave their rows alone, and after a reset the same call gives the same bits."""
+    import time
+    import torch
+    cache, call = long_chunk(fp, dtype)
+    want, want_lse = call()
+    outs = [torch.full_like(want, 3.0) for _ in range(6)]
+    stopped = torch.tensor([fp.FP_ERR_TIMEOUT], dtype=torch.int32).pin_memory()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for out in outs:                                   # some 3 ms each
+        call(out=out)
+    time.sleep(0.001)
+    with torch.cuda.stream(side):
+        cache._ws[:1].copy_(stopped, non_blocking=True)
+    torch.cuda.synchronize()
+    assert cache.device_status() == fp.FP_ERR_TIMEOUT
+    assert bool((outs[-1] == 3).all())
+    cache.reset_status()
+    out, lse = call(out=outs[0])
+    assert cache.device_status() == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
