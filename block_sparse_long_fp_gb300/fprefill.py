@@ -408,6 +408,14 @@ class _OnDevice:
         self._stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+    def _settle(self):
+        """Waits for what the constructor enqueued, the status' zeros too: any stream may use the object from
+        here on.  One built in a graph's capture is ready where the graph has run."""
+        torch = self._torch
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+
     def _entry(self, name: str, arguments: int):
         """An entry point that takes its structures as bytes, and integers."""
         f = self._lib._FuncPtr((name, self._lib))
@@ -518,6 +526,7 @@ class _Cache(_OnDevice):
         self._scratch, self._scratch_bytes, self._lock = {}, {}, threading.Lock()
         self._f = tuple(self._entry(*f) for f in others) + (self._entry(attn, 9),)
         self._attn_name, self._scratch_query = attn, getattr(self._lib, attn + "_scratch_bytes")
+        self._settle()
 
     def attn(self, q, block_table, seqlens_k, cu_seqlens_q=None, max_q=None, out=None, lse=None, want_lse=True,
              q_scale=None, softmax_scale: float = 0.0):
@@ -741,8 +750,7 @@ class Rope(_OnDevice):
         _check(lib().fp_rope_turns(freq.ctypes.data, freq.size, turns.ctypes.data), "fp_rope_turns")
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
         super().__init__(self.turns.device)
-        if not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(self.device).synchronize()         # any stream may use it from here on
+        self._settle()
         self.rot, self.layout, self.scale = 2 * freq.size, layout, float(scale)
         self._t = FpRopeTable(self.rot, FP_ROPE_INTERLEAVED if layout == "interleaved" else FP_ROPE_HALF, self.scale,
                               _ptr(self.turns))

@@ -98,3 +98,29 @@ def test_attn_called_off_while_it_runs(fp, dtype):
     out, lse = call(out=outs[0])
     assert cache.device_status() == 0
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_a_cache_is_ready_for_any_stream(fp):
+    """The status is zero when the constructor returns, whatever its stream has still to do and whatever its
+    memory held: tiles look at it before they work."""
+    import torch
+    old, table = pages(fp, 300)
+    q, lens = torch.randn((300, 8, 128), device="cuda").to(torch.bfloat16), i32([300])
+    want, _ = old.attn(q, table, lens, max_q=300)
+    built, used = torch.cuda.Stream(priority=-1), torch.cuda.Stream()
+    with torch.cuda.stream(used):                      # memory of this stream's for the call below: none is allocated there
+        out = torch.full_like(q, 3.0)
+        lse = fp.KVCache(old.k_cache, old.v_cache).attn(q, table, lens, max_q=300)[1]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(built):
+        held = [torch.full((64,), fp.FP_ERR_TIMEOUT, dtype=torch.int32, device="cuda") for _ in range(64)]
+        places = {t.data_ptr() for t in held}
+        del held
+        torch.cuda._sleep(40_000_000)                  # some 20 ms
+        cache = fp.KVCache(old.k_cache, old.v_cache)
+    with torch.cuda.stream(used):
+        cache.attn(q, table, lens, max_q=300, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert cache._ws_ptr in places                     # or the test tells nothing
+    assert cache.device_status() == 0
+    assert torch.equal(out, want)
