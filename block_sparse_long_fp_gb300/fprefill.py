@@ -518,12 +518,21 @@ class PageTables(_OnDevice):
         return self
 
 
+class _Scratch:
+    """Memory of one stream, and the lock of those who enqueue calls that use it."""
+
+    def __init__(self):
+        self.memory, self.lock = None, threading.Lock()
+
+
 class _Cache(_OnDevice):
     """What QCache and KVCache share: attention over their pages, and its scratch."""
 
+    _scratch = {}              # _Scratch by device and stream, for all objects: a model's layers run one behind the other
+
     def _entries(self, attn: str, *others):
         """Sets up the entry points: `others`, pairs of names and argument counts, and last the attention's."""
-        self._scratch, self._scratch_bytes, self._lock = {}, {}, threading.Lock()
+        self._scratch_bytes = {}
         self._f = tuple(self._entry(*f) for f in others) + (self._entry(attn, 9),)
         self._attn_name, self._scratch_query = attn, getattr(self._lib, attn + "_scratch_bytes")
         self._settle()
@@ -594,18 +603,20 @@ class _Cache(_OnDevice):
         return out, lse
 
     def _attn(self, args, n: int):
-        """fp_qcache_attn with n bytes of scratch of the current stream: calls on
-        two streams share none, and a captured call has its own, out of the
-        graph's memory.  The library enqueues two kernels that hand partial
-        results over in it: of threads on one stream, one enqueues at a time."""
+        """The attention with n bytes of scratch of the current stream, which holds nothing between calls: calls on
+        two streams share none, and a captured call has its own, out of the graph's memory.  The library enqueues
+        several kernels that hand partial results over in it: of threads on one stream, one enqueues at a time."""
         torch, stream = self._torch, self._stream(self._index)
+        mine = self._scratch.get((self._index, stream))
+        if mine is None:
+            mine = self._scratch.setdefault((self._index, stream), _Scratch())       # one of two threads' stays
         capturing = torch.cuda.is_current_stream_capturing()
-        with self._lock:
-            scratch = None if capturing else self._scratch.get(stream)
+        with mine.lock:
+            scratch = None if capturing else mine.memory
             if scratch is None or scratch.numel() < n:
                 scratch = torch.empty(max(16, n), dtype=torch.uint8, device=self.device)
                 if not capturing:
-                    self._scratch[stream] = scratch
+                    mine.memory = scratch
             s = self._f[-1](*args, scratch.data_ptr(), n, self._ws_ptr, FP_WS_HEADER_BYTES, stream)
         if s != FP_OK:
             raise FprefillError(s, self._attn_name)
