@@ -8,7 +8,7 @@
 // A bf16 cache takes bf16 operands: queries as they are (e4m3 ones exactly), weights rounded
 // to bf16 (2^-8 of each).  Of an e4m3 cache K's codes are multiplied as they are (m16n8k32),
 // with e4m3 queries, or with bf16 ones under a power of two as two e4m3 terms of 4 bits each,
-// which hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it;
+// which hold 8 bits exactly down to 2^-9 of the row's largest, and the rest to 2^-17 of it;
 // V's become fp16, exactly, in registers, weights fp16 (2^-11).
 // For V^T two keys of a dim have to meet in a register: the 16-bit transpose brings two dims
 // of two keys, which a byte permutation sorts, and a tile's rows stand for even, then odd dims.

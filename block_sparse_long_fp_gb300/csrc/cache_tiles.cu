@@ -882,7 +882,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
 
 // Queries of another type than the tiles take, for the copies to fetch: e4m3 ones as bf16
 // rows; bf16 ones of an e4m3 cache under a power of two, as two e4m3 terms of 4 bits each,
-// which hold 8 bits exactly down to 2^-10 of the row's largest, and the rest to 2^-18 of it:
+// which hold 8 bits exactly down to 2^-9 of the row's largest, and the rest to 2^-17 of it:
 // [2][total_q, h_q, 128] codes, the exponents behind them.  16 lanes a row.
 template <bool kTerms>
 __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed char *exponent) {

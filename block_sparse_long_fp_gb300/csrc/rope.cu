@@ -5,7 +5,8 @@
 // held as the 64-bit fixed-point fraction of a turn that one position makes, so that p times
 // it, modulo 2^64, is the angle modulo whole turns exactly: its upper 32 bits are
 // the angle to 2^-32 of a turn at any position, where an fp32 product would be off by a
-// radian at position 2^24, and the way there is integer arithmetic of full rate.
+// radian at position 2^24, and the way there is integer arithmetic of full rate.  As an fp32,
+// for sincospif, it is rounded by up to 2^-26 of a turn: 2^-23 radians, beside bf16's 2^-8.
 //
 // A warp takes a token (or a share of its heads, where there are few tokens): it computes
 // the token's 64 cosines and sines once, and its four groups of 8 lanes then take a head's

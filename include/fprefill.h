@@ -530,8 +530,9 @@ fp_status fp_qcache_attn(const fp_qcache *c, const fp_qcache_query *q, void *out
  *   a' = scale * (a cos t - b sin t),   b' = scale * (b cos t + a sin t),
  * t negated for the inverse: with scale 1 the inverse undoes the rotation, and with any
  * scale it is the gradient.  Dims from `rot` on stay as they are (and are not scaled).
- * Angles are exact to 2^-32 of a turn at any int32 position (negative ones too); products
- * and sums are fp32, rounded once to the output's type.
+ * Angles are kept to 2^-32 of a turn at any int32 position (negative ones too), and rounded to
+ * fp32, by 2^-26 of a turn at most, where their cosine and sine are taken; products and sums are
+ * fp32, rounded once to the output's type.
  * ------------------------------------------------------------------------- */
 typedef enum { FP_ROPE_HALF = 0, FP_ROPE_INTERLEAVED = 1 } fp_rope_layout;
 typedef struct {
@@ -610,10 +611,11 @@ fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, cons
  *   or an infinity makes that dim of the row one that is not finite.  Other rows and dims are
  *   what they would be without, and keys and values that a row does not attend may be
  *   anything.  Finite values are below 2^100 in magnitude.
- *   Logits and sums are fp32.  Weights enter the sum of values in bf16 for a bf16 cache (half
- *   a step, 2^-9 of each), in fp16 for an e4m3 one (2^-12; nothing below 2^-34 of the row's
- *   largest), where bf16 queries enter as two e4m3 terms under a power of two of the row
- *   (exact down to 2^-10 of the row's largest element, the rest to 2^-18 of it).
+ *   Logits and sums are fp32.  Weights enter the sum of values rounded: to bf16 for a bf16 cache
+ *   (2^-8 of each at most), to fp16 for an e4m3 one (2^-11 of each, or 2^-34 of the row's
+ *   largest where that is more).  Weights below 2^-136 of the row's largest may count as none.
+ *   bf16 queries of an e4m3 cache enter as two e4m3 terms under a power of two of the row: exact
+ *   down to 2^-9 of the row's largest element, the rest to 2^-17 of it.
  *   Requests of many rows have bounded waits in their kernel, as the prefill's: one that runs
  *   out records FP_ERR_TIMEOUT, and until fp_reset_status such requests are left unwritten. */
 size_t fp_cache_attn_scratch_bytes(const fp_cache *c, const fp_qcache_query *q);
