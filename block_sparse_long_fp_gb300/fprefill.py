@@ -708,7 +708,7 @@ class QCache(_Cache):
 
 
 def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-                     original: int = 4096, low: float = 1.0, high: float = 4.0) -> np.ndarray:
+                     original: int = 4096, low: float | None = None, high: float | None = None) -> np.ndarray:
     """Radians a position for the rot / 2 pairs of a rotary embedding, float64:
     base^(-2 i / rot), scaled for contexts `factor` times the trained ones by
 
@@ -717,9 +717,13 @@ def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling: str | None 
     "base"     the base raised to base * factor^(rot / (rot - 2)), so that the
                longest wave is `factor` times as long and the shortest stays;
     "smooth"   by the waves that a pair makes in `original` positions: 1 / factor
-               up to `low` waves, 1 from `high` on, and linear in them between;
+               up to `low` waves (1), 1 from `high` (4) on, and linear in them between;
     "ramp"     the same, but linear in the pair's index between those indices
-               (rounded outwards) where a pair makes `high` and `low` waves."""
+               (rounded outwards) where a pair makes `high` (32) and `low` (1)
+               waves.  Models with a ramp mostly scale cos and sin as well:
+               Rope(..., scale=0.1 * math.log(factor) + 1)."""
+    low = 1.0 if low is None else low
+    high = (32.0 if scaling == "ramp" else 4.0) if high is None else high
     if rot < 2 or rot > 128 or rot % 2 or not base > 1 or not factor > 0:
         raise FprefillError(FP_ERR_INVALID, f"rope_frequencies: rot {rot}, base {base}, factor {factor}")
     i = np.arange(rot // 2, dtype=np.float64)
