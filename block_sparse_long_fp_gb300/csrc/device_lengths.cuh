@@ -32,6 +32,13 @@ struct Scratch {
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// The base that a largest logit of m sets: kTop below it; m itself from 2^27 on, where fp32's neighbours are 16
+// and more apart and m - kTop would round to m - 16, which makes a weight that fp16 does not hold.
+__device__ __forceinline__ float base_below(float m) {
+    const float b = m - kTop;
+    return m - b <= kTop + kSlack ? b : m;
+}
+
 // Transpose of the 8 x 8 fp16 matrix whose row lane / 4 holds the lane's pair.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;

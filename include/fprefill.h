@@ -610,7 +610,7 @@ fp_status fp_cache_append(const fp_cache *c, const fp_rope_table *rope_opt, cons
  *   infinity in either makes of the row is not defined.  In a value that a row attends, a NaN
  *   or an infinity makes that dim of the row one that is not finite.  Other rows and dims are
  *   what they would be without, and keys and values that a row does not attend may be
- *   anything.  Finite values are below 2^100 in magnitude.
+ *   anything.  Finite values, and logits, are below 2^100 in magnitude.
  *   Logits and sums are fp32.  Weights enter the sum of values rounded: to bf16 for a bf16 cache
  *   (2^-8 of each at most), to fp16 for an e4m3 one (2^-11 of each, or 2^-34 of the row's
  *   largest where that is more).  Weights below 2^-136 of the row's largest may count as none.
