@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<NT>()) attn_kernel(QAt
                         float m = fmaxf(l0, l1);
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-                        const float old = base[t][c], b = fmaxf(old, m - kTop);
+                        const float old = base[t][c], b = fmaxf(old, base_below(m));
                         const float keep = b == -INFINITY ? 1.f : exp2f(old - b);
                         base[t][c] = b;
                         sum[t][c] *= keep;
