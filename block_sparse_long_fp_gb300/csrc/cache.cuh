@@ -1,6 +1,8 @@
 // The bf16 / e4m3 paged K/V cache and rotary positions as their kernels see them.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <atomic>
 
 #include "qcache.cuh"
@@ -91,5 +93,41 @@ cudaError_t launch_large(std::atomic<unsigned long long> &told, void (*kernel)(P
     }
     return e;
 }
+
+// Two e4m3 codes in the low half of a register, as fp16.
+__device__ __forceinline__ uint32_t halves_of(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+// Two numbers as fp16 (of an e4m3 cache) or bf16.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if (kFp8) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two e4m3 codes as bf16, which holds them.
+__device__ __forceinline__ uint32_t bf16_of(uint32_t codes) {
+    const uint32_t h = halves_of(codes);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack16<false>(v.x, v.y);
+}
+// Two elements of a bf16 query for an e4m3 cache: times `up`, a power of two that brings the row's largest
+// into [2^7, 2^8), each as two e4m3 codes of 4 bits, which hold 8 bits exactly down to 2^-9 of the largest, and
+// the rest to 2^-17 of it.
+struct TwoTerms {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ TwoTerms two_terms(float a, float b, float up) {
+    // an infinity becomes a NaN: e4m3 would take it for its largest value
+    const float x = fmaf(a, up, a * 0.f), y = fmaf(b, up, b * 0.f);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3), back = halves_of(hi);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+    return {hi, __nv_cvt_float2_to_fp8x2(make_float2(x - v.x, y - v.y), __NV_SATFINITE, __NV_E4M3)};
+}
+__device__ __forceinline__ int term_exp(float top) { return fp16_scale_exp(__float_as_uint(top)) - 7; }
 
 }  // namespace fp

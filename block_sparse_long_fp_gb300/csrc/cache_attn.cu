@@ -96,20 +96,6 @@ __device__ __forceinline__ void load4_transposed(uint32_t r[4], uint32_t at) {
                  : "r"(at)
                  : "memory");
 }
-// The e4m3 codes in the low and in the high half of a register, as fp16.
-__device__ __forceinline__ uint32_t halves_of(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
-}
-template <bool kFp8>
-__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
-    if (kFp8) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 // The top bit of each half that is an infinity or a NaN.
 template <bool kFp8>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -175,13 +161,7 @@ __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Que
     } else if (e4m3) {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            uint32_t b[2] = {halves_of(raw.w[s].x), halves_of(raw.w[s].y)};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&b[e]));
-                b[e] = pack_pair<false>(v.x, v.y);
-            }
-            out.f[s] = make_uint2(b[0], b[1]);
+            out.f[s] = make_uint2(bf16_of(raw.w[s].x), bf16_of(raw.w[s].y));
         }
     } else if (!kFp8) {
 #pragma unroll
@@ -197,7 +177,7 @@ __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Que
             }
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
+        const int ex = term_exp(top);
         const float up = pow2f(ex);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
@@ -205,14 +185,9 @@ __device__ __forceinline__ void make_queries(const RawQuery &raw, bool e4m3, Que
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t w = e ? raw.w[s].y : raw.w[s].x;
-                // an infinity becomes a NaN: e4m3 would take it for its largest value
-                const float u = __uint_as_float(w << 16), v0 = __uint_as_float(w & 0xffff0000u);
-                const float x = fmaf(u, up, u * 0.f), y = fmaf(v0, up, v0 * 0.f);
-                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3), back = halves_of(hi);
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x - v.x, y - v.y), __NV_SATFINITE, __NV_E4M3);
-                term[0] |= hi << 16 * e;
-                term[1] |= lo << 16 * e;
+                const TwoTerms z = two_terms(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u), up);
+                term[0] |= z.hi << 16 * e;
+                term[1] |= z.lo << 16 * e;
             }
             (s & 1 ? out.f[s / 2].y : out.f[s / 2].x) = term[0];
             (s & 1 ? out.f[4 + s / 2].y : out.f[4 + s / 2].x) = term[1];
@@ -500,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kFp8, NT>()) columns_k
                 for (int e = 0; e < 4; ++e) y[t][e] = fast_exp2(y[t][e]);
                 sum[t][0] += y[t][0] + y[t][2];
                 sum[t][1] += y[t][1] + y[t][3];
-                p[t][0] = transpose8(pack_pair<kFp8>(y[t][0], y[t][1]));
-                p[t][1] = transpose8(pack_pair<kFp8>(y[t][2], y[t][3]));
+                p[t][0] = transpose8(pack16<kFp8>(y[t][0], y[t][1]));
+                p[t][1] = transpose8(pack16<kFp8>(y[t][2], y[t][3]));
             }
 
             // values: tile m's registers hold keys 2 j4, 2 j4 + 1 (and 8 further) of its rows r8, r8 + 8

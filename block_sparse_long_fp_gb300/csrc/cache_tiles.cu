@@ -190,19 +190,6 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t b, u
                  : "memory");
 }
 
-template <bool kFp8>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-    if (kFp8) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t codes_to_f16(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
-}
 // 16-byte piece `piece` (8 dims) of row `row` of a 128 x 128 tile: two halves of 128-byte rows,
 // pieces XORed by the row (the 128-byte swizzle of TMA and of the products' descriptors).
 __device__ __forceinline__ uint32_t piece_at(uint32_t tile, int row, int piece) {
@@ -612,7 +599,7 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
                     const auto convert = [&](uint4 w, uint32_t (&h)[8]) {
                         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = codes_to_f16(u[e >> 1] >> (16 * (e & 1)));
+                        for (int e = 0; e < 8; ++e) h[e] = halves_of(u[e >> 1] >> (16 * (e & 1)));
                     };
                     // lanes 4 .. 7 of a row write their two pieces the other way round: all banks, once
                     const auto put = [&](int row, const uint32_t (&h)[8]) {
@@ -889,9 +876,8 @@ tiles_kernel(const PAttn a, const Scratch sc, const __grid_constant__ CUtensorMa
 }
 
 // Queries of another type than the tiles take, for the copies to fetch: e4m3 ones as bf16
-// rows; bf16 ones of an e4m3 cache under a power of two, as two e4m3 terms of 4 bits each,
-// which hold 8 bits exactly down to 2^-9 of the row's largest, and the rest to 2^-17 of it:
-// [2][total_q, h_q, 128] codes, the exponents behind them.  16 lanes a row.
+// rows; bf16 ones of an e4m3 cache as two e4m3 terms, [2][total_q, h_q, 128] codes, the
+// exponents of their powers of two behind them.  16 lanes a row.
 template <bool kTerms>
 __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed char *exponent) {
     after_previous();
@@ -901,12 +887,7 @@ __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed 
     const long long tok = row / a.h_q, at = tok * a.q_stride_tok + (row - tok * a.h_q) * a.q_stride_head + 8 * c;
     if (!kTerms) {
         const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const unsigned char *>(a.q) + at);
-        uint32_t h[4] = {codes_to_f16(w.x), codes_to_f16(w.x >> 16), codes_to_f16(w.y), codes_to_f16(w.y >> 16)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-            h[e] = pack16<false>(f.x, f.y);
-        }
+        const uint32_t h[4] = {bf16_of(w.x), bf16_of(w.x >> 16), bf16_of(w.y), bf16_of(w.y >> 16)};
         *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(to) + row * kHeadDim + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
         return;
     }
@@ -922,17 +903,14 @@ __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed 
     const unsigned lanes = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, d));
-    const int ex = fp16_scale_exp(__float_as_uint(top)) - 7;         // the largest into [2^7, 2^8)
+    const int ex = term_exp(top);
     const float up = pow2f(ex);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        // an infinity becomes a NaN: e4m3 would take it for its largest value
-        const float u = fmaf(x[2 * e], up, x[2 * e] * 0.f), y = fmaf(x[2 * e + 1], up, x[2 * e + 1] * 0.f);
-        hi[e] = __nv_cvt_float2_to_fp8x2(make_float2(u, y), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t back = codes_to_f16(hi[e]);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-        lo[e] = __nv_cvt_float2_to_fp8x2(make_float2(u - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
+        const TwoTerms z = two_terms(x[2 * e], x[2 * e + 1], up);
+        hi[e] = z.hi;
+        lo[e] = z.lo;
     }
     unsigned char *p = static_cast<unsigned char *>(to) + row * kHeadDim + 8 * c;
     *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
