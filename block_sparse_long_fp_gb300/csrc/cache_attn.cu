@@ -23,8 +23,8 @@
 // join at the item's end; an item that a range's end cuts is joined by a second kernel.
 //
 // Bounds.  One octet of columns: memory.  64 requests up to 16384 (32/4 heads, bf16, 1.07 GB)
-// 165 us, 6.5 TB/s, 0.96 of the measured copy rate; e4m3 0.82 of it (262144 tokens of 8 heads, 537
-// MB, 97 us), where taking V's codes apart fills 44 % of the issue slots.  More octets: latency,
+// 165 us, 6.5 TB/s, 0.96 of the measured copy rate; e4m3 0.76 to 0.87 of it, by the box (262144
+// tokens of 8 heads, 537 MB, 91 to 104 us), where taking V's codes apart fills 44 % of the issue slots.  More octets: latency,
 // of 8 warps an SM (255 registers): 32 requests up to 8192 with 1 to 8 tokens of 4 heads (up to 4
 // octets, 530 MB) 100 us, 0.78.
 #include <limits.h>

@@ -29,9 +29,9 @@
 // Bounds: the chain from S through a half's softmax back to the next S, with the issuer's
 // instructions between: 1.5 us a block of 128 keys (2900 clocks; the products alone take 2048,
 // which 8 softmax warps beside them, reading and writing TMEM, do not slow).  A chunk of 2048
-// behind 32785 tokens (32/4 heads, bf16, 1.13e12 FLOP) 684 us, 1660 TFLOP/s, 0.86 of the measured
-// burst rate, 0.96 of the sustained one; e4m3 703 us with e4m3 queries, 758 with bf16 ones (two
-// terms of S).  An item's start and end cost some 4 us, a launch 6 before its first block.
+// behind 32785 tokens (32/4 heads, bf16, 1.13e12 FLOP) 684 to 697 us in a graph, 1630 to 1660 TFLOP/s,
+// 0.84 to 0.86 of the measured burst rate (called from Python in a loop of seconds, under the power
+// cap, up to 743: 0.79); e4m3 691 us with e4m3 queries, 751 with bf16 ones (two terms of S).  An item's start and end cost some 4 us, a launch 6 before its first block.
 // What it took: the issuer not waiting for tiles itself 810 to 718, results stored by runs of
 // rows 718 to 688.  Measured and left out: an issuer for each half (994 instead of 807: their
 // products mix on one pipe), all lanes of the issuer's warp at its instructions (897), P handed

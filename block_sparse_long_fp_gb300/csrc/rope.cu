@@ -19,8 +19,9 @@
 // Bounds: memory.  65536 tokens of 32 heads (1.07 GB) 175 us, 6.1 TB/s, 0.90 of the measured
 // copy rate; their projections into bf16 pages (32/4 heads, 1.34 GB) 218 us, 0.91.  At 80
 // registers 24 warps an SM hold 2 rows a group in flight; with 3 rows ahead (94 registers, 16
-// warps) it took 203, with 64 registers (spills) 243, with 1 row ahead 195.  e4m3 outputs are
-// bound by instructions: 175 us (floor 119), 254 us into pages of 8 heads (179).
+// warps) it took 203, with 64 registers (spills) 243, with 1 row ahead 195.  e4m3
+// outputs: 176 us (floor 119), 254 us into pages of 8 heads (179); two thirds of the issue slots and
+// half of DRAM's rate, so instructions and the loads' latency between them, at 22 warps an SM.
 // Below some thousand tokens a launch and one chain: 2.7 us.
 #include "cache.cuh"
 

@@ -775,7 +775,9 @@ class Rope(_OnDevice):
     def apply(self, x, positions, out=None, out_scale=None, inverse: bool = False):
         """x (bf16 [rows, heads, 128]) rotated by positions (int32 [rows]); with
         inverse, back (the gradient's rotation too).  Into out -- bf16, x itself
-        if wanted, or with out_scale [heads] e4m3 -- or into new rows."""
+        if wanted, or with out_scale [heads] e4m3 -- or into new rows.  As with
+        every call here, the result has no history: a backward pass calls it
+        with inverse itself."""
         x_at = self._heads(x, "x", None)
         rows, heads = x.shape[0], x.shape[1]
         fp8 = out_scale is not None
@@ -797,7 +799,8 @@ class KVCache(_Cache):
     fp_cache_append and fp_cache_attn on it.
 
     k_cache, v_cache: [num_pages, page_size, h_kv, 128], bf16, or e4m3 (uint8
-    codes or torch.float8_e4m3fn) with k_scale and v_scale (fp32 [h_kv]).
+    codes or torch.float8_e4m3fn) with k_scale and v_scale (fp32 [h_kv]).  Layer's
+    value caches by columns (v_layout 1) are not read here.
     """
 
     def __init__(self, k_cache, v_cache, k_scale=None, v_scale=None):

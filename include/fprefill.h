@@ -517,8 +517,9 @@ fp_status fp_qcache_attn(const fp_qcache *c, const fp_qcache_query *q, void *out
 
 /* ===========================================================================
  * The bf16 / e4m3 paged cache at any position: rotary positions, and keys and values
- * appended to the pages that the prefill entry points read.  Lengths, positions, slots and
- * tables are DEVICE arrays, as for the 4-bit cache above.
+ * appended to the pages that the prefill entry points read, with values stored by tokens
+ * (FP_V_TOKEN_MAJOR: a value cache stored by columns is the prefill's alone).  Lengths,
+ * positions, slots and tables are DEVICE arrays, as for the 4-bit cache above.
  * ========================================================================= */
 
 /* ---------------------------------------------------------------------------
