@@ -160,12 +160,12 @@ struct Waits {
     int *status;
     unsigned long long limit, item_limit;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-        return mbar_wait(bar, parity & 1u, abort, status, limit);
+        return mbar_wait<true>(bar, parity & 1u, abort, status, limit);
     }
     // A wait that may span an item: the walk's for the item before the last, the loaders' for an item's first edge
     // block, an idle half's for the next item.
     __device__ __forceinline__ bool through_item(uint32_t bar, uint32_t parity) const {
-        return mbar_wait(bar, parity & 1u, abort, status, item_limit);
+        return mbar_wait<true>(bar, parity & 1u, abort, status, item_limit);
     }
 };
 

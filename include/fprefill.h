@@ -20,8 +20,8 @@
  *    stream).  Argument errors are returned synchronously, before anything
  *    is enqueued.  Errors found by a kernel (a page-table entry out of range,
  *    a bounded wait that timed out) are recorded in a status word inside the
- *    workspace (the first error, or a wait that ran out) and read back with
- *    fp_device_status().
+ *    workspace (the first error stays, but for a wait that ran out in
+ *    fp_cache_attn) and read back with fp_device_status().
  *  - Every workspace is an opaque device buffer of at least the size its
  *    *_workspace_size() query returns.  Its first 256 bytes are a header
  *    holding the status word: zero them once (fp_reset_status) before first
@@ -628,8 +628,8 @@ fp_status fp_reset_status(void *ws, void *stream);
 
 /* Wait for `stream`, then read the status word of `ws` into *device_status
  * (an fp_status value; FP_OK when no kernel recorded an error): the first error
- * since the last reset, or FP_ERR_TIMEOUT if there was one, whatever came before
- * it -- results are not defined then. */
+ * since the last reset, or FP_ERR_TIMEOUT over it where fp_cache_attn recorded
+ * one -- its results are not defined then. */
 fp_status fp_device_status(const void *ws, void *stream, int *device_status);
 
 /* Time limit of every bounded wait inside the attention kernel, in
