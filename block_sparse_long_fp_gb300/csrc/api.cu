@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "launch.cuh"
 
@@ -461,7 +462,9 @@ void fp_set_wait_limit_ns(unsigned long long ns) { g_wait_ns = ns ? ns : 2000000
 
 fp_status fp_check_wait_timeout(void *ws, unsigned long long limit_ns, void *stream) {
     if (!ws || limit_ns == 0 || limit_ns > 10000000000ull) return FP_ERR_INVALID;
-    return launch_wait_timeout(status_ptr(ws), limit_ns, (cudaStream_t)stream) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (launch_wait_timeout(status_ptr(ws), limit_ns, st) != cudaSuccess) return FP_ERR_CUDA;
+    return launch_cache_wait_timeout(status_ptr(ws), limit_ns, st) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
 }
 
 }  // extern "C"

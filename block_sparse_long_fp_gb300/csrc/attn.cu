@@ -1335,7 +1335,7 @@ __global__ void wait_timeout_kernel(int *status, unsigned long long limit_ns) {
         abort_flag = 0;
         mbar_init(smem_u32(&bar), 1);
         fence_barrier_init();
-        mbar_wait<true>(smem_u32(&bar), 0, &abort_flag, status, limit_ns);
+        mbar_wait(smem_u32(&bar), 0, &abort_flag, status, limit_ns);
     }
 }
 cudaError_t launch_wait_timeout(int *status, unsigned long long limit_ns, cudaStream_t st) {

@@ -69,6 +69,8 @@ cudaError_t launch_cache_attn(const PAttn &a, void *scratch, unsigned long long 
 // cache_tiles.cu: the requests of more columns, by tiles
 size_t cache_tiles_scratch_bytes(const PAttn &a);
 cudaError_t launch_cache_tiles(const PAttn &a, void *scratch, unsigned long long limit_ns, cudaStream_t st);
+// a wait of the tiles on a barrier that nothing arrives on (fp_check_wait_timeout)
+cudaError_t launch_cache_wait_timeout(int *status, unsigned long long limit_ns, cudaStream_t st);
 // the limit of bounded waits (fp_set_wait_limit_ns)
 unsigned long long wait_limit_ns();
 

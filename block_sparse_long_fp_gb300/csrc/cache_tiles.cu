@@ -154,18 +154,36 @@ __device__ __forceinline__ long long units_of(const PAttn &a, const Tiles &t) {
     return u < (1ll << 50) ? u : 1ll << 50;      // past any lengths that fit together
 }
 
-// What a wait needs besides its barrier.
+// What a wait needs besides its barrier.  One that runs out is recorded over what was found in device data: that
+// leaves results defined, and it does not; and other blocks and later launches look for it.
 struct Waits {
     uint32_t abort;
     int *status;
     unsigned long long limit, item_limit;
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-        return mbar_wait<true>(bar, parity & 1u, abort, status, limit);
+    __device__ __forceinline__ bool bounded(uint32_t bar, uint32_t parity, unsigned long long ns) const {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long since = global_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 63u) == 0) {
+                if (ld_shared_volatile(abort)) return false;
+                if (status && *reinterpret_cast<volatile int *>(status) == FP_ERR_TIMEOUT) {
+                    st_shared_volatile(abort, 1);        // another block gave up
+                    return false;
+                }
+                if (global_ns() - since > ns) {
+                    if (status) atomicExch(status, FP_ERR_TIMEOUT);
+                    st_shared_volatile(abort, 1);
+                    return false;
+                }
+            }
+        }
     }
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const { return bounded(bar, parity & 1u, limit); }
     // A wait that may span an item: the walk's for the item before the last, the loaders' for an item's first edge
     // block, an idle half's for the next item.
     __device__ __forceinline__ bool through_item(uint32_t bar, uint32_t parity) const {
-        return mbar_wait<true>(bar, parity & 1u, abort, status, item_limit);
+        return bounded(bar, parity & 1u, item_limit);
     }
 };
 
@@ -918,6 +936,15 @@ __global__ void __launch_bounds__(256) queries_kernel(PAttn a, void *to, signed 
     if (c == 0) exponent[row] = (signed char)ex;
 }
 
+__global__ void wait_timeout_kernel(int *status, unsigned long long limit_ns) {
+    __shared__ __align__(8) unsigned long long nothing;
+    __shared__ uint32_t abort;
+    abort = 0;
+    mbar_init(smem_u32(&nothing), 1);
+    fence_barrier_init();
+    Waits{smem_u32(&abort), status, limit_ns, limit_ns}(smem_u32(&nothing), 0);
+}
+
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1063,6 +1090,11 @@ size_t cache_tiles_scratch_bytes(const PAttn &a) {
     const size_t n = tiles_blocks(a);
     return align256(n * sizeof(Open)) + align256(n * 2 * kRows * sizeof(float2)) + n * 2 * kRows * kHeadDim * sizeof(float) +
            converted_bytes(a);
+}
+
+cudaError_t launch_cache_wait_timeout(int *status, unsigned long long limit_ns, cudaStream_t st) {
+    wait_timeout_kernel<<<1, 1, 0, st>>>(status, limit_ns);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long long limit_ns, cudaStream_t st) {

@@ -62,21 +62,8 @@ struct WsHeader {
 };
 constexpr size_t kWsHeaderBytes = 256;
 
-// The first error stays ...
 __device__ __forceinline__ void set_status(int *status, int code) {
     if (status) atomicCAS(status, 0, code);
-}
-// ... or with kOver a wait that ran out is recorded over what was found in device data: that leaves
-// results defined, and it does not; and other blocks look for it.  (In the prefill's kernels, whose
-// first error stays, as their callers know it, this line alone cost 0.8 to 1.6 % of a bf16 layer at
-// 128K: code elsewhere in them moves.)
-template <bool kOver>
-__device__ __forceinline__ void set_timeout(int *status) {
-    if (kOver) {
-        if (status) atomicExch(status, FP_ERR_TIMEOUT);
-    } else {
-        set_status(status, FP_ERR_TIMEOUT);
-    }
 }
 
 // Fused selection: a score row of ncol entries is cut into 8 segments of

@@ -44,8 +44,7 @@ __device__ __forceinline__ uint64_t global_ns() {
 
 // Wait for the phase of `bar` with parity `parity` to complete.  Gives up when
 // another thread of the CTA raised `abort_flag`, or after `limit_ns` of
-// waiting, in which case it records FP_ERR_TIMEOUT (kOver: over another error) and raises the flag.
-template <bool kOver = false>
+// waiting, in which case it records FP_ERR_TIMEOUT and raises the flag.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           int *status, uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -59,7 +58,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
                 return false;
             }
             if (global_ns() - t0 > limit_ns) {
-                set_timeout<kOver>(status);
+                set_status(status, FP_ERR_TIMEOUT);
                 *abort_flag = 1;
                 return false;
             }
@@ -86,7 +85,6 @@ __device__ __forceinline__ void st_shared_volatile(uint32_t a, int v) {
     asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 // The same wait with the abort flag given by its shared-window address.
-template <bool kOver = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_flag, int *status,
                                           uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -100,7 +98,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
                 return false;
             }
             if (global_ns() - t0 > limit_ns) {
-                set_timeout<kOver>(status);
+                set_status(status, FP_ERR_TIMEOUT);
                 st_shared_volatile(abort_flag, 1);
                 return false;
             }

@@ -641,9 +641,10 @@ fp_status fp_device_status(const void *ws, void *stream, int *device_status);
 void fp_set_wait_limit_ns(unsigned long long ns);
 
 /* Failure-path check of the bounded waits, with no GPU fault: launches one
- * thread that waits, through the kernels' own bounded wait, on an mbarrier
- * that nothing arrives on, for limit_ns nanoseconds (1 .. 1e10).  The wait
- * runs out, FP_ERR_TIMEOUT lands in the status word of ws (over any other
+ * thread that waits, through the prefill's bounded wait, on an mbarrier that
+ * nothing arrives on, for limit_ns nanoseconds (1 .. 1e10), then one that does
+ * so through fp_cache_attn's (and stops at once where the first has recorded
+ * its wait).  FP_ERR_TIMEOUT lands in the status word of ws (over any other
  * error there), and the context stays usable: reset the status and carry on.
  * Returns FP_ERR_INVALID for a null ws or a limit out of range. */
 fp_status fp_check_wait_timeout(void *ws, unsigned long long limit_ns, void *stream);
