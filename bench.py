@@ -15,7 +15,7 @@ pairs) / (ms per layer); ms per layer is reported beside it.
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                   [--dtype bf16|e4m3] [--alpha A] [--no-mean-correction] [--logit-scale C]
 
-The same JSON line carries `variants`: the 128K layer with queries x 16 (the
+The same JSON line carries `variants`, as tables: the 128K layer with queries x 16 (the
 pages' sparse regime; mean correction on and off, and the top-k / top-p /
 union-of-heads ablations), in e4m3, a chunked-prefill step with split-KV,
 the 32K layer (mean correction on and off), the six-request varlen batch, and
@@ -614,10 +614,52 @@ def run_ours(args, rank, world):
         "gen_seconds": round(gen_s, 1),
     }
     if variants:
-        res["variants"] = variants
+        res["variants"] = packed(variants)
     if e2e:
         res["e2e"] = e2e
     return res, case
+
+
+def flat(d, prefix=""):
+    """The leaves of nested dicts, by dotted names."""
+    for k, v in d.items():
+        if isinstance(v, dict):
+            yield from flat(v, f"{prefix}{k}.")
+        else:
+            yield prefix + k, v
+
+
+def table(rows):
+    """Records as what they have in common, one list of column names and a list of values for each."""
+    rows = [dict(flat(r)) for r in rows]
+    columns = list(dict.fromkeys(k for r in rows for k in r))
+    same = {c: rows[0].get(c) for c in columns if len(rows) > 1 and all(r.get(c) == rows[0].get(c) for r in rows)}
+    columns = [c for c in columns if c not in same]
+    return {"all": same, "columns": columns, "rows": [[r.get(c) for c in columns] for r in rows]}
+
+
+def packed(variants):
+    """The variants as tables: with the names of every figure beside it the line has 24 KB, more than what
+    collects it may keep of a line."""
+    layers, ablation, sweeps, rest = [], [], {}, {}
+
+    def walk(name, v):
+        if "points" in v:
+            sweeps[name] = {**{k: x for k, x in v.items() if k != "points"}, "points": table(v["points"])}
+        elif "ms_per_layer" in v:
+            v = dict(v)
+            for rule, r in v.pop("selection_ablation", {}).items():
+                ablation.append({"variant": name, "rule": rule, **r})
+            layers.append({"variant": name, **v})
+        else:
+            for k, x in v.items():
+                if isinstance(x, dict):
+                    walk(f"{name}.{k}", x)
+                elif k != "workload":
+                    rest[f"{name}.{k}"] = x
+    for name, v in variants.items():
+        walk(name, v)
+    return {"layers": table(layers), "selection_ablation": table(ablation), "sweeps": sweeps, **rest}
 
 
 def run_e2e(layer, steps, flop):
