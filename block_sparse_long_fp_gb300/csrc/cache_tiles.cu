@@ -31,7 +31,8 @@
 // which 8 softmax warps beside them, reading and writing TMEM, do not slow).  A chunk of 2048
 // behind 32785 tokens (32/4 heads, bf16, 1.13e12 FLOP) 684 to 697 us in a graph, 1630 to 1660 TFLOP/s,
 // 0.84 to 0.86 of the measured burst rate (called from Python in a loop of seconds, under the power
-// cap, up to 743: 0.79); e4m3 691 us with e4m3 queries, 751 with bf16 ones (two terms of S).  An item's start and end cost some 4 us, a launch 6 before its first block.
+// cap, up to 743: 0.79); e4m3 691 us with e4m3 queries, 751 with bf16 ones (two terms of S).  An
+// item's start and end cost some 4 us, a launch 6 before its first block.
 // What it took: the issuer not waiting for tiles itself 810 to 718, results stored by runs of
 // rows 718 to 688.  Measured and left out: an issuer for each half (994 instead of 807: their
 // products mix on one pipe), all lanes of the issuer's warp at its instructions (897), P handed
@@ -1135,7 +1136,8 @@ cudaError_t launch_cache_tiles(const PAttn &args, void *scratch, unsigned long l
         !make_map(&map_v, c.v, c.h_kv, tokens, kHeadDim, pitch, 1, box, fp8, !fp8))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> told[2];
-    const unsigned long long item_limit_ns = limit_ns + kBlockNs * ((unsigned long long)(a.max_len + rows / c.h_kv) / kBlock + 1);
+    const unsigned long long item_ns = kBlockNs * ((unsigned long long)(a.max_len + rows / c.h_kv) / kBlock + 1);
+    const unsigned long long item_limit_ns = limit_ns + item_ns < limit_ns ? ~0ull : limit_ns + item_ns;
     if ((e = launch_large(told[fp8], fp8 ? tiles_kernel<true> : tiles_kernel<false>, (unsigned)n, kTilesThreads, kSmem, st, a, sc,
                           map_q, map_k, map_v, limit_ns, item_limit_ns)) != cudaSuccess)
         return e;

@@ -74,6 +74,22 @@ def test_waits_that_span_an_item_have_its_time(fp, dtype):
     assert torch.equal(out, again) and torch.equal(lse, lse_again)
 
 
+@pytest.mark.parametrize("limit", [2 ** 64 - 1, 2 ** 64 - 64000 * 2305])
+def test_a_limit_without_end(fp, limit):
+    """What waits that span an item are given beside the limit (64 us for each of this call's 2305 blocks of
+    tokens and rows) does not turn a limit of centuries into none."""
+    import torch
+    cache, call = long_chunk(fp, "bf16")
+    out, lse = call()
+    try:
+        fp.lib().fp_set_wait_limit_ns(limit)
+        again, lse_again = call()
+        assert cache.device_status() == 0
+    finally:
+        fp.lib().fp_set_wait_limit_ns(0)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_attn_called_off_while_it_runs(fp, dtype):
     """FP_ERR_TIMEOUT recorded while tiles are on their way (as by another block, or a call on another stream):
@@ -82,7 +98,7 @@ def test_attn_called_off_while_it_runs(fp, dtype):
     import torch
     cache, call = long_chunk(fp, dtype)
     want, want_lse = call()
-    outs = [torch.full_like(want, 3.0) for _ in range(6)]
+    outs = [torch.full_like(want, 3.0) for _ in range(20)]
     stopped = torch.tensor([fp.FP_ERR_TIMEOUT], dtype=torch.int32).pin_memory()
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
