@@ -639,8 +639,7 @@ def table(rows):
 
 
 def packed(variants):
-    """The variants as tables: with the names of every figure beside it the line has 24 KB, more than what
-    collects it may keep of a line."""
+    """The variants as tables: with the name of every figure beside it the line had 24 KB."""
     layers, ablation, sweeps, rest = [], [], {}, {}
 
     def walk(name, v):
